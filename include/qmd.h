@@ -23,10 +23,10 @@
  *    launch refusals; "Kernel SPI and the selection algorithm", "Why a kernel declines").
  *  - Layouts are batch-major and row-major; K is the reduction length (columns of W), a
  *    multiple of 256; nb = K / 256.
- *  - Launch order: qmd_q8k_pack, qmd_rmsnorm_q8k_pack and qmd_qmatvec are launched as
- *    programmatic dependents of the preceding kernel in the stream.  Before waiting for that
- *    kernel to finish they read only weight buffers (W, W_aux; the norm gain g); everything
- *    else is read and written after it has finished.  Weights therefore must not be written
+ *  - Launch order: qmd_q8k_pack, qmd_rmsnorm_q8k_pack, qmd_qmatvec, the qmd_kv_* calls and
+ *    qmd_lora_add are launched as programmatic dependents of the preceding kernel in the
+ *    stream.  Before waiting for that kernel to finish they read only weight buffers (W, W_aux;
+ *    the norm gain g; an adapter's A, B and scale); everything else is read and written after it has finished.  Weights therefore must not be written
  *    by the kernel launched immediately before them in the same stream unless that kernel
  *    signals completion only by exiting (every kernel not written for programmatic launch
  *    does; so do this library's bind calls).
@@ -48,6 +48,9 @@ extern "C" {
 #define QMD_Q6K_BLOCK_BYTES 210
 #define QMD_Q6K_BODY_BYTES 208
 #define QMD_WORKSPACE_BYTES 4096 /* scheduling workspace of qmd_qmatvec_ws / qmd_qmatvec_x_ws */
+#define QMD_KV_BLOCK 16          /* tokens of one head that share a scale in the key/value cache */
+#define QMD_KV_MAX_SEQS 4096     /* sequences per key/value call */
+#define QMD_LORA_MAX_RANK 128
 
 typedef enum qmd_status {
     QMD_OK = 0,
@@ -60,8 +63,10 @@ typedef enum qmd_status {
     QMD_ERR_LAUNCH = 7,                /* the CUDA runtime refused the launch (see qmd_last_error_detail) */
     QMD_ERR_DEVICE_TIMEOUT = 8,        /* a bounded wait inside a kernel gave up (qmd_get_device_error) */
     QMD_ERR_DEVICE = 9,                /* no usable CUDA device, or it is not an sm_103 part */
-    QMD_ERR_VALUE = 10                 /* a scalar argument is out of its range (e.g. eps < 0 or not finite),
+    QMD_ERR_VALUE = 10,                /* a scalar argument is out of its range (e.g. eps < 0 or not finite),
                                           or buffers that must not overlap do */
+    QMD_ERR_INDEX = 11                 /* a kernel met an index in device memory that is out of its range (a page,
+                                          a length, a row offset, an adapter); see qmd_get_device_error */
 } qmd_status;
 
 /* Weight formats, named by their GGUF type ids. */
@@ -310,6 +315,158 @@ qmd_status qmd_bind_q4k(const void *gguf, int64_t rows, int64_t K);
  */
 qmd_status qmd_bind_q5k(const void *gguf, int64_t rows, int64_t K);
 
+/* ---- the key/value cache of a decode step -------------------------------------------------
+ *
+ * Between the fused q|k|v projection and the o projection a decode step rotates the queries and
+ * keys, keeps the new keys and values, and attends over all that were kept ("Language models on
+ * the device: the cajeta-llm kernels", §2.5 attention over the key/value cache with 1, 4 or 8
+ * query heads to a key/value head, §2.6 rope).  Here the cache holds 8-bit codes.
+ *
+ * qmd_kv_cache: pages of `page_tokens` tokens.  A cached value is code * scale, with one f32
+ * scale for each block of QMD_KV_BLOCK tokens of one head.
+ *   k, v              int8 [pages][kv_heads][page_tokens][head_dim], 16-byte aligned
+ *   k_scale, v_scale  f32  [pages][kv_heads][page_tokens / 16], 4-byte aligned
+ *   head_dim 64, 128 or 256; page_tokens a multiple of 16, at most 65536; kv_heads 1..1024;
+ *   pages 1..2^31 - 1.
+ *
+ * qmd_kv_batch: what one call is about; the same descriptor serves every layer of a step.
+ *   q_start      int32 [seqs + 1], device: sequence s has the call's rows q_start[s] ..
+ *                q_start[s + 1] - 1 (possibly none), not decreasing; or NULL: max_q rows each
+ *   kv_len       int32 [seqs], device: tokens of sequence s in the cache, the call's rows
+ *                counted in: row i of its n rows is at position kv_len - n + i
+ *   page_table   int32 [seqs][table_stride], device: token p is in page page_table[s][p / page_tokens]
+ *   max_q        at least as many rows as any sequence has
+ *   rows         rows of the call's row tensors; rows that no sequence owns are neither read nor written
+ *   seqs 1..QMD_KV_MAX_SEQS, max_q 1..2^20, rows 1..2^24, table_stride 1..2^24.
+ * The arrays are read on the device when the call runs, so a captured call sees their contents at
+ * replay.  What they hold is checked there: a page outside [0, pages), a length above
+ * table_stride * page_tokens or below 0, offsets outside [0, rows], a sequence with more than
+ * max_q rows.  A kernel that meets one sets the device error word (qmd_get_device_error then
+ * returns QMD_ERR_INDEX), leaves out the sequence or page it concerns and touches no memory for it.
+ */
+typedef struct qmd_kv_cache {
+    int8_t *k, *v;
+    float *k_scale, *v_scale;
+    int64_t pages;
+    int kv_heads, page_tokens, head_dim;
+} qmd_kv_cache;
+
+typedef struct qmd_kv_batch {
+    const int32_t *page_table, *kv_len, *q_start;
+    int64_t table_stride, rows;
+    int seqs, max_q;
+} qmd_kv_batch;
+
+/* How rope pairs the first `rot` values of a head: (i, i + rot / 2) or (2 i, 2 i + 1). */
+typedef enum qmd_rope_pairs { QMD_ROPE_HALVES = 0, QMD_ROPE_ADJACENT = 1 } qmd_rope_pairs;
+
+/*
+ * qmd_kv_append -- rotates the new rows' keys (and queries), quantises keys and values and
+ * stores them at their positions in the cache, in one launch.
+ *
+ * Rotation at position p, for a pair (a, b) with cosine c and sine s of table row p, each f32
+ * operation rounded on its own:  a' = a * c - b * s,  b' = b * c + a * s;  values past the
+ * first `rot` are left as they are.
+ * Quantisation, per block of 16 positions and head, each f32 operation rounded on its own:
+ *   d_row  = amax / 127, amax = max |x| over a row's head; 0 where amax < 1e-30
+ *   d      = the largest d_row of the call's rows in the block -- and the block's scale, if the
+ *            block also holds earlier positions of the sequence
+ *   code   = clamp(round_to_nearest_even(x * (1 / d)), -127, 127), 0 where d = 0
+ *   and if d grew past the scale d0 that the block had, its earlier codes become
+ *   clamp(round_to_nearest_even((code * d0) * (1 / d)), -127, 127).
+ * A block's scale thus never shrinks while positions are added, and a position's error is at most
+ * half a step of the final scale for each time that it grew (the first rounding included).  Rows
+ * may overwrite positions that were used before (after a draft was rejected, or in a recycled
+ * page): whatever the block held at or after the first of them is forgotten.  Codes at positions
+ * behind the last row are left as they were.
+ * Non-finite inputs are outside the contract (no fault, the blocks they fall in are unspecified).
+ *
+ *   k, v    f32 rows of kv_heads * head_dim values, row r at k + r * k_stride
+ *   q       f32 rows of q_heads * head_dim values, rotated into q_out; or NULL (then q_out NULL
+ *           and q_heads 0).  q_out may be q itself with the same stride; no other overlap.
+ *   rope    f32 [rope_rows][rot]: rot / 2 cosines, then rot / 2 sines, of position p; or NULL
+ *           (then rot 0): nothing is rotated and q is copied.  A position at or past rope_rows is
+ *           an index error: that row is not stored.
+ *   rot     a multiple of 32, at most head_dim
+ * A sequence shorter than its rows is an index error (none of its rows is stored).
+ * Row pointers 16-byte aligned, strides (in f32 values) multiples of 4 and at least a row long.
+ * A block that is appended to must belong to one sequence: the same block under two sequences of
+ * one call, or of calls that overlap on the GPU, is a race.
+ * Errors: NULL, SHAPE, MISALIGNED, VALUE (pairs, overlap, q without q_out), DEVICE, LAUNCH.
+ */
+qmd_status qmd_kv_append(const qmd_kv_cache *cache, const qmd_kv_batch *batch, const float *k, int64_t k_stride,
+                         const float *v, int64_t v_stride, const float *q, int64_t q_stride, int q_heads,
+                         float *q_out, int64_t q_out_stride, const float *rope, int64_t rope_rows, int rot,
+                         qmd_rope_pairs pairs, void *stream);
+
+/*
+ * qmd_kv_read -- the call's rows as the cache holds them: k_out and v_out receive code * scale
+ * (one rounding) of every row's position, f32 [rows][kv_heads][head_dim] with the given row
+ * strides.  Either may be NULL (not both).  A descriptor with other q_start than the append's
+ * reads any last part of each sequence.  A sequence shorter than its rows is an index error.
+ * Pointers 16-byte aligned, strides (in f32 values) multiples of 4 and at least kv_heads * head_dim.
+ * Errors: NULL, SHAPE, MISALIGNED, VALUE (k_out and v_out overlap), DEVICE, LAUNCH.
+ */
+qmd_status qmd_kv_read(const qmd_kv_cache *cache, const qmd_kv_batch *batch, float *k_out, int64_t k_stride,
+                       float *v_out, int64_t v_stride, void *stream);
+
+/*
+ * qmd_kv_attention -- for each row r at position p and query head h (key/value head
+ * g = h / (q_heads / kv_heads)), over the cached positions j with j <= p and, where window > 0,
+ * j > p - window:
+ *     s_j = scale * sum_d q[r][h][d] * K[j][g][d],   out[r][h] = sum_j e^(s_j - m) V[j][g] / sum_j e^(s_j - m)
+ * with m the largest s_j.  A row that sees no position (a sequence with fewer tokens than rows)
+ * gets zeros.  f32 throughout to about 1e-6: the 8-bit codes enter the tensor cores exactly, the
+ * query and the weights as two f16 parts each (22 bits), sums are f32.  NaN or infinite queries
+ * affect their own row and head only.
+ *
+ *   q         f32 rows of q_heads * head_dim values (rotated already), row r at q + r * q_stride
+ *   out       f32 rows likewise; must not overlap q
+ *   scale     finite (1 / sqrt(head_dim) as a rule)
+ *   window    0: no window; else >= 1
+ *   workspace device, qmd_kv_workspace_bytes() bytes, 16-byte aligned, owned by the caller.  Zero
+ *             it once; every call that completes leaves its counters zeroed again.  Calls ordered in
+ *             one stream may share it; calls that may run at the same time on the GPU (other
+ *             streams, two captured graphs) need their own.
+ * q_heads a multiple of kv_heads, at most 64 to one.  Pointers 16-byte aligned, strides (in f32
+ * values) multiples of 4 and at least q_heads * head_dim.  The same inputs on the same device give
+ * the same bits.  Built for the few rows of a decode step: the work of a long prompt's rows is
+ * done right but not at a prompt kernel's rate.
+ * Errors: NULL, SHAPE, MISALIGNED, VALUE (scale, window, overlap), DEVICE, LAUNCH.
+ */
+qmd_status qmd_kv_attention(const qmd_kv_cache *cache, const qmd_kv_batch *batch, const float *q, int64_t q_stride,
+                            int q_heads, float scale, int64_t window, float *out, int64_t out_stride, void *workspace,
+                            void *stream);
+
+/* Bytes of qmd_kv_attention's workspace on the current device (0 if there is none). */
+size_t qmd_kv_workspace_bytes(void);
+
+/* ---- low-rank adapters beside a shared projection ------------------------------------------ */
+
+typedef enum qmd_half { QMD_F16 = 1, QMD_BF16 = 2 } qmd_half;
+
+/*
+ * qmd_lora_add -- adds each vector's own low-rank adapter to a projection that all share:
+ *     out[v] = base[v] + scale[a] * (B[a] (A[a] x[v])),   a = adapter[v];  out[v] = base[v] where a < 0
+ * for v < batch, in f32 (A and B are widened exactly; x is not quantised).  base is the shared
+ * projection's output (qmd_qmatvec's y) and out may be base itself.
+ *   type     QMD_F16 or QMD_BF16: how A and B are held
+ *   A        [adapters][rank][K], B [adapters][rows][rank], 16-byte aligned.  A smaller adapter in
+ *            the same stack is padded with zeros.
+ *   scale    f32 [adapters]; adapter int32 [batch], device, read when the call runs (an index at
+ *            or above `adapters` is an index error: that vector's base is copied)
+ *   x        f32 [batch][K], 16-byte aligned; base, out f32 [batch][rows], 4-byte aligned
+ * rank a multiple of 8, 8..QMD_LORA_MAX_RANK; K a multiple of 256, at most 65536; rows 1..2^24;
+ * batch 1..QMD_MAX_BATCH; adapters 1..2^20.
+ * A, B and scale are weights in the sense of the launch order above.  out must not overlap x, nor
+ * base otherwise than by being it.
+ * Errors: NULL, FORMAT (type), K_NOT_MULTIPLE_OF_256, BATCH, SHAPE, MISALIGNED, VALUE (overlap),
+ * DEVICE, LAUNCH.
+ */
+qmd_status qmd_lora_add(qmd_half type, const float *x, const float *base, const void *A, const void *B,
+                        const float *scale, const int32_t *adapter, float *out, int64_t K, int64_t rows, int rank,
+                        int adapters, int batch, void *stream);
+
 /* Name of a status code (static string). */
 const char *qmd_status_str(qmd_status s);
 
@@ -320,8 +477,9 @@ const char *qmd_last_error_detail(void);
 /*
  * qmd_get_device_error -- synchronises `stream`, then reads and clears the current device's
  * error word, which kernels set when a bounded wait (on an asynchronous copy) gives up instead
- * of hanging.  Returns QMD_ERR_DEVICE_TIMEOUT if it was set, QMD_ERR_LAUNCH if the stream
- * reported a CUDA error, else QMD_OK.  ("One kernel, any device", §1: a refused launch is
+ * of hanging, and when they meet an index in device memory that is out of range.  Returns
+ * QMD_ERR_DEVICE_TIMEOUT if a wait gave up, else QMD_ERR_INDEX if an index was out of range,
+ * QMD_ERR_LAUNCH if the stream reported a CUDA error, else QMD_OK.  ("One kernel, any device", §1: a refused launch is
  * returned with its reason, never dropped.)
  */
 qmd_status qmd_get_device_error(void *stream);

@@ -1,4 +1,5 @@
-"""Thin Python binding of libqmd (ctypes): decode-time Q4_K / Q6_K x q8_K mat-vec on GB300.
+"""Thin Python binding of libqmd (ctypes): decode-time Q4_K / Q6_K x q8_K mat-vec on GB300, and
+the operators of a decode step around it (the 8-bit key/value cache, low-rank adapters).
 
 Argument marshalling only.  Every step of the computation runs in the library's CUDA kernels;
 torch supplies device memory and streams.  The functions here carry the C ABI's names
@@ -20,6 +21,9 @@ QMD_WORKSPACE_BYTES = 4096
 Q4_K = 12
 Q5_K = 13
 Q6_K_SPLIT = 14
+QMD_KV_BLOCK = 16
+ROPE_HALVES, ROPE_ADJACENT = 0, 1
+F16, BF16 = 1, 2
 
 STATUS = {
     0: "QMD_OK",
@@ -33,6 +37,7 @@ STATUS = {
     8: "QMD_ERR_DEVICE_TIMEOUT",
     9: "QMD_ERR_DEVICE",
     10: "QMD_ERR_VALUE",
+    11: "QMD_ERR_INDEX",
 }
 
 
@@ -45,6 +50,18 @@ class QmdError(RuntimeError):
 
 class Q8KPtrs(ctypes.Structure):
     _fields_ = [("qs", ctypes.c_void_p), ("d", ctypes.c_void_p), ("bsums", ctypes.c_void_p)]
+
+
+class KVCachePtrs(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int),
+                ("page_tokens", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class KVBatchPtrs(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("rows", ctypes.c_int64), ("seqs", ctypes.c_int),
+                ("max_q", ctypes.c_int)]
 
 
 _lib = None
@@ -66,6 +83,7 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         i64, i32, vp, u64 = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_uint64
         ip = ctypes.POINTER(ctypes.c_int)
         sizep = ctypes.POINTER(ctypes.c_size_t)
+        cp, bp = ctypes.POINTER(KVCachePtrs), ctypes.POINTER(KVBatchPtrs)
         sigs = {
             "qmd_q8k_pack": ([vp, Q8KPtrs, i64, i32, vp], i32),
             "qmd_rmsnorm_q8k_pack": ([vp, vp, vp, ctypes.c_float, vp, Q8KPtrs, i64, i32, vp], i32),
@@ -96,6 +114,11 @@ def lib(path: str | None = None) -> ctypes.CDLL:
             "qmd_debug_set_dynamic_tiles": ([i32], None),
             "qmd_debug_set_split_k": ([i32], None),
             "qmd_version": ([], i32),
+            "qmd_kv_append": ([cp, bp, vp, i64, vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, i32, vp], i32),
+            "qmd_kv_read": ([cp, bp, vp, i64, vp, i64, vp], i32),
+            "qmd_kv_attention": ([cp, bp, vp, i64, i32, ctypes.c_float, i64, vp, i64, vp, vp], i32),
+            "qmd_kv_workspace_bytes": ([], ctypes.c_size_t),
+            "qmd_lora_add": ([i32, vp, vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, vp], i32),
         }
         if hasattr(L, "qmd_debug_trace"):  # the traced build (include/qmd_trace.h)
             sigs["qmd_debug_trace"] = ([vp, i64], i32)
@@ -245,6 +268,203 @@ def qmatvec_rmsnorm_x(fmt: int, W, W_aux, x, r, g, eps: float, h_out=None, y=Non
     _check(lib().qmd_qmatvec_rmsnorm_x(fmt, _ptr(W), _ptr(W_aux), _ptr(x), _ptr(r), _ptr(g), float(eps),
                                        _ptr(h_out), out, _ptr(y), rows, K, batch, _stream(stream)))
     return y
+
+
+# ---- the key/value cache and the adapters ------------------------------------------------------
+
+
+def _need(ok: bool, status: int, detail: str) -> None:
+    if not ok:
+        raise QmdError(status, detail)
+
+
+def _on_current_device(t, what: str) -> None:
+    import torch
+    _need(t.is_cuda and t.device.index == torch.cuda.current_device(), 9,
+          f"{what} must be on the current CUDA device")
+
+
+def _array(t, dtype, shape, device, what: str) -> None:
+    """A contiguous tensor of this type and shape (None: any extent) on this device."""
+    _need(t.dtype == dtype, 2, f"{what}: {dtype} is wanted, got {t.dtype}")
+    _need(t.dim() == len(shape) and all(w is None or n == w for n, w in zip(t.shape, shape)), 6,
+          f"{what}: shape {tuple(shape)} is wanted, got {tuple(t.shape)}")
+    _need(t.is_contiguous(), 6, f"{what} must be contiguous")
+    _need(t.device == device, 9, f"{what} is on {t.device}, not on {device}")
+
+
+def _rows_of(t, rows: int, heads: int | None, dim: int, device, what: str) -> tuple[int, int]:
+    """(heads, row stride) of f32 rows [rows or more, heads, dim] or [rows or more, heads * dim],
+    strided by rows only."""
+    import torch
+    _need(t.dtype == torch.float32, 2, f"{what}: float32 is wanted, got {t.dtype}")
+    _need(t.device == device, 9, f"{what} is on {t.device}, not on {device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        width = shape[1] * shape[2]
+        ok = shape[2] == dim and stride[2] == 1 and (stride[1] == dim or shape[1] == 1)
+    else:
+        width = shape[1] if len(shape) == 2 else 0
+        ok = len(shape) == 2 and width % dim == 0 and stride[1] == 1
+    _need(ok and width > 0 and shape[0] >= rows and (heads is None or width == heads * dim), 6,
+          f"{what}: {rows} or more rows of {heads or 'some'} heads of {dim} values are wanted, strided by rows only; "
+          f"got shape {tuple(shape)}, strides {tuple(stride)}")
+    return width // dim, stride[0] if shape[0] > 1 else (width + 3) // 4 * 4
+
+
+class KVCache:
+    """A paged 8-bit key/value cache: int8 codes [pages, kv_heads, page_tokens, head_dim] of keys and
+    of values, and f32 scales [pages, kv_heads, page_tokens / 16].  A cached value is code * scale."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        _need(k.dim() == 4, 6, "k: [pages, kv_heads, page_tokens, head_dim] is wanted")
+        pages, heads, tokens, dim = k.shape
+        _array(k, torch.int8, k.shape, k.device, "k")
+        _array(v, torch.int8, k.shape, k.device, "v")
+        for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _array(t, torch.float32, (pages, heads, tokens // QMD_KV_BLOCK), k.device, what)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.kv_heads, self.head_dim, self.device = heads, dim, k.device
+        self.ptrs = KVCachePtrs(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), pages, heads, tokens, dim)
+
+    @staticmethod
+    def empty(pages: int, kv_heads: int, page_tokens: int, head_dim: int, device="cuda") -> "KVCache":
+        import torch
+        codes = [torch.zeros((pages, kv_heads, page_tokens, head_dim), dtype=torch.int8, device=device) for _ in "kv"]
+        scales = [torch.zeros((pages, kv_heads, page_tokens // QMD_KV_BLOCK), device=device) for _ in "kv"]
+        return KVCache(*codes, *scales)
+
+
+class KVBatch:
+    """The sequences of a call, for every layer of a step: page_table int32 [seqs, columns], kv_len
+    int32 [seqs] (tokens in the cache, the call's rows counted in), and q_start int32 [seqs + 1] (the
+    first row of each sequence, and the end of the last) with the most rows a sequence has and the
+    rows of the call's tensors; without q_start every sequence has max_q rows."""
+
+    def __init__(self, page_table, kv_len, q_start=None, max_q: int = 1, rows: int | None = None):
+        import torch
+        _need(page_table.dim() == 2, 6, "page_table: [seqs, columns] is wanted")
+        seqs = page_table.shape[0]
+        _array(page_table, torch.int32, page_table.shape, page_table.device, "page_table")
+        _array(kv_len, torch.int32, (seqs,), page_table.device, "kv_len")
+        if q_start is not None:
+            _array(q_start, torch.int32, (seqs + 1,), page_table.device, "q_start")
+            _need(rows is not None, 6, "rows: the rows of the call's tensors are wanted with q_start")
+        self.page_table, self.kv_len, self.q_start = page_table, kv_len, q_start
+        self.max_q, self.rows, self.device = max_q, seqs * max_q if rows is None else rows, page_table.device
+        self.ptrs = KVBatchPtrs(_ptr(page_table), _ptr(kv_len), _ptr(q_start), page_table.shape[1], self.rows, seqs, max_q)
+
+
+def _kv_devices(cache: KVCache, batch: KVBatch) -> None:
+    _on_current_device(cache.k, "the cache")
+    _need(batch.device == cache.device, 9, f"the batch is on {batch.device}, the cache on {cache.device}")
+
+
+def rope_table(positions: int, rot: int, base: float = 10000.0, inv_freq=None, device="cuda"):
+    """f32 [positions, rot]: the rot / 2 cosines and then the rot / 2 sines of each position's angles
+    p * base^(-2 i / rot) (or p * inv_freq[i]), taken in 64 bits: made once, when a model is loaded."""
+    import torch
+    if inv_freq is None:
+        inv_freq = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    inv_freq = torch.as_tensor(inv_freq, dtype=torch.float64)
+    _need(inv_freq.shape == (rot // 2,), 6, f"inv_freq: {rot // 2} values are wanted")
+    angle = torch.arange(positions, dtype=torch.float64)[:, None] * inv_freq
+    return torch.cat((angle.cos(), angle.sin()), 1).float().to(device)
+
+
+def kv_append(cache: KVCache, batch: KVBatch, k, v, rope=None, q=None, q_out=None, pairs: int = ROPE_HALVES,
+              stream=None):
+    """qmd_kv_append: rotates the rows' keys and queries by the table's positions, quantises keys and
+    values into the cache and returns the rotated queries (q_out, by default a new tensor; None
+    without q).  k, v f32 [rows, kv_heads, head_dim], q f32 [rows, heads, head_dim], strided by rows
+    only (parts of one fused projection's output); q_out may be q."""
+    import torch
+    _kv_devices(cache, batch)
+    D, dev, T = cache.head_dim, cache.device, batch.rows
+    _, ks = _rows_of(k, T, cache.kv_heads, D, dev, "k")
+    _, vs = _rows_of(v, T, cache.kv_heads, D, dev, "v")
+    heads = qs = os_ = 0
+    if q is not None:
+        heads, qs = _rows_of(q, T, None, D, dev, "q")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.float32, device=dev)
+        _, os_ = _rows_of(q_out, T, heads, D, dev, "q_out")
+    n = rot = 0
+    if rope is not None:
+        _array(rope, torch.float32, (None, None), dev, "rope")
+        n, rot = rope.shape
+    _check(lib().qmd_kv_append(cache.ptrs, batch.ptrs, _ptr(k), ks, _ptr(v), vs, _ptr(q), qs, heads, _ptr(q_out), os_,
+                               _ptr(rope), n, rot, pairs, _stream(stream)))
+    return q_out
+
+
+def kv_read(cache: KVCache, batch: KVBatch, k_out=None, v_out=None, stream=None):
+    """qmd_kv_read: the rows' keys and values as the cache holds them, code * scale, f32
+    [rows, kv_heads, head_dim] each (new tensors by default)."""
+    import torch
+    _kv_devices(cache, batch)
+    H, D, dev, T = cache.kv_heads, cache.head_dim, cache.device, batch.rows
+    if k_out is None:
+        k_out = torch.empty((T, H, D), dtype=torch.float32, device=dev)
+    if v_out is None:
+        v_out = torch.empty((T, H, D), dtype=torch.float32, device=dev)
+    _, ks = _rows_of(k_out, T, H, D, dev, "k_out")
+    _, vs = _rows_of(v_out, T, H, D, dev, "v_out")
+    _check(lib().qmd_kv_read(cache.ptrs, batch.ptrs, _ptr(k_out), ks, _ptr(v_out), vs, _stream(stream)))
+    return k_out, v_out
+
+
+def kv_workspace(device="cuda"):
+    """A zeroed workspace for kv_attention on the current device.  Calls ordered in one stream may
+    share it; calls that may run at the same time (other streams, two captured graphs) need their own."""
+    import torch
+    n = int(lib().qmd_kv_workspace_bytes())
+    _need(n > 0, 9, "no usable device")
+    return torch.zeros(n // 4, dtype=torch.int32, device=device)
+
+
+def kv_attention(cache: KVCache, batch: KVBatch, q, scale: float, workspace, window: int = 0, out=None, stream=None):
+    """qmd_kv_attention: attention of the rows' queries (rotated; f32 [rows, heads, head_dim], strided
+    by rows only) over the cached keys and values of their sequences.  out f32, by default
+    [rows, heads * head_dim]; rows that no sequence owns are not written."""
+    import torch
+    _kv_devices(cache, batch)
+    D, dev, T = cache.head_dim, cache.device, batch.rows
+    heads, qs = _rows_of(q, T, None, D, dev, "q")
+    if out is None:
+        out = torch.empty((T, heads * D), dtype=torch.float32, device=dev)
+    _, os_ = _rows_of(out, T, heads, D, dev, "out")
+    _array(workspace, torch.int32, (None,), dev, "workspace")
+    _need(workspace.numel() * 4 >= lib().qmd_kv_workspace_bytes(), 6, "the workspace is too small")
+    _check(lib().qmd_kv_attention(cache.ptrs, batch.ptrs, _ptr(q), qs, heads, float(scale), int(window), _ptr(out), os_,
+                                  _ptr(workspace), _stream(stream)))
+    return out
+
+
+def lora_add(x, base, A, B, adapter, scale, out=None, stream=None):
+    """qmd_lora_add: out[v] = base[v] + scale[a] * (B[a] (A[a] x[v])) with a = adapter[v], or base[v]
+    where a < 0.  x f32 [batch, K]; base, out f32 [batch, rows] (out may be base); A f16 or bf16
+    [adapters, rank, K], B [adapters, rows, rank]; adapter int32 [batch]; scale f32 [adapters]."""
+    import torch
+    _on_current_device(x, "x")
+    dev = x.device
+    _need(A.dtype in (torch.float16, torch.bfloat16), 2, f"A: float16 or bfloat16 is wanted, got {A.dtype}")
+    _need(A.dim() == 3 and x.dim() == 2 and base.dim() == 2, 6,
+          "x [batch, K], base [batch, rows] and A [adapters, rank, K] are wanted")
+    (n, rank, K), batch, rows = A.shape, x.shape[0], base.shape[1]
+    _array(x, torch.float32, (batch, K), dev, "x")
+    _array(base, torch.float32, (batch, rows), dev, "base")
+    _array(A, A.dtype, (n, rank, K), dev, "A")
+    _array(B, A.dtype, (n, rows, rank), dev, "B")
+    _array(scale, torch.float32, (n,), dev, "scale")
+    _array(adapter, torch.int32, (batch,), dev, "adapter")
+    if out is None:
+        out = torch.empty((batch, rows), dtype=torch.float32, device=dev)
+    _array(out, torch.float32, (batch, rows), dev, "out")
+    _check(lib().qmd_lora_add(F16 if A.dtype == torch.float16 else BF16, _ptr(x), _ptr(base), _ptr(A), _ptr(B),
+                              _ptr(scale), _ptr(adapter), _ptr(out), K, rows, rank, n, batch, _stream(stream)))
+    return out
 
 
 def q6k_prefix_stride(K: int) -> int:

@@ -934,6 +934,7 @@ const char *qmd_status_str(qmd_status s)
     case QMD_ERR_DEVICE_TIMEOUT: return "QMD_ERR_DEVICE_TIMEOUT";
     case QMD_ERR_DEVICE: return "QMD_ERR_DEVICE";
     case QMD_ERR_VALUE: return "QMD_ERR_VALUE";
+    case QMD_ERR_INDEX: return "QMD_ERR_INDEX";
     }
     return "QMD_ERR_UNKNOWN";
 }
@@ -956,7 +957,7 @@ qmd_status qmd_get_device_error(void *stream)
         if (e != cudaSuccess)
             return fail(QMD_ERR_LAUNCH, "clear error word", e);
         snprintf(g_detail, sizeof g_detail, "device error word 0x%x", v);
-        return QMD_ERR_DEVICE_TIMEOUT;
+        return v == ERRBIT_INDEX ? QMD_ERR_INDEX : QMD_ERR_DEVICE_TIMEOUT;
     }
     return QMD_OK;
 }

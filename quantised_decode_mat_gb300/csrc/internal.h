@@ -14,6 +14,7 @@ enum : unsigned {
     ERRBIT_DEBUG_WAIT = 2u,   // the test-only wait kernel gave up (as intended)
     ERRBIT_DRAIN_WAIT = 4u,   // draining copies after a give-up also gave up
     ERRBIT_PLAN = 8u,         // a launch whose geometry its plan does not allow (rows per CTA, threads)
+    ERRBIT_INDEX = 16u,       // an index in device memory (page, length, row offset, adapter) out of its range
 };
 
 struct DeviceInfo {
@@ -115,5 +116,21 @@ qmd_status launch_q8k_pack(const float *x, int8_t *qs, float *d, int16_t *bsums,
                            cudaStream_t s);
 qmd_status launch_q6k_split(const uint8_t *gguf, uint8_t *body, uint16_t *prefix, int64_t rows,
                             int nb, int64_t prefix_stride, cudaStream_t s);
+
+// ---- key/value cache, adapters -------------------------------------------------------------
+struct KvParams;  // kv.cuh
+qmd_status launch_kv_append(const KvParams &kv, int head_dim, const float *k, int64_t k_stride, const float *v,
+                            int64_t v_stride, const float *q, int64_t q_stride, int q_heads, float *q_out,
+                            int64_t q_out_stride, const float *rope, int64_t rope_rows, int rot, int pairs, int sms,
+                            cudaStream_t s);
+qmd_status launch_kv_read(const KvParams &kv, int head_dim, float *k, int64_t k_stride, float *v, int64_t v_stride,
+                          int sms, cudaStream_t s);
+qmd_status launch_kv_attention(const KvParams &kv, int head_dim, const float *q, int64_t q_stride, int q_heads,
+                               float scale, int64_t window, float *out, int64_t out_stride, void *ws,
+                               const DeviceInfo &dev, cudaStream_t s);
+size_t kv_attention_workspace(const DeviceInfo &dev);
+qmd_status launch_lora_add(qmd_half type, const float *x, const float *base, const void *A, const void *B,
+                           const float *scale, const int32_t *adapter, float *out, int64_t K, int64_t rows, int rank,
+                           int adapters, int batch, const DeviceInfo &dev, unsigned *err, cudaStream_t s);
 
 }  // namespace qmd
