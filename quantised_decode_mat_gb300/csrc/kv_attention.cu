@@ -3,9 +3,43 @@
 // "Language models on the device: the cajeta-llm kernels", §2.5: attention over the key/value
 // cache, 1, 4 or 8 query heads to a key/value head.  Per row at position p and query head, over the
 // positions j that it sees:  out = sum_j e^(s_j - m) V[j] / sum_j e^(s_j - m),  s_j = scale q . K[j].
-// One pass with a running maximum m and sum.
 //
-// Plain form: one warp per (row, query head), a position at a time.
+// One pass over the cache, which bounds it: a decode row does 2 multiply-adds per byte read.
+//
+// Work.  An item is up to R = 4 NT query rows (rows x heads that share a key/value head) of one
+// sequence and one key/value head; a unit is one block of 16 positions of an item.  The units of
+// all items stand in one line (sequence, row group, head, block), which is cut into equal ranges
+// for one CTA per SM and these into equal ranges for the CTA's warps, whatever the sequences'
+// lengths: no work list, no launch that depends on lengths held on the device.  An item inside one
+// warp's range is finished by that warp; one cut inside a CTA is joined through shared memory; one
+// cut between CTAs through the workspace, by the CTA that comes last (a counter per CTA; nobody
+// waits).  The joins add in the order of the parts, so the bits do not depend on who comes last.
+//
+// A unit.  S^T = K Q^T and O^T += V^T P^T by mma.sync m16n8k16 (f16 in, f32 sums): positions (or
+// the head's dimension) are the 16 rows, query rows the 8 columns, two columns to a query row: the
+// value's first 11 bits and the next 11 (2^11 times larger), so that q and the weights keep 22
+// bits and the codes, integers up to 127, enter exactly.  (tcgen05 wants its operands in shared
+// memory and 128 rows: the codes would be widened and written there at twice the bytes for columns
+// that a decode step does not fill.)  The order of the head's dimension inside a product is free,
+// so a lane takes 16 neighbouring bytes of a key for four products, and of four values' rows 16
+// neighbouring dimensions for eight, straight from the cache's rows; the accumulators then hold 16
+// neighbouring outputs.  A code c becomes an f16 by bytes: c + 128 under the exponent byte 0x64 is
+// 1024 + c + 128, less 1152.  P^T moves from the first product's layout to the second's by an 8 x 8
+// transpose between lanes (movmatrix).
+//
+// The running maximum moves only when a score passes it by more than 2^8 (then every sum is
+// rescaled); until then weights are at most 2^8, which costs f32 nothing.  A value block's scale
+// enters the weights relative to a running power of two at or above every scale so far, so the f16
+// parts neither overflow nor lose bits that the sum keeps.
+//
+// Loads: each lane copies its own 16-byte pieces (cp.async) into its own places of a ring of STAGES
+// blocks per warp in shared memory: no bank conflicts, no barriers, 4 KB a block (head_dim 128) and
+// warp in flight.  Page numbers and scales are looked up 32 blocks at a time, a lane each, a chunk
+// ahead.
+#include <climits>
+#include <mutex>
+
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -18,84 +52,684 @@ struct AttnArgs {
     KvParams kv;
     const float *q;
     float *out;
+    float *part;     // workspace: [CTA][2][R][D] sums, then [CTA][2][R][2] maximum and weight sum
+    unsigned *ctr;   // workspace: a counter per CTA
     int64_t q_stride, out_stride, window;
-    int q_heads;
-    float scale;
+    int q_heads, group;  // query heads; of them per key/value head
+    float scale_log2e;
 };
 
-template <int D>
-__global__ void __launch_bounds__(32) kv_attention_kernel(const AttnArgs a)
+// Warps, ring depth and shared memory of an instance.
+template <int D, int NT>
+struct AttnCfg {
+    static constexpr int R = 4 * NT;
+    static constexpr int W = D == 256 ? (NT == 1 ? 8 : 6) : D * NT <= 128 ? 16 : NT <= 2 ? 12 : 8;
+    static constexpr int STAGES = 2;
+    static constexpr int BLOCK_BYTES = 32 * D;  // keys and values of 16 positions
+    static constexpr int RING = STAGES * BLOCK_BYTES;
+    static constexpr int SLOT = R * D * 4;
+    // query fragments stay in registers until the sums alone take 64 of them
+    static constexpr bool QS = R * D >= 1024;
+    static constexpr int QBYTES = QS ? R * D * 4 : 0;  // two f16 parts
+    static_assert(RING >= SLOT, "a warp's last part lies in its ring");
+    // rings, first parts, query fragments, maxima and sums of 2 W parts, jobs
+    static constexpr int FIXED = W * (RING + SLOT + QBYTES) + 2 * W * R * 8 + (W + 1) * 32;
+    static_assert(FIXED + 256 + (QMD_KV_MAX_SEQS + 1) * 8 <= 227 * 1024, "fits beside the sums of the most sequences");
+};
+
+constexpr int ATT_MAX_ROWS_FLOATS = 16 * 128;  // the largest R x D of an instance (8 x 256 is the same)
+constexpr float ATT_NONE = -3.0e38f;           // the maximum before any score
+constexpr float ATT_SLACK = 8.0f;              // how far (log2) a score may pass the running maximum
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
 {
-    constexpr int E = D / 32;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// Two bytes of w (biased by 128), picked by sel over (w, 0x64646464), as codes in f16.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t codes_f16(uint32_t w)
+{
+    const uint32_t u = __byte_perm(w, 0x64646464u, SEL);
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const __half2 c = __hsub2(*reinterpret_cast<const __half2 *>(&u), bias);
+    return *reinterpret_cast<const uint32_t *>(&c);
+}
+
+// x as two f16: the first 11 bits, and the rest 2^11 times larger.
+__device__ __forceinline__ uint32_t split_f16(float x)
+{
+    const __half h = __float2half_rn(x);
+    const __half l = __float2half_rn((x - __half2float(h)) * 2048.0f);
+    return (uint32_t)__half_as_ushort(h) | (uint32_t)__half_as_ushort(l) << 16;
+}
+
+constexpr float LOW_PART = 1.0f / 2048.0f;
+
+struct Group {  // the rows of a row group and what they see
+    int lo, hi;  // blocks [lo, hi) that any of them sees
+    int rows;    // query rows in the group
+};
+
+__device__ __forceinline__ int row_end(const KvSeq &q, int i) { return max(0, q.len - q.n + 1 + i); }
+__device__ __forceinline__ int row_begin(const AttnArgs &a, int end)
+{
+    return a.window > 0 && end > a.window ? (int)(end - a.window) : 0;
+}
+
+template <int R>
+__device__ __forceinline__ Group group_of(const AttnArgs &a, const KvSeq &q, int cg)
+{
+    Group g;
+    g.rows = min(R, q.n * a.group - cg * R);
+    const int last = row_end(q, (cg * R + g.rows - 1) / a.group);
+    g.lo = row_begin(a, row_end(q, cg * R / a.group)) / KV_BLOCK;
+    g.hi = (last + KV_BLOCK - 1) / KV_BLOCK;
+    return g;
+}
+
+struct Job {  // an item cut at the end of a warp's range
+    int start, end;    // its units, counted from the CTA's first
+    int row0, first;   // the sequence's first row; the group's first query row
+    int head, rows;    // rows 0: no job
+    int pad[2];
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel(const AttnArgs a)
+{
+    using C = AttnCfg<D, NT>;
+    constexpr int R = C::R, W = C::W, S = C::STAGES;
+    constexpr int KH = D / 64;   // 64-byte parts of a key, 16 bytes to a lane
+    constexpr int MT = D / 16;   // 16-row tiles of V^T
+    constexpr int VW = D / 32;   // words of a value row that a lane holds
+    extern __shared__ __align__(16) unsigned char smem[];
+    float2 *s_ml = reinterpret_cast<float2 *>(smem + W * (C::RING + C::SLOT + C::QBYTES));  // [W][2][R] maximum, weight sum
+    Job *s_job = reinterpret_cast<Job *>(s_ml + 2 * W * R);                      // [1 + W]
+    int64_t *s_pre = reinterpret_cast<int64_t *>(s_job + W + 1);                 // [seqs + 1] units before a sequence
+    __shared__ int64_t s_warp[W + 1];
+    __shared__ int s_last[2];
+
     pdl_launch_dependents();
     pdl_wait();
     const KvParams &p = a.kv;
-    const int lane = threadIdx.x;
-    const int s = blockIdx.x / p.max_q, i = blockIdx.x % p.max_q, h = blockIdx.y;
-    const int g = h / (a.q_heads / p.heads);
-    const KvSeq sq = kv_seq(p, s);
-    if (i >= sq.n)
-        return;
-    const int64_t row = sq.row0 + i;
-    float x[E], o[E] = {};
-    load_f32(x, a.q + row * a.q_stride + h * D + E * lane);
-    const int pos = sq.len - sq.n + i;
-    const int begin = a.window > 0 && pos + 1 > a.window ? (int)(pos + 1 - a.window) : 0;
-    float m = -INFINITY, l = 0.0f;
-    for (int j = begin; j <= pos; ++j) {
-        const int page = kv_page(p, s, j / KV_BLOCK);
-        if (page < 0)
-            continue;
-        const int64_t blk = kv_block_offset(p, page, g, j / KV_BLOCK);
-        float c[E];
-        load_codes(c, p.k + (blk * KV_BLOCK + j % KV_BLOCK) * D + E * lane);
-        float t = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            t = fmaf(x[e], c[e], t);
-#pragma unroll
-        for (int w = 16; w > 0; w >>= 1)
-            t += __shfl_xor_sync(0xffffffffu, t, w);
-        t *= p.ks[blk] * a.scale;
-        const float mn = fmaxf(m, t), f = m == mn ? 1.0f : expf(m - mn), w = p.vs[blk], pr = expf(t - mn);
-        m = mn;
-        l = l * f + pr;
-        load_codes(c, p.v + (blk * KV_BLOCK + j % KV_BLOCK) * D + E * lane);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            o[e] = fmaf(pr * w, c[e], o[e] * f);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+
+    // ---- the line of units: an exclusive sum over the sequences ------------------------------
+    if (lane == 0) {
+        s_job[1 + warp].rows = 0;
+        if (warp == 0)
+            s_job[0].rows = 0;
     }
+    int64_t before = 0;
+    for (int s0 = 0; s0 < p.seqs; s0 += W * 32) {
+        const int s = s0 + tid;
+        int64_t u = 0;
+        if (s < p.seqs) {
+            const KvSeq q = kv_seq(p, s);
+            for (int cg = 0; cg * R < q.n * a.group; ++cg) {
+                const Group gr = group_of<R>(a, q, cg);
+                u += max(1, gr.hi - gr.lo);
+            }
+            u *= p.heads;
+        }
+        int64_t sum = u;
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        o[e] = l == 0.0f ? 0.0f : o[e] / l;
-    store_f32(a.out + row * a.out_stride + h * D + E * lane, o);
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o)
+                sum += x;
+        }
+        __syncthreads();
+        if (lane == 31)
+            s_warp[warp] = sum;
+        __syncthreads();
+        int64_t base = before, total = 0;
+        for (int w = 0; w < W; ++w) {
+            if (w < warp)
+                base += s_warp[w];
+            total += s_warp[w];
+        }
+        if (s < p.seqs)
+            s_pre[s] = base + sum - u;
+        before += total;
+    }
+    const int64_t units = before;
+    if (tid == 0)
+        s_pre[p.seqs] = units;
+    __syncthreads();
+
+    // ---- this CTA's range, this warp's range ---------------------------------------------------
+    // at least a unit for every warp, so that short items are cut inside a CTA, not between CTAs
+    int64_t per = (units + gridDim.x - 1) / gridDim.x;
+    if (per < W)
+        per = W;
+    const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(units, u0 + per);
+    if (u0 >= units)
+        return;
+    const int span = (int)(u1 - u0), pw = (span + W - 1) / W;
+    int u = warp * pw;  // from here on counted from u0
+    const int w1 = min(span, u + pw);
+
+    unsigned char *ring = smem + warp * C::RING;
+    float *slot0 = reinterpret_cast<float *>(smem + W * C::RING + warp * C::SLOT);
+    const uint32_t ring_a = smem_addr(ring) + 16 * lane;
+
+    int s = 0, cg = 0, head = 0, b0 = 0;  // the item of unit u, and the unit's block in it
+    if (u < w1) {
+        const int64_t at = u0 + u;
+        int lo = 0, hi = p.seqs;  // s_pre[lo] <= at < s_pre[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_pre[mid] <= at)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        s = lo;
+        int64_t rem = at - s_pre[s];
+        const KvSeq sq = kv_seq(p, s);
+        int nb;
+        for (;; ++cg) {
+            const Group gr = group_of<R>(a, sq, cg);
+            nb = max(1, gr.hi - gr.lo);
+            if (rem < (int64_t)p.heads * nb)
+                break;
+            rem -= (int64_t)p.heads * nb;
+        }
+        head = (int)(rem / nb);
+        b0 = (int)(rem % nb);
+    }
+    while (u < w1) {
+        const KvSeq sq = kv_seq(p, s);
+        const Group gr = group_of<R>(a, sq, cg);
+        const int nb = max(1, gr.hi - gr.lo);
+        const int cnt = min(nb - b0, w1 - u);              // units of this item in the range
+        const int real = min(cnt, gr.hi - gr.lo - b0);          // those that hold positions
+
+        // pages and scales, 32 blocks at a time: block index in the pool, or -1
+        const int first_blk = gr.lo + b0;
+        auto page_of = [&](int i) -> int {  // of the item's i-th block here; INT_MIN past the end
+            return i < real ? p.table[(int64_t)s * p.table_stride + (first_blk + i) / p.page_blocks] : INT_MIN;
+        };
+        auto block_of = [&](int i, int page) -> int {
+            if (page < 0 || page >= p.pages) {
+                if (page != INT_MIN)
+                    kv_index_error(p);
+                return -1;
+            }
+            return (page * p.heads + head) * p.page_blocks + (first_blk + i) % p.page_blocks;
+        };
+        int bi_c = block_of(lane, page_of(lane)), bi_n = -1, page_nn = INT_MIN;
+        float ks_c = bi_c >= 0 ? p.ks[bi_c] : 0.0f, vs_c = bi_c >= 0 ? p.vs[bi_c] : 0.0f, ks_n = 0.0f, vs_n = 0.0f;
+        if (real > 32) {
+            bi_n = block_of(32 + lane, page_of(32 + lane));
+            ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
+            page_nn = page_of(64 + lane);
+        }
+
+        auto issue = [&](int j, int idx) {  // copy the item's j-th block into its ring stage
+            if (j < real) {
+                const int bi = __shfl_sync(0xffffffffu, (j >> 5) == (idx >> 5) ? bi_c : bi_n, j & 31);
+                if (bi >= 0) {
+                    const uint32_t dst = ring_a + (j % S) * C::BLOCK_BYTES;
+                    const int8_t *kp = p.k + (int64_t)bi * (KV_BLOCK * D) + g * D + 16 * t;
+#pragma unroll
+                    for (int h = 0; h < KH; ++h) {
+                        cp_async16(dst + (2 * h) * 512, kp + 64 * h);
+                        cp_async16(dst + (2 * h + 1) * 512, kp + 8 * D + 64 * h);
+                    }
+                    const int8_t *vp = p.v + (int64_t)bi * (KV_BLOCK * D) + 2 * t * D + g * (D / 8);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int8_t *src = vp + ((x & 1) + (x >> 1) * 8) * D;
+                        if constexpr (D == 64) {
+                            cp_async8(dst - 8 * lane + 16 * D + x * 256, src);
+                        } else {
+#pragma unroll
+                            for (int y = 0; y < VW / 4; ++y)
+                                cp_async16(dst + 16 * D + (x * (VW / 4) + y) * 512, src + 16 * y);
+                        }
+                    }
+                }
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int j = 0; j < S - 1; ++j)
+            issue(j, 0);
+
+        // ---- the queries: lane (g, t) holds columns g of the tiles, dimensions 64 h + 16 t + 0..15
+        uint32_t qf[C::QS ? 1 : NT][KH * 4][2];
+        float qscale[NT];  // of query row 4 nt + t
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = 4 * nt + (g >> 1);
+            const int rr = cg * R + min(r, gr.rows - 1);  // a column past the rows repeats the last one
+            const float *qp = a.q + (int64_t)(sq.row0 + rr / a.group) * a.q_stride +
+                              (head * a.group + rr % a.group) * D + 16 * t;
+            float x[KH][16];
+            float top = 0.0f;
+#pragma unroll
+            for (int h = 0; h < KH; ++h) {
+                load_f32(x[h], qp + 64 * h);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    top = fmaxf(top, fabsf(x[h][e]));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // q times a power of two, the largest value in [0.5, 1)
+            const int ex = min(252, (int)(__float_as_uint(top) >> 23));
+            const float f = __uint_as_float((uint32_t)(253 - ex) << 23);
+#pragma unroll
+            for (int h = 0; h < KH; ++h)
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t u0_ = split_f16(x[h][4 * w + 2 * e] * f);
+                        const uint32_t u1_ = split_f16(x[h][4 * w + 2 * e + 1] * f);
+                        qf[C::QS ? 0 : nt][4 * h + w][e] = __byte_perm(u0_, u1_, (g & 1) ? 0x7632 : 0x5410);
+                    }
+            if constexpr (C::QS) {
+                uint4 *dst = reinterpret_cast<uint4 *>(smem + W * (C::RING + C::SLOT) + warp * C::QBYTES) + lane;
+#pragma unroll
+                for (int i = 0; i < KH * 2; ++i)
+                    dst[(nt * KH * 2 + i) * 32] =
+                        make_uint4(qf[0][2 * i][0], qf[0][2 * i][1], qf[0][2 * i + 1][0], qf[0][2 * i + 1][1]);
+            }
+            const float back = __uint_as_float((uint32_t)max(1, ex + 1) << 23) * a.scale_log2e;
+            qscale[nt] = __shfl_sync(0xffffffffu, back, 8 * t);
+        }
+        // positions in [all_from, all_to) are seen by every row of the group
+        const int all_to = row_end(sq, cg * R / a.group);
+        const int all_from = row_begin(a, row_end(sq, (cg * R + gr.rows - 1) / a.group));
+
+        float o[NT][MT][4];
+        float m[NT], l[NT];
+        float vref = 1.17549435e-38f, vinv = 8.50705917e37f;  // 2^-126, 2^126
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt] = ATT_NONE;
+            l[nt] = 0.0f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
+        }
+
+        for (int idx = 0; idx < real; ++idx) {
+            if ((idx & 31) == 0 && idx > 0) {
+                bi_c = bi_n, ks_c = ks_n, vs_c = vs_n;
+                bi_n = block_of(idx + 32 + lane, page_nn);
+                ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
+                page_nn = page_of(idx + 64 + lane);
+            }
+            issue(idx + S - 1, idx);
+            cp_async_wait<S - 1>();
+            const unsigned char *st = ring + (idx % S) * C::BLOCK_BYTES;
+            const float ks = __shfl_sync(0xffffffffu, ks_c, idx & 31);
+            const float vs = __shfl_sync(0xffffffffu, vs_c, idx & 31);
+            const int bi = __shfl_sync(0xffffffffu, bi_c, idx & 31);
+
+            // S^T = K Q^T
+            float c[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.0f;
+#pragma unroll
+            for (int h = 0; h < KH; ++h) {
+                uint4 ka = lds128(st + 16 * lane + (2 * h) * 512), kb = lds128(st + 16 * lane + (2 * h + 1) * 512);
+                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+                for (int w2 = 0; w2 < 4; w2 += 2) {
+                    uint32_t f[2][4];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t x = wa[w2 + e] ^ 0x80808080u, y = wb[w2 + e] ^ 0x80808080u;
+                        f[e][0] = codes_f16<0x4140>(x), f[e][1] = codes_f16<0x4140>(y);
+                        f[e][2] = codes_f16<0x4342>(x), f[e][3] = codes_f16<0x4342>(y);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if constexpr (C::QS) {
+                            const uint4 qv = lds128(smem + W * (C::RING + C::SLOT) + warp * C::QBYTES + 16 * lane +
+                                                    (nt * KH * 2 + 2 * h + w2 / 2) * 512);
+                            mma_16816(c[nt], f[0], qv.x, qv.y);
+                            mma_16816(c[nt], f[1], qv.z, qv.w);
+                        } else {
+                            mma_16816(c[nt], f[0], qf[nt][4 * h + w2][0], qf[nt][4 * h + w2][1]);
+                            mma_16816(c[nt], f[1], qf[nt][4 * h + w2 + 1][0], qf[nt][4 * h + w2 + 1][1]);
+                        }
+                    }
+                }
+            }
+
+            // scores of positions pos + g and pos + g + 8 against query row 4 nt + t, in log2 units
+            const int pos = (first_blk + idx) * KV_BLOCK;
+            const bool whole = pos >= all_from && pos + KV_BLOCK <= all_to && bi >= 0;
+            float sc[NT][2];
+            bool up = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float f = qscale[nt] * ks;
+                sc[nt][0] = fmaf(c[nt][1], LOW_PART, c[nt][0]) * f;
+                sc[nt][1] = fmaf(c[nt][3], LOW_PART, c[nt][2]) * f;
+                if (!whole) {
+                    const int end = row_end(sq, (cg * R + min(4 * nt + t, gr.rows - 1)) / a.group);
+                    const int begin = row_begin(a, end), j = pos + g;
+                    if (bi < 0 || j < begin || j >= end)
+                        sc[nt][0] = -INFINITY;
+                    if (bi < 0 || j + 8 < begin || j + 8 >= end)
+                        sc[nt][1] = -INFINITY;
+                }
+                up |= fmaxf(sc[nt][0], sc[nt][1]) > m[nt] + ATT_SLACK;
+            }
+            if (__any_sync(0xffffffffu, up) || vs > vref) {
+                float fv = 1.0f;
+                if (vs > vref) {
+                    const float r = __uint_as_float((__float_as_uint(vs) + 0x7fffffu) & 0x7f800000u);
+                    fv = vref / r;
+                    vref = r;
+                    vinv = 1.0f / r;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float top = fmaxf(sc[nt][0], sc[nt][1]);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    const float mn = top > m[nt] ? top : m[nt];
+                    const float f = ex2(m[nt] - mn);
+                    m[nt] = mn;
+                    l[nt] *= f;
+                    const float fo = f * fv;
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[nt][mt][e] *= fo;
+                }
+            }
+            const float vr = vs * vinv;
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float w = ex2(sc[nt][e] - m[nt]);
+                    l[nt] += w;
+                    pb[nt][e] = transpose_8x8(split_f16(w * vr));
+                }
+
+            // O^T += V^T P^T
+            const unsigned char *sv = st + 16 * D;
+#pragma unroll
+            for (int y = 0; y < (VW + 3) / 4; ++y) {
+                uint32_t v[4][VW < 4 ? VW : 4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    if constexpr (D == 64) {
+                        const uint2 q2 = *reinterpret_cast<const uint2 *>(sv + x * 256 + 8 * lane);
+                        v[x][0] = q2.x, v[x][1] = q2.y;
+                    } else {
+                        const uint4 q4 = lds128(sv + (x * (VW / 4) + y) * 512 + 16 * lane);
+                        v[x][0] = q4.x, v[x][1] = q4.y, v[x][2] = q4.z, v[x][3] = q4.w;
+                    }
+                }
+#pragma unroll
+                for (int w = 0; w < (VW < 4 ? VW : 4); ++w) {
+                    const uint32_t x0 = v[0][w] ^ 0x80808080u, x1 = v[1][w] ^ 0x80808080u;
+                    const uint32_t x2 = v[2][w] ^ 0x80808080u, x3 = v[3][w] ^ 0x80808080u;
+                    const uint32_t e01 = __byte_perm(x0, x1, 0x5140), e23 = __byte_perm(x2, x3, 0x5140);
+                    const uint32_t f01 = __byte_perm(x0, x1, 0x7362), f23 = __byte_perm(x2, x3, 0x7362);
+                    const uint32_t fa[4] = {codes_f16<0x4140>(e01), codes_f16<0x4342>(e01), codes_f16<0x4140>(e23),
+                                            codes_f16<0x4342>(e23)};
+                    const uint32_t fb[4] = {codes_f16<0x4140>(f01), codes_f16<0x4342>(f01), codes_f16<0x4140>(f23),
+                                            codes_f16<0x4342>(f23)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_16816(o[nt][8 * y + 2 * w], fa, pb[nt][0], pb[nt][1]);
+                        mma_16816(o[nt][8 * y + 2 * w + 1], fb, pb[nt][0], pb[nt][1]);
+                    }
+                }
+            }
+        }
+        cp_async_wait<0>();
+
+        // ---- the item's part: finished, or laid down for the join --------------------------------
+        const bool done = b0 == 0 && cnt == nb;
+        const int part = b0 > 0 ? 0 : 1;
+        float *dst = part == 0 ? slot0 : reinterpret_cast<float *>(ring);
+        if (part == 1 && !done)
+            __syncwarp();  // every lane has read the ring
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 4);
+            l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 8);
+            l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 16);
+            const int r = 4 * nt + t;
+            const float f = done ? (l[nt] == 0.0f ? 0.0f : vref / l[nt]) : vref;
+            float y[2 * MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                y[2 * mt] = fmaf(o[nt][mt][1], LOW_PART, o[nt][mt][0]) * f;
+                y[2 * mt + 1] = fmaf(o[nt][mt][3], LOW_PART, o[nt][mt][2]) * f;
+            }
+            if (!done) {
+                store_f32(dst + r * D + 2 * MT * g, y);
+                if (g == 0)
+                    s_ml[(warp * 2 + part) * R + r] = make_float2(m[nt], l[nt]);
+            } else if (r < gr.rows) {
+                const int rr = cg * R + r;
+                store_f32(a.out + (int64_t)(sq.row0 + rr / a.group) * a.out_stride +
+                              (head * a.group + rr % a.group) * D + 2 * MT * g,
+                          y);
+            }
+        }
+        // the item's first cut in this CTA makes the job of joining it
+        if (!done && lane == 0 && (part == 1 || warp == 0)) {
+            Job &j = s_job[part == 1 ? 1 + warp : 0];
+            j.start = u - b0;
+            j.end = u - b0 + nb;
+            j.row0 = sq.row0;
+            j.first = cg * R;
+            j.head = head;
+            j.rows = gr.rows;
+        }
+        u += cnt;
+        b0 = 0;
+        if (u < w1 && ++head == p.heads) {  // on to the next row group, or the next sequence with rows
+            head = 0;
+            if (++cg * R >= sq.n * a.group) {
+                cg = 0;
+                do
+                    ++s;
+                while (s_pre[s + 1] == s_pre[s]);
+            }
+        }
+    }
+    __syncthreads();
+
+    // ---- joins inside the CTA -------------------------------------------------------------------
+    const int64_t part_ml = (int64_t)gridDim.x * 2 * R * D;
+    auto write_out = [&](const Job &j, int r, int d, float y) {
+        const int rr = j.first + r;
+        a.out[(int64_t)(j.row0 + rr / a.group) * a.out_stride + (j.head * a.group + rr % a.group) * D + d] = y;
+    };
+    bool cut = false;  // some item goes on in another CTA
+    for (int jj = 0; jj <= W; ++jj) {
+        const Job j = s_job[jj];
+        if (j.rows == 0)
+            continue;
+        const bool whole = j.start >= 0 && j.end <= span;
+        const int wa = jj == 0 ? 0 : jj - 1;
+        const int wb = (min(j.end, span) - 1) / pw;
+        cut |= !whole;
+        for (int e = tid; e < j.rows * D; e += W * 32) {
+            const int r = e / D, d = e % D;
+            float M = ATT_NONE, L = 0.0f, y = 0.0f;
+            for (int w = wa; w <= wb; ++w)
+                M = fmaxf(M, s_ml[(w * 2 + (w == wa && jj > 0)) * R + r].x);
+            for (int w = wa; w <= wb; ++w) {
+                const bool one = w == wa && jj > 0;
+                const float2 ml = s_ml[(w * 2 + one) * R + r];
+                const float f = ex2(ml.x - M);
+                const float *src = reinterpret_cast<const float *>(one ? smem + w * C::RING
+                                                                       : smem + W * C::RING + w * C::SLOT);
+                L = fmaf(ml.y, f, L);
+                y = fmaf(src[r * D + d], f, y);
+            }
+            if (whole) {
+                write_out(j, r, d, L == 0.0f ? 0.0f : y / L);
+            } else {
+                const int64_t at = ((int64_t)blockIdx.x * 2 + (j.start < 0 ? 0 : 1)) * R + r;
+                a.part[at * D + d] = y;
+                if (d == 0)
+                    reinterpret_cast<float2 *>(a.part + part_ml)[at] = make_float2(M, L);
+            }
+        }
+    }
+    if (!cut)
+        return;
+
+    // ---- joins between CTAs: the one that comes last adds the parts, in their order ---------------
+    __threadfence();
+    __syncthreads();
+    // at most two items are cut: the one that began before this CTA's range (job 0), and the one
+    // that goes on after it (the job with the largest end)
+    int tail = -1;
+    for (int jj = 0; jj <= W; ++jj)
+        if (s_job[jj].rows > 0 && s_job[jj].end > span)
+            tail = jj;
+    const int jobs[2] = {s_job[0].rows > 0 ? 0 : -1, tail == 0 ? -1 : tail};
+    if (tid < 2) {
+        int last = 0;
+        if (jobs[tid] >= 0) {
+            const Job &j = s_job[jobs[tid]];
+            const int c0 = (int)((u0 + j.start) / per), c1 = (int)((u0 + j.end - 1) / per);
+            last = atomicAdd(a.ctr + c0, 1u) == (unsigned)(c1 - c0);
+            if (last)
+                a.ctr[c0] = 0;  // every part has come: left as it was found
+        }
+        s_last[tid] = last;
+    }
+    __syncthreads();
+    for (int x = 0; x < 2; ++x) {
+        if (!s_last[x])
+            continue;
+        __threadfence();
+        const Job j = s_job[jobs[x]];
+        const int c0 = (int)((u0 + j.start) / per), c1 = (int)((u0 + j.end - 1) / per);
+        const float2 *ml = reinterpret_cast<const float2 *>(a.part + part_ml);
+        for (int e = tid; e < j.rows * D; e += W * 32) {
+            const int r = e / D, d = e % D;
+            float M = ATT_NONE, L = 0.0f, y = 0.0f;
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c)
+                M = fmaxf(M, __ldcg(&ml[((int64_t)c * 2 + (c == c0)) * R + r]).x);
+#pragma unroll 4
+            for (int c = c0; c <= c1; ++c) {
+                const int64_t at = ((int64_t)c * 2 + (c == c0)) * R + r;
+                const float2 v = __ldcg(&ml[at]);
+                const float f = ex2(v.x - M);
+                L = fmaf(v.y, f, L);
+                y = fmaf(__ldcg(&a.part[at * D + d]), f, y);
+            }
+            write_out(j, r, d, L == 0.0f ? 0.0f : y / L);
+        }
+    }
 }
 
-qmd_status launch_kv_attention(const KvParams &kv, int head_dim, const float *q, int64_t q_stride, int q_heads,
-                               float scale, int64_t window, float *out, int64_t out_stride, void *ws,
-                               const DeviceInfo &dev, cudaStream_t s)
+template <int D, int NT>
+static qmd_status launch_att(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s)
 {
-    (void)ws, (void)dev;
-    const AttnArgs a = {kv, q, out, q_stride, out_stride, window, q_heads, scale};
+    using C = AttnCfg<D, NT>;
+    const size_t smem = C::FIXED + ((size_t)a.kv.seqs + 1) * sizeof(int64_t);
+    if (smem + 256 > (size_t)dev.smem_optin)
+        return QMD_ERR_SHAPE;
+    {
+        static std::mutex mu;
+        static bool opted[64] = {false};
+        std::lock_guard<std::mutex> lock(mu);
+        if (!opted[dev.device]) {
+            const cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<D, NT>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, dev.smem_optin - 256);
+            if (e != cudaSuccess)
+                return fail(QMD_ERR_LAUNCH, "kv_attention smem attribute", e);
+            opted[dev.device] = true;
+        }
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)kv.seqs * (unsigned)kv.max_q, (unsigned)q_heads);
-    cfg.blockDim = dim3(32);
+    cfg.gridDim = dim3((unsigned)dev.sm_count);
+    cfg.blockDim = dim3(C::W * 32);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (launch_flags() & LAUNCH_NO_PDL) ? 0 : 1;
-    const cudaError_t e = head_dim == 64    ? cudaLaunchKernelEx(&cfg, kv_attention_kernel<64>, a)
-                          : head_dim == 128 ? cudaLaunchKernelEx(&cfg, kv_attention_kernel<128>, a)
-                                            : cudaLaunchKernelEx(&cfg, kv_attention_kernel<256>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, NT>, a);
     return e == cudaSuccess ? QMD_OK : fail(QMD_ERR_LAUNCH, "kv_attention launch", e);
 }
 
+// counters (a CTA each, to a multiple of 16 bytes), then the parts and their maxima and sums
+static size_t counter_bytes(const DeviceInfo &dev) { return ((size_t)dev.sm_count * 4 + 15) / 16 * 16; }
+
 size_t kv_attention_workspace(const DeviceInfo &dev)
 {
-    (void)dev;
-    return 4096;
+    return counter_bytes(dev) + (size_t)dev.sm_count * 2 * (ATT_MAX_ROWS_FLOATS + 16 * 2) * 4;
+}
+
+qmd_status launch_kv_attention(const KvParams &kv, int head_dim, const float *q, int64_t q_stride, int q_heads,
+                               float scale, int64_t window, float *out, int64_t out_stride, void *ws,
+                               const DeviceInfo &dev, cudaStream_t s)
+{
+    const AttnArgs a = {kv, q, out, reinterpret_cast<float *>(static_cast<char *>(ws) + counter_bytes(dev)),
+                        static_cast<unsigned *>(ws), q_stride, out_stride, window, q_heads, q_heads / kv.heads,
+                        scale * 1.4426950408889634f};
+    // rows per item: the least of 4, 8, 16 that holds a sequence's rows of one key/value head
+    const int64_t rows = (int64_t)a.group * kv.max_q;
+    if (head_dim == 64)
+        return rows <= 4 ? launch_att<64, 1>(a, dev, s) : rows <= 8 ? launch_att<64, 2>(a, dev, s) : launch_att<64, 4>(a, dev, s);
+    if (head_dim == 128)
+        return rows <= 4   ? launch_att<128, 1>(a, dev, s)
+               : rows <= 8 ? launch_att<128, 2>(a, dev, s)
+                           : launch_att<128, 4>(a, dev, s);
+    return rows <= 4 ? launch_att<256, 1>(a, dev, s) : launch_att<256, 2>(a, dev, s);
 }
 
 }  // namespace qmd
