@@ -327,7 +327,7 @@ qmd_status qmd_bind_q5k(const void *gguf, int64_t rows, int64_t K);
  *   k, v              int8 [pages][kv_heads][page_tokens][head_dim], 16-byte aligned
  *   k_scale, v_scale  f32  [pages][kv_heads][page_tokens / 16], 4-byte aligned
  *   head_dim 64, 128 or 256; page_tokens a multiple of 16, at most 65536; kv_heads 1..1024;
- *   pages 1..2^31 - 1.
+ *   pages * kv_heads * (page_tokens / 16) at most 2^31 - 1.
  *
  * qmd_kv_batch: what one call is about; the same descriptor serves every layer of a step.
  *   q_start      int32 [seqs + 1], device: sequence s has the call's rows q_start[s] ..

@@ -32,7 +32,8 @@ qmd_status check_kv(const qmd_kv_cache *c, const qmd_kv_batch *b, bool want_k, b
         return QMD_ERR_NULL;
     if ((c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) || c->page_tokens < KV_BLOCK ||
         c->page_tokens > 65536 || c->page_tokens % KV_BLOCK != 0 || c->kv_heads < 1 || c->kv_heads > 1024 ||
-        c->pages < 1 || c->pages > 0x7fffffff)
+        c->pages < 1 || c->pages > 0x7fffffff ||
+        c->pages * c->kv_heads > 0x7fffffff / (c->page_tokens / KV_BLOCK))  // blocks are counted in 31 bits
         return QMD_ERR_SHAPE;
     if (b->seqs < 1 || b->seqs > QMD_KV_MAX_SEQS || b->max_q < 1 || b->max_q > (1 << 20) || b->rows < 1 ||
         b->rows > (1 << 24) || b->table_stride < 1 || b->table_stride > (1 << 24))

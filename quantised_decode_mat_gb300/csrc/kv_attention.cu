@@ -48,6 +48,26 @@
 
 namespace qmd {
 
+// n / d for 0 <= n < 2^31 and a divisor that the host knows, by a product: floor(n m / 2^shift)
+// with m = ceil(2^shift / d), shift = 31 + ceil(log2 d) (an integer division is some 40 dependent
+// instructions, and there are a dozen before a warp's first load).
+struct FastDiv {
+    unsigned d, m, shift;
+};
+
+static FastDiv fast_div(unsigned d)
+{
+    unsigned l = 0;
+    while ((1ull << l) < d)
+        ++l;
+    return {d, (unsigned)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+}
+
+__device__ __forceinline__ int operator/(int n, const FastDiv &f)
+{
+    return (int)((uint64_t)(unsigned)n * f.m >> f.shift);
+}
+
 struct AttnArgs {
     KvParams kv;
     const float *q;
@@ -55,7 +75,8 @@ struct AttnArgs {
     float *part;     // workspace: [CTA][2][R][D] sums, then [CTA][2][R][2] maximum and weight sum
     unsigned *ctr;   // workspace: a counter per CTA
     int64_t q_stride, out_stride, window;
-    int q_heads, group;  // query heads; of them per key/value head
+    int group;  // query heads to a key/value head
+    FastDiv by_group, by_blocks;  // blocks of a page
     float scale_log2e;
 };
 
@@ -72,9 +93,9 @@ struct AttnCfg {
     static constexpr bool QS = R * D >= 1024;
     static constexpr int QBYTES = QS ? R * D * 4 : 0;  // two f16 parts
     static_assert(RING >= SLOT, "a warp's last part lies in its ring");
-    // rings, first parts, query fragments, maxima and sums of 2 W parts, jobs
-    static constexpr int FIXED = W * (RING + SLOT + QBYTES) + 2 * W * R * 8 + (W + 1) * 32;
-    static_assert(FIXED + 256 + (QMD_KV_MAX_SEQS + 1) * 8 <= 227 * 1024, "fits beside the sums of the most sequences");
+    // rings, first parts, query fragments, maxima and sums of 2 W parts and W + 1 joins, jobs
+    static constexpr int FIXED = W * (RING + SLOT + QBYTES) + (3 * W + 1) * R * 8 + (W + 1) * 32;
+    static_assert(FIXED + 256 + (QMD_KV_MAX_SEQS + 1) * 4 <= 227 * 1024, "fits beside the sums of the most sequences");
 };
 
 constexpr int ATT_MAX_ROWS_FLOATS = 16 * 128;  // the largest R x D of an instance (8 x 256 is the same)
@@ -153,10 +174,17 @@ __device__ __forceinline__ Group group_of(const AttnArgs &a, const KvSeq &q, int
 {
     Group g;
     g.rows = min(R, q.n * a.group - cg * R);
-    const int last = row_end(q, (cg * R + g.rows - 1) / a.group);
-    g.lo = row_begin(a, row_end(q, cg * R / a.group)) / KV_BLOCK;
+    const int last = row_end(q, (cg * R + g.rows - 1) / a.by_group);
+    g.lo = row_begin(a, row_end(q, cg * R / a.by_group)) / KV_BLOCK;
     g.hi = (last + KV_BLOCK - 1) / KV_BLOCK;
     return g;
+}
+
+// Query row r of a group that starts at query row `first`: its row of the call and its query head.
+__device__ __forceinline__ int64_t row_offset(const AttnArgs &a, int row0, int head, int r, int64_t stride, int dim)
+{
+    const int i = r / a.by_group;
+    return (int64_t)(row0 + i) * stride + (head * a.group + r - i * a.group) * dim;
 }
 
 struct Job {  // an item cut at the end of a warp's range
@@ -176,9 +204,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
     constexpr int VW = D / 32;   // words of a value row that a lane holds
     extern __shared__ __align__(16) unsigned char smem[];
     float2 *s_ml = reinterpret_cast<float2 *>(smem + W * (C::RING + C::SLOT + C::QBYTES));  // [W][2][R] maximum, weight sum
-    Job *s_job = reinterpret_cast<Job *>(s_ml + 2 * W * R);                      // [1 + W]
-    int64_t *s_pre = reinterpret_cast<int64_t *>(s_job + W + 1);                 // [seqs + 1] units before a sequence
-    __shared__ int64_t s_warp[W + 1];
+    Job *s_job = reinterpret_cast<Job *>(s_ml + (3 * W + 1) * R);                // [1 + W]
+    int *s_pre = reinterpret_cast<int *>(s_job + W + 1);                         // [seqs + 1] units before a sequence
+    __shared__ int64_t s_warp[W];
     __shared__ int s_last[2];
 
     pdl_launch_dependents();
@@ -193,53 +221,82 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
         if (warp == 0)
             s_job[0].rows = 0;
     }
-    int64_t before = 0;
-    for (int s0 = 0; s0 < p.seqs; s0 += W * 32) {
-        const int s = s0 + tid;
+    auto units_of = [&](const KvSeq &q) {
         int64_t u = 0;
-        if (s < p.seqs) {
-            const KvSeq q = kv_seq(p, s);
-            for (int cg = 0; cg * R < q.n * a.group; ++cg) {
-                const Group gr = group_of<R>(a, q, cg);
-                u += max(1, gr.hi - gr.lo);
-            }
-            u *= p.heads;
+        for (int cg = 0; cg * R < q.n * a.group; ++cg) {
+            const Group gr = group_of<R>(a, q, cg);
+            u += max(1, gr.hi - gr.lo);
         }
-        int64_t sum = u;
+        return u * p.heads;
+    };
+    // up to 32 sequences: every warp for itself, a lane a sequence; else through shared memory
+    const bool few = p.seqs <= 32;
+    KvSeq mine = {0, 0, 0};
+    int my_pre = 0, my_units = 0;
+    int64_t total = 0;
+    if (few) {
+        if (lane < p.seqs)
+            mine = kv_seq(p, lane);
+        my_units = (int)min(units_of(mine), (int64_t)INT_MAX / 32 + 1);
+        int sum = my_units;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+            const int x = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o)
                 sum += x;
         }
-        __syncthreads();
-        if (lane == 31)
-            s_warp[warp] = sum;
-        __syncthreads();
-        int64_t base = before, total = 0;
-        for (int w = 0; w < W; ++w) {
-            if (w < warp)
-                base += s_warp[w];
-            total += s_warp[w];
+        my_pre = sum - my_units;
+        total = __any_sync(0xffffffffu, my_units > INT_MAX / 32) ? INT64_MAX : __shfl_sync(0xffffffffu, sum, 31);
+    } else {
+        for (int s0 = 0; s0 < p.seqs; s0 += W * 32) {
+            const int s = s0 + tid;
+            const int64_t u = s < p.seqs ? units_of(kv_seq(p, s)) : 0;
+            int64_t sum = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o)
+                    sum += x;
+            }
+            __syncthreads();
+            if (lane == 31)
+                s_warp[warp] = sum;
+            __syncthreads();
+            int64_t base = total;
+            for (int w = 0; w < W; ++w) {
+                if (w < warp)
+                    base += s_warp[w];
+                total += s_warp[w];
+            }
+            if (s < p.seqs)
+                s_pre[s] = (int)(base + sum - u);
         }
-        if (s < p.seqs)
-            s_pre[s] = base + sum - u;
-        before += total;
     }
-    const int64_t units = before;
-    if (tid == 0)
-        s_pre[p.seqs] = units;
-    __syncthreads();
+    if (total > INT_MAX) {  // more blocks than a launch counts
+        kv_index_error(p);
+        return;
+    }
+    const int units = (int)total;
+    if (!few) {
+        if (tid == 0)
+            s_pre[p.seqs] = units;
+        __syncthreads();
+    }
+    auto seq_at = [&](int s) {
+        if (!few)
+            return kv_seq(p, s);
+        const KvSeq q = {__shfl_sync(0xffffffffu, mine.row0, s), __shfl_sync(0xffffffffu, mine.n, s),
+                         __shfl_sync(0xffffffffu, mine.len, s)};
+        return q;
+    };
 
     // ---- this CTA's range, this warp's range ---------------------------------------------------
     // at least a unit for every warp, so that short items are cut inside a CTA, not between CTAs
-    int64_t per = (units + gridDim.x - 1) / gridDim.x;
-    if (per < W)
-        per = W;
-    const int64_t u0 = (int64_t)blockIdx.x * per, u1 = min(units, u0 + per);
-    if (u0 >= units)
+    const int per = max(W, (int)(((unsigned)units + gridDim.x - 1) / gridDim.x));
+    if ((int64_t)blockIdx.x * per >= units)
         return;
-    const int span = (int)(u1 - u0), pw = (span + W - 1) / W;
+    const int u0 = blockIdx.x * per;
+    const int span = min(units - u0, per), pw = (span + W - 1) / W;
     int u = warp * pw;  // from here on counted from u0
     const int w1 = min(span, u + pw);
 
@@ -249,31 +306,38 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
 
     int s = 0, cg = 0, head = 0, b0 = 0;  // the item of unit u, and the unit's block in it
     if (u < w1) {
-        const int64_t at = u0 + u;
-        int lo = 0, hi = p.seqs;  // s_pre[lo] <= at < s_pre[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s_pre[mid] <= at)
-                lo = mid;
-            else
-                hi = mid;
+        const int at = u0 + u;
+        int pre;
+        if (few) {
+            s = 31 - __clz(__ballot_sync(0xffffffffu, my_units > 0 && my_pre <= at));
+            pre = __shfl_sync(0xffffffffu, my_pre, s);
+        } else {
+            int lo = 0, hi = p.seqs;  // s_pre[lo] <= at < s_pre[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_pre[mid] <= at)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            s = lo;
+            pre = s_pre[s];
         }
-        s = lo;
-        int64_t rem = at - s_pre[s];
-        const KvSeq sq = kv_seq(p, s);
+        int rem = at - pre;
+        const KvSeq sq = seq_at(s);
         int nb;
         for (;; ++cg) {
             const Group gr = group_of<R>(a, sq, cg);
             nb = max(1, gr.hi - gr.lo);
-            if (rem < (int64_t)p.heads * nb)
+            if (rem < p.heads * nb)
                 break;
-            rem -= (int64_t)p.heads * nb;
+            rem -= p.heads * nb;
         }
-        head = (int)(rem / nb);
-        b0 = (int)(rem % nb);
+        head = rem / nb;
+        b0 = rem - head * nb;
     }
     while (u < w1) {
-        const KvSeq sq = kv_seq(p, s);
+        const KvSeq sq = seq_at(s);
         const Group gr = group_of<R>(a, sq, cg);
         const int nb = max(1, gr.hi - gr.lo);
         const int cnt = min(nb - b0, w1 - u);              // units of this item in the range
@@ -282,7 +346,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
         // pages and scales, 32 blocks at a time: block index in the pool, or -1
         const int first_blk = gr.lo + b0;
         auto page_of = [&](int i) -> int {  // of the item's i-th block here; INT_MIN past the end
-            return i < real ? p.table[(int64_t)s * p.table_stride + (first_blk + i) / p.page_blocks] : INT_MIN;
+            return i < real ? p.table[(int64_t)s * p.table_stride + (first_blk + i) / a.by_blocks] : INT_MIN;
         };
         auto block_of = [&](int i, int page) -> int {
             if (page < 0 || page >= p.pages) {
@@ -290,15 +354,25 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
                     kv_index_error(p);
                 return -1;
             }
-            return (page * p.heads + head) * p.page_blocks + (first_blk + i) % p.page_blocks;
+            const int blk = first_blk + i;
+            return (page * p.heads + head - blk / a.by_blocks) * p.page_blocks + blk;
         };
-        int bi_c = block_of(lane, page_of(lane)), bi_n = -1, page_nn = INT_MIN;
-        float ks_c = bi_c >= 0 ? p.ks[bi_c] : 0.0f, vs_c = bi_c >= 0 ? p.vs[bi_c] : 0.0f, ks_n = 0.0f, vs_n = 0.0f;
-        if (real > 32) {
-            bi_n = block_of(32 + lane, page_of(32 + lane));
-            ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
-            page_nn = page_of(64 + lane);
-        }
+        const int page_c = page_of(lane), page_n = page_of(32 + lane);
+        int page_nn = page_of(64 + lane);
+        // lane (g, t) holds columns g of the query tiles, dimensions 64 h + 16 t + 0..15; a column past
+        // the rows repeats the last one
+        float x[KH][16];
+        auto load_q = [&](int nt) {
+            const int r = cg * R + min(4 * nt + (g >> 1), gr.rows - 1);
+            const float *qp = a.q + row_offset(a, sq.row0, head, r, a.q_stride, D) + 16 * t;
+#pragma unroll
+            for (int h = 0; h < KH; ++h)
+                load_f32(x[h], qp + 64 * h);
+        };
+        load_q(0);
+        int bi_c = block_of(lane, page_c), bi_n = block_of(32 + lane, page_n);
+        float ks_c = bi_c >= 0 ? p.ks[bi_c] : 0.0f, vs_c = bi_c >= 0 ? p.vs[bi_c] : 0.0f;
+        float ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
 
         auto issue = [&](int j, int idx) {  // copy the item's j-th block into its ring stage
             if (j < real) {
@@ -331,24 +405,19 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
         for (int j = 0; j < S - 1; ++j)
             issue(j, 0);
 
-        // ---- the queries: lane (g, t) holds columns g of the tiles, dimensions 64 h + 16 t + 0..15
+        // ---- the queries as two f16 parts ------------------------------------------------------
         uint32_t qf[C::QS ? 1 : NT][KH * 4][2];
         float qscale[NT];  // of query row 4 nt + t
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = 4 * nt + (g >> 1);
-            const int rr = cg * R + min(r, gr.rows - 1);  // a column past the rows repeats the last one
-            const float *qp = a.q + (int64_t)(sq.row0 + rr / a.group) * a.q_stride +
-                              (head * a.group + rr % a.group) * D + 16 * t;
-            float x[KH][16];
+            if (nt > 0)
+                load_q(nt);
             float top = 0.0f;
 #pragma unroll
-            for (int h = 0; h < KH; ++h) {
-                load_f32(x[h], qp + 64 * h);
+            for (int h = 0; h < KH; ++h)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     top = fmaxf(top, fabsf(x[h][e]));
-            }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // q times a power of two, the largest value in [0.5, 1)
@@ -375,8 +444,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
             qscale[nt] = __shfl_sync(0xffffffffu, back, 8 * t);
         }
         // positions in [all_from, all_to) are seen by every row of the group
-        const int all_to = row_end(sq, cg * R / a.group);
-        const int all_from = row_begin(a, row_end(sq, (cg * R + gr.rows - 1) / a.group));
+        const int all_to = row_end(sq, cg * R / a.by_group);
+        const int all_from = row_begin(a, row_end(sq, (cg * R + gr.rows - 1) / a.by_group));
 
         float o[NT][MT][4];
         float m[NT], l[NT];
@@ -448,7 +517,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
                 sc[nt][0] = fmaf(c[nt][1], LOW_PART, c[nt][0]) * f;
                 sc[nt][1] = fmaf(c[nt][3], LOW_PART, c[nt][2]) * f;
                 if (!whole) {
-                    const int end = row_end(sq, (cg * R + min(4 * nt + t, gr.rows - 1)) / a.group);
+                    const int end = row_end(sq, (cg * R + min(4 * nt + t, gr.rows - 1)) / a.by_group);
                     const int begin = row_begin(a, end), j = pos + g;
                     if (bi < 0 || j < begin || j >= end)
                         sc[nt][0] = -INFINITY;
@@ -553,10 +622,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
                 if (g == 0)
                     s_ml[(warp * 2 + part) * R + r] = make_float2(m[nt], l[nt]);
             } else if (r < gr.rows) {
-                const int rr = cg * R + r;
-                store_f32(a.out + (int64_t)(sq.row0 + rr / a.group) * a.out_stride +
-                              (head * a.group + rr % a.group) * D + 2 * MT * g,
-                          y);
+                store_f32(a.out + row_offset(a, sq.row0, head, cg * R + r, a.out_stride, D) + 2 * MT * g, y);
             }
         }
         // the item's first cut in this CTA makes the job of joining it
@@ -575,101 +641,179 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
             head = 0;
             if (++cg * R >= sq.n * a.group) {
                 cg = 0;
-                do
-                    ++s;
-                while (s_pre[s + 1] == s_pre[s]);
+                if (few) {
+                    s = __ffs(__ballot_sync(0xffffffffu, my_units > 0) & ~((2u << s) - 1)) - 1;
+                } else {
+                    do
+                        ++s;
+                    while (s_pre[s + 1] == s_pre[s]);
+                }
             }
         }
     }
     __syncthreads();
 
     // ---- joins inside the CTA -------------------------------------------------------------------
+    // Job 0 is the item that began before the CTA's range (parts 0 of warps 0 ..), job 1 + w the one
+    // that warp w's range cut (its part 1, parts 0 of the warps after it).
+    float2 *s_tot = s_ml + 2 * W * R;  // [1 + W][R] a job's maximum and weight sum
     const int64_t part_ml = (int64_t)gridDim.x * 2 * R * D;
-    auto write_out = [&](const Job &j, int r, int d, float y) {
-        const int rr = j.first + r;
-        a.out[(int64_t)(j.row0 + rr / a.group) * a.out_stride + (j.head * a.group + rr % a.group) * D + d] = y;
-    };
+    const unsigned live = __ballot_sync(0xffffffffu, lane <= W && s_job[lane <= W ? lane : 0].rows > 0);
+    if (live == 0)
+        return;
+    // the parts' factors: 16 lanes to a job's row, a lane to a part
+    for (int i = tid >> 4; i < (W + 1) * R; i += 2 * W) {
+        const int jj = i / R, r = i % R, k = tid & 15;
+        const unsigned half = 0xffffu << (tid & 16);
+        if (live >> jj & 1) {
+            const int wa = max(0, jj - 1), wb = (min(s_job[jj].end, span) - 1) / pw;
+            const int at = ((wa + k) * 2 + (k == 0 && jj > 0)) * R + r;
+            const float2 ml = wa + k <= wb ? s_ml[at] : make_float2(ATT_NONE, 0.0f);
+            float M = ml.x;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(half, M, o));
+            const float f = ex2(ml.x - M);
+            float L = ml.y * f;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1)
+                L += __shfl_xor_sync(half, L, o);
+            if (wa + k <= wb)
+                s_ml[at].x = f;
+            if (k == 0)
+                s_tot[jj * R + r] = make_float2(M, L);
+        }
+    }
+    __syncthreads();
     bool cut = false;  // some item goes on in another CTA
-    for (int jj = 0; jj <= W; ++jj) {
-        const Job j = s_job[jj];
-        if (j.rows == 0)
-            continue;
-        const bool whole = j.start >= 0 && j.end <= span;
-        const int wa = jj == 0 ? 0 : jj - 1;
-        const int wb = (min(j.end, span) - 1) / pw;
-        cut |= !whole;
-        for (int e = tid; e < j.rows * D; e += W * 32) {
-            const int r = e / D, d = e % D;
-            float M = ATT_NONE, L = 0.0f, y = 0.0f;
-            for (int w = wa; w <= wb; ++w)
-                M = fmaxf(M, s_ml[(w * 2 + (w == wa && jj > 0)) * R + r].x);
+    int tail = -1;     // the item that goes on after this CTA's range
+    {
+        constexpr int EL = R * D / 4;  // 4 neighbouring values to a thread
+        const int njobs = __popc(live);
+        unsigned left = live;
+        int jj = -1, seen = 0;
+        for (int e = tid; e < njobs * EL; e += W * 32) {
+            while (seen <= e / EL) {
+                jj = __ffs(left) - 1;
+                left &= left - 1;
+                ++seen;
+            }
+            const int r = e % EL / (D / 4), d = e % (D / 4) * 4;
+            const int start = s_job[jj].start, end = s_job[jj].end;
+            const int wa = max(0, jj - 1), wb = (min(end, span) - 1) / pw;
+            if (r >= s_job[jj].rows)
+                continue;
+            float y[4] = {};
             for (int w = wa; w <= wb; ++w) {
                 const bool one = w == wa && jj > 0;
-                const float2 ml = s_ml[(w * 2 + one) * R + r];
-                const float f = ex2(ml.x - M);
-                const float *src = reinterpret_cast<const float *>(one ? smem + w * C::RING
-                                                                       : smem + W * C::RING + w * C::SLOT);
-                L = fmaf(ml.y, f, L);
-                y = fmaf(src[r * D + d], f, y);
+                const float f = s_ml[(w * 2 + one) * R + r].x;
+                float v[4];
+                load_f32(v, reinterpret_cast<const float *>(one ? smem + w * C::RING : smem + W * C::RING + w * C::SLOT) +
+                                r * D + d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    y[i] = fmaf(v[i], f, y[i]);
             }
-            if (whole) {
-                write_out(j, r, d, L == 0.0f ? 0.0f : y / L);
+            const float2 tot = s_tot[jj * R + r];
+            if (start >= 0 && end <= span) {
+                const float f = tot.y == 0.0f ? 0.0f : 1.0f / tot.y;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    y[i] *= f;
+                store_f32(a.out + row_offset(a, s_job[jj].row0, s_job[jj].head, s_job[jj].first + r, a.out_stride, D) + d, y);
             } else {
-                const int64_t at = ((int64_t)blockIdx.x * 2 + (j.start < 0 ? 0 : 1)) * R + r;
-                a.part[at * D + d] = y;
+                const int64_t at = ((int64_t)blockIdx.x * 2 + (start < 0 ? 0 : 1)) * R + r;
+                store_f32(a.part + at * D + d, y);
                 if (d == 0)
-                    reinterpret_cast<float2 *>(a.part + part_ml)[at] = make_float2(M, L);
+                    reinterpret_cast<float2 *>(a.part + part_ml)[at] = tot;
             }
         }
+        for (unsigned x = live; x; x &= x - 1) {
+            const int i = __ffs(x) - 1;
+            if (s_job[i].end > span)
+                tail = i;
+        }
+        cut = (live & 1) || tail >= 0;
     }
     if (!cut)
         return;
 
     // ---- joins between CTAs: the one that comes last adds the parts, in their order ---------------
-    __threadfence();
+    // At most two items are cut: job 0, and the tail.
     __syncthreads();
-    // at most two items are cut: the one that began before this CTA's range (job 0), and the one
-    // that goes on after it (the job with the largest end)
-    int tail = -1;
-    for (int jj = 0; jj <= W; ++jj)
-        if (s_job[jj].rows > 0 && s_job[jj].end > span)
-            tail = jj;
-    const int jobs[2] = {s_job[0].rows > 0 ? 0 : -1, tail == 0 ? -1 : tail};
     if (tid < 2) {
+        const int jj = tid == 0 ? ((live & 1) ? 0 : -1) : tail == 0 ? -1 : tail;
         int last = 0;
-        if (jobs[tid] >= 0) {
-            const Job &j = s_job[jobs[tid]];
-            const int c0 = (int)((u0 + j.start) / per), c1 = (int)((u0 + j.end - 1) / per);
+        if (jj >= 0) {
+            const int c0 = (u0 + s_job[jj].start) / per, c1 = (u0 + s_job[jj].end - 1) / per;
+            __threadfence();
             last = atomicAdd(a.ctr + c0, 1u) == (unsigned)(c1 - c0);
             if (last)
                 a.ctr[c0] = 0;  // every part has come: left as it was found
+            __threadfence();
         }
-        s_last[tid] = last;
+        s_last[tid] = last ? jj + 1 : 0;
     }
     __syncthreads();
+    constexpr int EL = R * D / 4, NG = W * 32 / EL > 0 ? W * 32 / EL : 1;  // groups of threads share the parts
+    float *s_f = reinterpret_cast<float *>(smem);  // [parts][R] factors
+    float4 *s_y = reinterpret_cast<float4 *>(smem + (size_t)gridDim.x * R * 4);  // [NG][EL]
     for (int x = 0; x < 2; ++x) {
         if (!s_last[x])
             continue;
-        __threadfence();
-        const Job j = s_job[jobs[x]];
-        const int c0 = (int)((u0 + j.start) / per), c1 = (int)((u0 + j.end - 1) / per);
+        const Job j = s_job[s_last[x] - 1];
+        const int c0 = (u0 + j.start) / per, parts = (u0 + j.end - 1) / per - c0 + 1;
         const float2 *ml = reinterpret_cast<const float2 *>(a.part + part_ml);
-        for (int e = tid; e < j.rows * D; e += W * 32) {
-            const int r = e / D, d = e % D;
-            float M = ATT_NONE, L = 0.0f, y = 0.0f;
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c)
-                M = fmaxf(M, __ldcg(&ml[((int64_t)c * 2 + (c == c0)) * R + r]).x);
-#pragma unroll 4
-            for (int c = c0; c <= c1; ++c) {
-                const int64_t at = ((int64_t)c * 2 + (c == c0)) * R + r;
-                const float2 v = __ldcg(&ml[at]);
+        // part i lies with CTA c0 + i, as its part 1 if the item began there
+        for (int r = warp; r < j.rows; r += W) {
+            float M = ATT_NONE, L = 0.0f;
+            for (int i = lane; i < parts; i += 32)
+                M = fmaxf(M, __ldcg(&ml[((int64_t)(c0 + i) * 2 + (i == 0)) * R + r]).x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+            for (int i = lane; i < parts; i += 32) {
+                const float2 v = __ldcg(&ml[((int64_t)(c0 + i) * 2 + (i == 0)) * R + r]);
                 const float f = ex2(v.x - M);
+                s_f[i * R + r] = f;
                 L = fmaf(v.y, f, L);
-                y = fmaf(__ldcg(&a.part[at * D + d]), f, y);
             }
-            write_out(j, r, d, L == 0.0f ? 0.0f : y / L);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                L += __shfl_xor_sync(0xffffffffu, L, o);
+            if (lane == 0)
+                s_tot[r].y = L;
         }
+        __syncthreads();
+        for (int e = tid; e < NG * EL; e += W * 32) {
+            const int n = e / EL, r = e % EL / (D / 4);
+            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (r < j.rows)
+#pragma unroll 8
+                for (int i = n; i < parts; i += NG) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(
+                                                a.part + ((int64_t)(c0 + i) * 2 + (i == 0)) * R * D) + e % EL);
+                    const float f = s_f[i * R + r];
+                    y.x = fmaf(v.x, f, y.x), y.y = fmaf(v.y, f, y.y), y.z = fmaf(v.z, f, y.z), y.w = fmaf(v.w, f, y.w);
+                }
+            s_y[e] = y;
+        }
+        __syncthreads();
+        for (int e = tid; e < EL; e += W * 32) {
+            const int r = e / (D / 4), d = e % (D / 4) * 4;
+            if (r >= j.rows)
+                continue;
+            float4 y = s_y[e];
+#pragma unroll
+            for (int n = 1; n < NG; ++n) {
+                const float4 v = s_y[n * EL + e];
+                y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+            }
+            const float f = s_tot[r].y == 0.0f ? 0.0f : 1.0f / s_tot[r].y;
+            *reinterpret_cast<float4 *>(a.out + row_offset(a, j.row0, j.head, j.first + r, a.out_stride, D) + d) =
+                make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+        }
+        __syncthreads();
     }
 }
 
@@ -677,7 +821,7 @@ template <int D, int NT>
 static qmd_status launch_att(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s)
 {
     using C = AttnCfg<D, NT>;
-    const size_t smem = C::FIXED + ((size_t)a.kv.seqs + 1) * sizeof(int64_t);
+    const size_t smem = C::FIXED + ((size_t)a.kv.seqs + 1) * sizeof(int);
     if (smem + 256 > (size_t)dev.smem_optin)
         return QMD_ERR_SHAPE;
     {
@@ -719,7 +863,8 @@ qmd_status launch_kv_attention(const KvParams &kv, int head_dim, const float *q,
                                const DeviceInfo &dev, cudaStream_t s)
 {
     const AttnArgs a = {kv, q, out, reinterpret_cast<float *>(static_cast<char *>(ws) + counter_bytes(dev)),
-                        static_cast<unsigned *>(ws), q_stride, out_stride, window, q_heads, q_heads / kv.heads,
+                        static_cast<unsigned *>(ws), q_stride, out_stride, window, q_heads / kv.heads,
+                        fast_div((unsigned)(q_heads / kv.heads)), fast_div((unsigned)kv.page_blocks),
                         scale * 1.4426950408889634f};
     // rows per item: the least of 4, 8, 16 that holds a sequence's rows of one key/value head
     const int64_t rows = (int64_t)a.group * kv.max_q;
