@@ -49,7 +49,7 @@ extern "C" {
 #define QMD_Q6K_BODY_BYTES 208
 #define QMD_WORKSPACE_BYTES 4096 /* scheduling workspace of qmd_qmatvec_ws / qmd_qmatvec_x_ws */
 #define QMD_KV_BLOCK 16          /* tokens of one head that share a scale in the key/value cache */
-#define QMD_KV_MAX_SEQS 4096     /* sequences per key/value call */
+#define QMD_KV_MAX_SEQS 2048     /* sequences per key/value call */
 #define QMD_LORA_MAX_RANK 128
 
 typedef enum qmd_status {

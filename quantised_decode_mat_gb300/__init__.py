@@ -278,38 +278,54 @@ def _need(ok: bool, status: int, detail: str) -> None:
         raise QmdError(status, detail)
 
 
-def _on_current_device(t, what: str) -> None:
+def _stream_on(stream, t, what: str) -> int:
+    """The stream of a call on tensor t's device, which has to be the current one."""
     import torch
-    _need(t.is_cuda and t.device.index == torch.cuda.current_device(), 9,
-          f"{what} must be on the current CUDA device")
+    index = t.get_device()
+    if index < 0 or index != torch._C._cuda_getDevice():
+        raise QmdError(9, f"{what} must be on the current CUDA device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _array(t, dtype, shape, device, what: str) -> None:
-    """A contiguous tensor of this type and shape (None: any extent) on this device."""
-    _need(t.dtype == dtype, 2, f"{what}: {dtype} is wanted, got {t.dtype}")
-    _need(t.dim() == len(shape) and all(w is None or n == w for n, w in zip(t.shape, shape)), 6,
-          f"{what}: shape {tuple(shape)} is wanted, got {tuple(t.shape)}")
-    _need(t.is_contiguous(), 6, f"{what} must be contiguous")
-    _need(t.device == device, 9, f"{what} is on {t.device}, not on {device}")
+# The checks below run on every call of a decode step's small operators: messages are made only for
+# a refusal.
+def _array(t, dtype, shape, device, what: str) -> int:
+    """The address of a contiguous tensor of this type and shape (None: any extent) on this device."""
+    if t.dtype is not dtype:
+        raise QmdError(2, f"{what}: {dtype} is wanted, got {t.dtype}")
+    if t.shape != shape and (t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape))):
+        raise QmdError(6, f"{what}: shape {tuple(shape)} is wanted, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise QmdError(6, f"{what} must be contiguous")
+    if t.device != device:
+        raise QmdError(9, f"{what} is on {t.device}, not on {device}")
+    return t.data_ptr()
 
 
 def _rows_of(t, rows: int, heads: int | None, dim: int, device, what: str) -> tuple[int, int]:
     """(heads, row stride) of f32 rows [rows or more, heads, dim] or [rows or more, heads * dim],
     strided by rows only."""
     import torch
-    _need(t.dtype == torch.float32, 2, f"{what}: float32 is wanted, got {t.dtype}")
-    _need(t.device == device, 9, f"{what} is on {t.device}, not on {device}")
+    if t.dtype is not torch.float32:
+        raise QmdError(2, f"{what}: float32 is wanted, got {t.dtype}")
+    if t.device != device:
+        raise QmdError(9, f"{what} is on {t.device}, not on {device}")
     shape, stride = t.shape, t.stride()
     if len(shape) == 3:
-        width = shape[1] * shape[2]
-        ok = shape[2] == dim and stride[2] == 1 and (stride[1] == dim or shape[1] == 1)
+        n, h, d = shape
+        width = h * d
+        ok = d == dim and stride[2] == 1 and (stride[1] == dim or h == 1)
+    elif len(shape) == 2:
+        n, width = shape
+        ok = width % dim == 0 and stride[1] == 1
     else:
-        width = shape[1] if len(shape) == 2 else 0
-        ok = len(shape) == 2 and width % dim == 0 and stride[1] == 1
-    _need(ok and width > 0 and shape[0] >= rows and (heads is None or width == heads * dim), 6,
-          f"{what}: {rows} or more rows of {heads or 'some'} heads of {dim} values are wanted, strided by rows only; "
-          f"got shape {tuple(shape)}, strides {tuple(stride)}")
-    return width // dim, stride[0] if shape[0] > 1 else (width + 3) // 4 * 4
+        ok = False
+    if not ok or width == 0 or n < rows or (heads is not None and width != heads * dim):
+        raise QmdError(6, f"{what}: {rows} or more rows of {heads or 'some'} heads of {dim} values are wanted, "
+                          f"strided by rows only; got shape {tuple(shape)}, strides {tuple(stride)}")
+    return width // dim, stride[0] if n > 1 else (width + 3) // 4 * 4
 
 
 class KVCache:
@@ -356,9 +372,10 @@ class KVBatch:
         self.ptrs = KVBatchPtrs(_ptr(page_table), _ptr(kv_len), _ptr(q_start), page_table.shape[1], self.rows, seqs, max_q)
 
 
-def _kv_devices(cache: KVCache, batch: KVBatch) -> None:
-    _on_current_device(cache.k, "the cache")
-    _need(batch.device == cache.device, 9, f"the batch is on {batch.device}, the cache on {cache.device}")
+def _kv_stream(cache: KVCache, batch: KVBatch, stream) -> int:
+    if batch.device != cache.device:
+        raise QmdError(9, f"the batch is on {batch.device}, the cache on {cache.device}")
+    return _stream_on(stream, cache.k, "the cache")
 
 
 def rope_table(positions: int, rot: int, base: float = 10000.0, inv_freq=None, device="cuda"):
@@ -380,7 +397,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, rope=None, q=None, q_out=Non
     without q).  k, v f32 [rows, kv_heads, head_dim], q f32 [rows, heads, head_dim], strided by rows
     only (parts of one fused projection's output); q_out may be q."""
     import torch
-    _kv_devices(cache, batch)
+    st = _kv_stream(cache, batch, stream)
     D, dev, T = cache.head_dim, cache.device, batch.rows
     _, ks = _rows_of(k, T, cache.kv_heads, D, dev, "k")
     _, vs = _rows_of(v, T, cache.kv_heads, D, dev, "v")
@@ -394,8 +411,8 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, rope=None, q=None, q_out=Non
     if rope is not None:
         _array(rope, torch.float32, (None, None), dev, "rope")
         n, rot = rope.shape
-    _check(lib().qmd_kv_append(cache.ptrs, batch.ptrs, _ptr(k), ks, _ptr(v), vs, _ptr(q), qs, heads, _ptr(q_out), os_,
-                               _ptr(rope), n, rot, pairs, _stream(stream)))
+    _check(lib().qmd_kv_append(cache.ptrs, batch.ptrs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, heads,
+                               _ptr(q_out), os_, _ptr(rope), n, rot, pairs, st))
     return q_out
 
 
@@ -403,7 +420,7 @@ def kv_read(cache: KVCache, batch: KVBatch, k_out=None, v_out=None, stream=None)
     """qmd_kv_read: the rows' keys and values as the cache holds them, code * scale, f32
     [rows, kv_heads, head_dim] each (new tensors by default)."""
     import torch
-    _kv_devices(cache, batch)
+    st = _kv_stream(cache, batch, stream)
     H, D, dev, T = cache.kv_heads, cache.head_dim, cache.device, batch.rows
     if k_out is None:
         k_out = torch.empty((T, H, D), dtype=torch.float32, device=dev)
@@ -411,7 +428,7 @@ def kv_read(cache: KVCache, batch: KVBatch, k_out=None, v_out=None, stream=None)
         v_out = torch.empty((T, H, D), dtype=torch.float32, device=dev)
     _, ks = _rows_of(k_out, T, H, D, dev, "k_out")
     _, vs = _rows_of(v_out, T, H, D, dev, "v_out")
-    _check(lib().qmd_kv_read(cache.ptrs, batch.ptrs, _ptr(k_out), ks, _ptr(v_out), vs, _stream(stream)))
+    _check(lib().qmd_kv_read(cache.ptrs, batch.ptrs, k_out.data_ptr(), ks, v_out.data_ptr(), vs, st))
     return k_out, v_out
 
 
@@ -429,16 +446,15 @@ def kv_attention(cache: KVCache, batch: KVBatch, q, scale: float, workspace, win
     by rows only) over the cached keys and values of their sequences.  out f32, by default
     [rows, heads * head_dim]; rows that no sequence owns are not written."""
     import torch
-    _kv_devices(cache, batch)
+    st = _kv_stream(cache, batch, stream)
     D, dev, T = cache.head_dim, cache.device, batch.rows
     heads, qs = _rows_of(q, T, None, D, dev, "q")
     if out is None:
         out = torch.empty((T, heads * D), dtype=torch.float32, device=dev)
     _, os_ = _rows_of(out, T, heads, D, dev, "out")
-    _array(workspace, torch.int32, (None,), dev, "workspace")
-    _need(workspace.numel() * 4 >= lib().qmd_kv_workspace_bytes(), 6, "the workspace is too small")
-    _check(lib().qmd_kv_attention(cache.ptrs, batch.ptrs, _ptr(q), qs, heads, float(scale), int(window), _ptr(out), os_,
-                                  _ptr(workspace), _stream(stream)))
+    L = lib()
+    ws = _array(workspace, torch.int32, (L.qmd_kv_workspace_bytes() // 4,), dev, "workspace")
+    _check(L.qmd_kv_attention(cache.ptrs, batch.ptrs, q.data_ptr(), qs, heads, scale, window, out.data_ptr(), os_, ws, st))
     return out
 
 
@@ -447,23 +463,24 @@ def lora_add(x, base, A, B, adapter, scale, out=None, stream=None):
     where a < 0.  x f32 [batch, K]; base, out f32 [batch, rows] (out may be base); A f16 or bf16
     [adapters, rank, K], B [adapters, rows, rank]; adapter int32 [batch]; scale f32 [adapters]."""
     import torch
-    _on_current_device(x, "x")
+    st = _stream_on(stream, x, "x")
     dev = x.device
-    _need(A.dtype in (torch.float16, torch.bfloat16), 2, f"A: float16 or bfloat16 is wanted, got {A.dtype}")
-    _need(A.dim() == 3 and x.dim() == 2 and base.dim() == 2, 6,
-          "x [batch, K], base [batch, rows] and A [adapters, rank, K] are wanted")
+    if A.dtype is torch.float16:
+        half = F16
+    elif A.dtype is torch.bfloat16:
+        half = BF16
+    else:
+        raise QmdError(2, f"A: float16 or bfloat16 is wanted, got {A.dtype}")
+    if A.dim() != 3 or x.dim() != 2 or base.dim() != 2:
+        raise QmdError(6, "x [batch, K], base [batch, rows] and A [adapters, rank, K] are wanted")
     (n, rank, K), batch, rows = A.shape, x.shape[0], base.shape[1]
-    _array(x, torch.float32, (batch, K), dev, "x")
-    _array(base, torch.float32, (batch, rows), dev, "base")
-    _array(A, A.dtype, (n, rank, K), dev, "A")
-    _array(B, A.dtype, (n, rows, rank), dev, "B")
-    _array(scale, torch.float32, (n,), dev, "scale")
-    _array(adapter, torch.int32, (batch,), dev, "adapter")
     if out is None:
         out = torch.empty((batch, rows), dtype=torch.float32, device=dev)
-    _array(out, torch.float32, (batch, rows), dev, "out")
-    _check(lib().qmd_lora_add(F16 if A.dtype == torch.float16 else BF16, _ptr(x), _ptr(base), _ptr(A), _ptr(B),
-                              _ptr(scale), _ptr(adapter), _ptr(out), K, rows, rank, n, batch, _stream(stream)))
+    f32 = torch.float32
+    _check(lib().qmd_lora_add(half, _array(x, f32, (batch, K), dev, "x"), _array(base, f32, (batch, rows), dev, "base"),
+                              _array(A, A.dtype, (n, rank, K), dev, "A"), _array(B, A.dtype, (n, rows, rank), dev, "B"),
+                              _array(scale, f32, (n,), dev, "scale"), _array(adapter, torch.int32, (batch,), dev, "adapter"),
+                              _array(out, f32, (batch, rows), dev, "out"), K, rows, rank, n, batch, st))
     return out
 
 

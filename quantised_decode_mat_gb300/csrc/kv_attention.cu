@@ -32,11 +32,13 @@
 // enters the weights relative to a running power of two at or above every scale so far, so the f16
 // parts neither overflow nor lose bits that the sum keeps.
 //
-// Loads: each lane copies its own 16-byte pieces (cp.async) into its own places of a ring of STAGES
-// blocks per warp in shared memory: no bank conflicts, no barriers, 4 KB a block (head_dim 128) and
-// warp in flight.  Page numbers and scales are looked up 32 blocks at a time, a lane each, a chunk
-// ahead.
+// Loads: a lane asks for each block's keys and values by tiled tensor copies (TMA) into a ring of
+// STAGES blocks per warp in shared memory, 4 KB a block (head_dim 128), an mbarrier to a stage.  The
+// copies swizzle the rows' 16-byte pieces, and rows are dealt to lanes so that the eight lanes that
+// read shared memory together meet eight different pieces: no bank conflicts.  Page numbers and
+// scales are looked up 32 blocks at a time, a lane each, a chunk ahead.
 #include <climits>
+#include <cstring>
 #include <mutex>
 
 #include <cuda_fp16.h>
@@ -45,6 +47,7 @@
 #include "internal.h"
 #include "kv.cuh"
 #include "ptx.cuh"
+#include "tensor_map.h"
 
 namespace qmd {
 
@@ -75,6 +78,7 @@ struct AttnArgs {
     float *part;     // workspace: [CTA][2][R][D] sums, then [CTA][2][R][2] maximum and weight sum
     unsigned *ctr;   // workspace: a counter per CTA
     int64_t q_stride, out_stride, window;
+    uint64_t wait_ns;
     int group;  // query heads to a key/value head
     FastDiv by_group, by_blocks;  // blocks of a page
     float scale_log2e;
@@ -84,38 +88,28 @@ struct AttnArgs {
 template <int D, int NT>
 struct AttnCfg {
     static constexpr int R = 4 * NT;
-    static constexpr int W = D == 256 ? (NT == 1 ? 8 : 6) : D * NT <= 128 ? 16 : NT <= 2 ? 12 : 8;
-    static constexpr int STAGES = 2;
+    static constexpr int W = D == 256 ? (NT == 1 ? 6 : 5) : NT == 1 ? 14 : NT == 2 ? (D == 64 ? 12 : 10) : 7;
+    static constexpr int STAGES = 3;
+    static constexpr int META = 64 * 16;  // block index and scales of two chunks of 32 blocks
+    static constexpr int BOX = D < 128 ? D : 128;  // bytes of a row that one copy takes
+    static constexpr int TILE = 16 * BOX;          // a copy: BOX bytes of 16 rows
     static constexpr int BLOCK_BYTES = 32 * D;  // keys and values of 16 positions
     static constexpr int RING = STAGES * BLOCK_BYTES;
     static constexpr int SLOT = R * D * 4;
     // query fragments stay in registers until the sums alone take 64 of them
+    static constexpr bool PIPE = NT <= 2;
     static constexpr bool QS = R * D >= 1024;
     static constexpr int QBYTES = QS ? R * D * 4 : 0;  // two f16 parts
     static_assert(RING >= SLOT, "a warp's last part lies in its ring");
-    // rings, first parts, query fragments, maxima and sums of 2 W parts and W + 1 joins, jobs
-    static constexpr int FIXED = W * (RING + SLOT + QBYTES) + (3 * W + 1) * R * 8 + (W + 1) * 32;
+    // rings, first parts, query fragments, maxima and sums of 2 W parts and W + 1 joins, jobs,
+    // barriers, scans
+    static constexpr int FIXED = W * (RING + SLOT + QBYTES + META) + (3 * W + 1) * R * 8 + (W + 1) * 32 + W * (STAGES + 1) * 8 + 8;
     static_assert(FIXED + 256 + (QMD_KV_MAX_SEQS + 1) * 4 <= 227 * 1024, "fits beside the sums of the most sequences");
 };
 
 constexpr int ATT_MAX_ROWS_FLOATS = 16 * 128;  // the largest R x D of an instance (8 x 256 is the same)
 constexpr float ATT_NONE = -3.0e38f;           // the maximum before any score
 constexpr float ATT_SLACK = 8.0f;              // how far (log2) a score may pass the running maximum
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -148,12 +142,15 @@ __device__ __forceinline__ uint32_t codes_f16(uint32_t w)
     return *reinterpret_cast<const uint32_t *>(&c);
 }
 
-// x as two f16: the first 11 bits, and the rest 2^11 times larger.
-__device__ __forceinline__ uint32_t split_f16(float x)
+// x and y as two f16 each: the first 11 bits, and the rest 2^11 times larger (in the upper half).
+__device__ __forceinline__ void split_f16(float x, float y, uint32_t &px, uint32_t &py)
 {
-    const __half h = __float2half_rn(x);
-    const __half l = __float2half_rn((x - __half2float(h)) * 2048.0f);
-    return (uint32_t)__half_as_ushort(h) | (uint32_t)__half_as_ushort(l) << 16;
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 b = __half22float2(h);
+    const __half2 l = __floats2half2_rn((x - b.x) * 2048.0f, (y - b.y) * 2048.0f);
+    const uint32_t hw = *reinterpret_cast<const uint32_t *>(&h), lw = *reinterpret_cast<const uint32_t *>(&l);
+    px = __byte_perm(hw, lw, 0x5410);
+    py = __byte_perm(hw, lw, 0x7632);
 }
 
 constexpr float LOW_PART = 1.0f / 2048.0f;
@@ -194,26 +191,45 @@ struct Job {  // an item cut at the end of a warp's range
     int pad[2];
 };
 
+struct AttnMaps {  // the pools as [block][16][head_dim] bytes
+    CUtensorMap k, v;
+};
+
 template <int D, int NT>
-__global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
+    kv_attention_kernel(const AttnArgs a, const __grid_constant__ AttnMaps maps)
 {
     using C = AttnCfg<D, NT>;
     constexpr int R = C::R, W = C::W, S = C::STAGES;
     constexpr int KH = D / 64;   // 64-byte parts of a key, 16 bytes to a lane
     constexpr int MT = D / 16;   // 16-row tiles of V^T
     constexpr int VW = D / 32;   // words of a value row that a lane holds
-    extern __shared__ __align__(16) unsigned char smem[];
-    float2 *s_ml = reinterpret_cast<float2 *>(smem + W * (C::RING + C::SLOT + C::QBYTES));  // [W][2][R] maximum, weight sum
+    extern __shared__ __align__(1024) unsigned char smem[];
+    float2 *s_ml = reinterpret_cast<float2 *>(smem + W * (C::RING + C::SLOT + C::QBYTES + C::META));  // [W][2][R] maximum, weight sum
     Job *s_job = reinterpret_cast<Job *>(s_ml + (3 * W + 1) * R);                // [1 + W]
-    int *s_pre = reinterpret_cast<int *>(s_job + W + 1);                         // [seqs + 1] units before a sequence
-    __shared__ int64_t s_warp[W];
-    __shared__ int s_last[2];
+    uint64_t *s_bar = reinterpret_cast<uint64_t *>(s_job + W + 1);               // [W][STAGES]
+    int64_t *s_warp = reinterpret_cast<int64_t *>(s_bar + W * S);                // [W]
+    int *s_last = reinterpret_cast<int *>(s_warp + W);                           // [2]
+    int *s_pre = s_last + 2;                                                     // [seqs + 1] units before a sequence
 
-    pdl_launch_dependents();
-    pdl_wait();
     const KvParams &p = a.kv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
+    const uint32_t bar0 = smem_addr(s_bar + warp * S);
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+            mbar_init(bar0 + 8 * i, 1);
+        fence_barrier_init();
+        fence_proxy_async_smem();
+    }
+    pdl_launch_dependents();
+    pdl_wait();
+    if ((smem_addr(smem) & 1023u) != 0) {  // the copies' swizzle counts from 1024-byte boundaries
+        atomicOr(p.err, (unsigned)ERRBIT_PLAN);
+        return;
+    }
+    __syncwarp();
 
     // ---- the line of units: an exclusive sum over the sequences ------------------------------
     if (lane == 0) {
@@ -302,7 +318,19 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
 
     unsigned char *ring = smem + warp * C::RING;
     float *slot0 = reinterpret_cast<float *>(smem + W * C::RING + warp * C::SLOT);
-    const uint32_t ring_a = smem_addr(ring) + 16 * lane;
+    const uint32_t ring_a = smem_addr(ring);
+    uint32_t use = 0, use_phase = 0;  // the ring stage of the next block to read, and its barrier's phase
+    bool dead = false;                // a copy did not land in time
+    // Lane (g, t) reads row rho of a tile's upper and lower 8 rows of keys, 16-byte pieces 4 h + t.
+    // Rows of 128 bytes: the copies put piece c of row r at c ^ (r & 7); lanes 0-7 hold rows 0 and 4
+    // (pieces apart by 4), so rho swaps g's lowest and highest bits' places.  Rows of 64 bytes: at
+    // c ^ (r >> 1 & 3), and the rows' own 64 bytes keep neighbours apart.
+    const int rho = D > 64 ? (g >> 1) | (g & 1) << 2 : g;
+    const uint32_t k_at = D > 64 ? rho * 128 + ((t ^ rho) << 4) : g * 64 + ((t ^ (g >> 1 & 3)) << 4);
+    // ... and of values rows (positions) v0, v0 + v1, v0 + 8, v0 + v1 + 8: those that rho deals to
+    // columns 2 t, 2 t + 1, 2 t + 8, 2 t + 9, dimensions 16 rho + 0..15 (of a 64-wide head 8 g + 0..7).
+    const uint32_t v_at = D > 64 ? t * 128 + ((rho ^ t) << 4) : 2 * t * 64 + (((g >> 1) ^ t) << 4) + (g & 1) * 8;
+    int4 *meta = reinterpret_cast<int4 *>(smem + W * (C::RING + C::SLOT + C::QBYTES) + warp * C::META);
 
     int s = 0, cg = 0, head = 0, b0 = 0;  // the item of unit u, and the unit's block in it
     if (u < w1) {
@@ -361,63 +389,70 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
         int page_nn = page_of(64 + lane);
         // lane (g, t) holds columns g of the query tiles, dimensions 64 h + 16 t + 0..15; a column past
         // the rows repeats the last one
-        float x[KH][16];
+        float x[NT][KH][16];
         auto load_q = [&](int nt) {
             const int r = cg * R + min(4 * nt + (g >> 1), gr.rows - 1);
             const float *qp = a.q + row_offset(a, sq.row0, head, r, a.q_stride, D) + 16 * t;
 #pragma unroll
             for (int h = 0; h < KH; ++h)
-                load_f32(x[h], qp + 64 * h);
+                load_f32(x[nt][h], qp + 64 * h);
         };
-        load_q(0);
-        int bi_c = block_of(lane, page_c), bi_n = block_of(32 + lane, page_n);
-        float ks_c = bi_c >= 0 ? p.ks[bi_c] : 0.0f, vs_c = bi_c >= 0 ? p.vs[bi_c] : 0.0f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            load_q(nt);
+        int bi_n = block_of(lane, page_c);
         float ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
+        int bi_1 = -1;
+        float ks_1 = 0.0f, vs_1 = 0.0f;
+        if (real > 32) {
+            bi_1 = block_of(32 + lane, page_n);
+            ks_1 = bi_1 >= 0 ? p.ks[bi_1] : 0.0f, vs_1 = bi_1 >= 0 ? p.vs[bi_1] : 0.0f;
+        }
+        __syncwarp();  // every lane has read the last item's
+        meta[lane] = make_int4(bi_n, __float_as_int(ks_n), __float_as_int(vs_n), 0);
+        meta[32 + lane] = make_int4(bi_1, __float_as_int(ks_1), __float_as_int(vs_1), 0);
+        if (real > 64) {
+            bi_n = block_of(64 + lane, page_nn);
+            ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
+            page_nn = page_of(96 + lane);
+        }
+        __syncwarp();
 
-        auto issue = [&](int j, int idx) {  // copy the item's j-th block into its ring stage
+        auto issue = [&](int j, uint32_t stage) {  // copy the item's j-th block into a ring stage
             if (j < real) {
-                const int bi = __shfl_sync(0xffffffffu, (j >> 5) == (idx >> 5) ? bi_c : bi_n, j & 31);
+                const int bi = meta[j & 63].x;
                 if (bi >= 0) {
-                    const uint32_t dst = ring_a + (j % S) * C::BLOCK_BYTES;
-                    const int8_t *kp = p.k + (int64_t)bi * (KV_BLOCK * D) + g * D + 16 * t;
+                    if (lane == 0) {
+                        const uint32_t dst = ring_a + stage * C::BLOCK_BYTES, bar = bar0 + 8 * stage;
+                        mbar_arrive_expect_tx(bar, C::BLOCK_BYTES);
 #pragma unroll
-                    for (int h = 0; h < KH; ++h) {
-                        cp_async16(dst + (2 * h) * 512, kp + 64 * h);
-                        cp_async16(dst + (2 * h + 1) * 512, kp + 8 * D + 64 * h);
-                    }
-                    const int8_t *vp = p.v + (int64_t)bi * (KV_BLOCK * D) + 2 * t * D + g * (D / 8);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int8_t *src = vp + ((x & 1) + (x >> 1) * 8) * D;
-                        if constexpr (D == 64) {
-                            cp_async8(dst - 8 * lane + 16 * D + x * 256, src);
-                        } else {
-#pragma unroll
-                            for (int y = 0; y < VW / 4; ++y)
-                                cp_async16(dst + 16 * D + (x * (VW / 4) + y) * 512, src + 16 * y);
+                        for (int x = 0; x < D / C::BOX; ++x) {
+                            tma_load_3d(dst + x * C::TILE, &maps.k, x * C::BOX, 0, bi, bar);
+                            tma_load_3d(dst + 16 * D + x * C::TILE, &maps.v, x * C::BOX, 0, bi, bar);
                         }
                     }
+                } else if (lane == 0) {
+                    mbar_arrive_expect_tx(bar0 + 8 * stage, 0);  // nothing to wait for
                 }
             }
-            cp_async_commit();
         };
-#pragma unroll
-        for (int j = 0; j < S - 1; ++j)
-            issue(j, 0);
+        uint32_t put = use;  // the ring stage of the next block to ask for
+        for (int j = 0; j < S - 1; ++j) {
+            issue(j, put);
+            put = put + 1 == S ? 0 : put + 1;
+        }
 
         // ---- the queries as two f16 parts ------------------------------------------------------
         uint32_t qf[C::QS ? 1 : NT][KH * 4][2];
         float qscale[NT];  // of query row 4 nt + t
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            if (nt > 0)
-                load_q(nt);
             float top = 0.0f;
 #pragma unroll
             for (int h = 0; h < KH; ++h)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    top = fmaxf(top, fabsf(x[h][e]));
+                    top = fmaxf(top, fabsf(x[nt][h][e]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // q times a power of two, the largest value in [0.5, 1)
@@ -429,9 +464,9 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
                 for (int w = 0; w < 4; ++w)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const uint32_t u0_ = split_f16(x[h][4 * w + 2 * e] * f);
-                        const uint32_t u1_ = split_f16(x[h][4 * w + 2 * e + 1] * f);
-                        qf[C::QS ? 0 : nt][4 * h + w][e] = __byte_perm(u0_, u1_, (g & 1) ? 0x7632 : 0x5410);
+                        uint32_t lo, hi;
+                        split_f16(x[nt][h][4 * w + 2 * e] * f, x[nt][h][4 * w + 2 * e + 1] * f, lo, hi);
+                        qf[C::QS ? 0 : nt][4 * h + w][e] = __byte_perm(lo, hi, (g & 1) ? 0x7632 : 0x5410);
                     }
             if constexpr (C::QS) {
                 uint4 *dst = reinterpret_cast<uint4 *>(smem + W * (C::RING + C::SLOT) + warp * C::QBYTES) + lane;
@@ -459,28 +494,17 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
                 o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
         }
 
-        for (int idx = 0; idx < real; ++idx) {
-            if ((idx & 31) == 0 && idx > 0) {
-                bi_c = bi_n, ks_c = ks_n, vs_c = vs_n;
-                bi_n = block_of(idx + 32 + lane, page_nn);
-                ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
-                page_nn = page_of(idx + 64 + lane);
-            }
-            issue(idx + S - 1, idx);
-            cp_async_wait<S - 1>();
-            const unsigned char *st = ring + (idx % S) * C::BLOCK_BYTES;
-            const float ks = __shfl_sync(0xffffffffu, ks_c, idx & 31);
-            const float vs = __shfl_sync(0xffffffffu, vs_c, idx & 31);
-            const int bi = __shfl_sync(0xffffffffu, bi_c, idx & 31);
-
-            // S^T = K Q^T
-            float c[NT][4];
+        // S^T = K Q^T of the block in a ring stage
+        auto scores = [&](float (&c)[NT][4], const unsigned char *st) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
                 c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.0f;
+            // one column tile: two chains of sums
+            float c2[4] = {};
 #pragma unroll
             for (int h = 0; h < KH; ++h) {
-                uint4 ka = lds128(st + 16 * lane + (2 * h) * 512), kb = lds128(st + 16 * lane + (2 * h + 1) * 512);
+                const unsigned char *kp = st + (h >> 1) * C::TILE + (k_at ^ (h & 1) << 6);
+                const uint4 ka = lds128(kp), kb = lds128(kp + 8 * C::BOX);
                 const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
                 for (int w2 = 0; w2 < 4; w2 += 2) {
@@ -497,16 +521,64 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
                             const uint4 qv = lds128(smem + W * (C::RING + C::SLOT) + warp * C::QBYTES + 16 * lane +
                                                     (nt * KH * 2 + 2 * h + w2 / 2) * 512);
                             mma_16816(c[nt], f[0], qv.x, qv.y);
-                            mma_16816(c[nt], f[1], qv.z, qv.w);
+                            mma_16816(NT == 1 ? c2 : c[nt], f[1], qv.z, qv.w);
                         } else {
                             mma_16816(c[nt], f[0], qf[nt][4 * h + w2][0], qf[nt][4 * h + w2][1]);
-                            mma_16816(c[nt], f[1], qf[nt][4 * h + w2 + 1][0], qf[nt][4 * h + w2 + 1][1]);
+                            mma_16816(NT == 1 ? c2 : c[nt], f[1], qf[nt][4 * h + w2 + 1][0], qf[nt][4 * h + w2 + 1][1]);
                         }
                     }
                 }
             }
 
-            // scores of positions pos + g and pos + g + 8 against query row 4 nt + t, in log2 units
+            if (NT == 1)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    c[0][e] += c2[e];
+        };
+        // With up to two column tiles, the next block's first product runs beside this block's weights and second product: two
+        // chains of dependent instructions for the scheduler instead of one.
+        float c[NT][4];
+        // wait for the block in stage use (phase use_phase), or the one after it
+        auto landed = [&](uint32_t stage, uint32_t phase) {
+            if (__all_sync(0xffffffffu, mbar_wait_bounded(bar0 + 8 * stage, phase, a.wait_ns)))
+                return true;
+            dead = true;
+            return false;
+        };
+        if constexpr (C::PIPE) {
+            if (real > 0 && landed(use, use_phase))
+                scores(c, ring + use * C::BLOCK_BYTES);
+        }
+        for (int idx = 0; idx < real && !dead; ++idx) {
+            if ((idx & 31) == 0 && idx > 0 && idx + 32 < real) {
+                __syncwarp();
+                meta[(idx + 32 + lane) & 63] = make_int4(bi_n, __float_as_int(ks_n), __float_as_int(vs_n), 0);
+                bi_n = block_of(idx + 64 + lane, page_nn);
+                ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
+                page_nn = page_of(idx + 96 + lane);
+                __syncwarp();
+            }
+            const uint32_t next = use + 1 == S ? 0 : use + 1, next_phase = next == 0 ? use_phase ^ 1u : use_phase;
+            fence_proxy_async_smem();
+            __syncwarp();  // every lane has read the stage that is asked for again
+            issue(idx + S - 1, put);
+            put = put + 1 == S ? 0 : put + 1;
+            float cn[NT][4];
+            if constexpr (C::PIPE) {
+                if (idx + 1 < real && !landed(next, next_phase))
+                    break;
+                scores(cn, ring + next * C::BLOCK_BYTES);  // past the last block: of what the ring holds, not used
+            } else {
+                if (!landed(use, use_phase))
+                    break;
+                scores(c, ring + use * C::BLOCK_BYTES);
+            }
+            const int4 md = meta[idx & 63];
+            const int bi = md.x;
+            const float ks = __int_as_float(md.y), vs = __int_as_float(md.z);
+            const unsigned char *st = ring + use * C::BLOCK_BYTES;
+
+            // scores of positions pos + rho and pos + rho + 8 against query row 4 nt + t, in log2 units
             const int pos = (first_blk + idx) * KV_BLOCK;
             const bool whole = pos >= all_from && pos + KV_BLOCK <= all_to && bi >= 0;
             float sc[NT][2];
@@ -518,7 +590,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
                 sc[nt][1] = fmaf(c[nt][3], LOW_PART, c[nt][2]) * f;
                 if (!whole) {
                     const int end = row_end(sq, (cg * R + min(4 * nt + t, gr.rows - 1)) / a.by_group);
-                    const int begin = row_begin(a, end), j = pos + g;
+                    const int begin = row_begin(a, end), j = pos + rho;
                     if (bi < 0 || j < begin || j >= end)
                         sc[nt][0] = -INFINITY;
                     if (bi < 0 || j + 8 < begin || j + 8 >= end)
@@ -555,13 +627,14 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
             const float vr = vs * vinv;
             uint32_t pb[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float w = ex2(sc[nt][e] - m[nt]);
-                    l[nt] += w;
-                    pb[nt][e] = transpose_8x8(split_f16(w * vr));
-                }
+            for (int nt = 0; nt < NT; ++nt) {
+                const float w0 = ex2(sc[nt][0] - m[nt]), w1 = ex2(sc[nt][1] - m[nt]);
+                l[nt] += w0 + w1;
+                uint32_t a0, a1;
+                split_f16(w0 * vr, w1 * vr, a0, a1);
+                pb[nt][0] = transpose_8x8(a0);
+                pb[nt][1] = transpose_8x8(a1);
+            }
 
             // O^T += V^T P^T
             const unsigned char *sv = st + 16 * D;
@@ -571,10 +644,10 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     if constexpr (D == 64) {
-                        const uint2 q2 = *reinterpret_cast<const uint2 *>(sv + x * 256 + 8 * lane);
+                        const uint2 q2 = *reinterpret_cast<const uint2 *>(sv + v_at + (x & 1) * 64 + (x >> 1) * 512);
                         v[x][0] = q2.x, v[x][1] = q2.y;
                     } else {
-                        const uint4 q4 = lds128(sv + (x * (VW / 4) + y) * 512 + 16 * lane);
+                        const uint4 q4 = lds128(sv + y * C::TILE + ((x & 1) ? (v_at ^ 64) + 512 : v_at) + (x >> 1) * 1024);
                         v[x][0] = q4.x, v[x][1] = q4.y, v[x][2] = q4.z, v[x][3] = q4.w;
                     }
                 }
@@ -595,12 +668,45 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
                     }
                 }
             }
+            if constexpr (C::PIPE)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        c[nt][e] = cn[nt][e];
+            use = next;
+            use_phase = next_phase;
         }
-        cp_async_wait<0>();
+        if (dead) {
+            // flag it, wait (bounded) for this warp's copies that may be in flight, leave the rest out
+            if (lane == 0) {
+                atomicOr(p.err, (unsigned)ERRBIT_QMV_WAIT);
+                for (int i = 0; i < S; ++i) {
+                    if (!mbar_wait_bounded(bar0 + 8 * use, use_phase, a.wait_ns)) {
+                        atomicOr(p.err, (unsigned)ERRBIT_DRAIN_WAIT);
+                        break;
+                    }
+                    use = use + 1 == S ? 0 : use + 1;
+                    use_phase = use == 0 ? use_phase ^ 1u : use_phase;
+                }
+            }
+            __syncwarp();
+            break;
+        }
 
         // ---- the item's part: finished, or laid down for the join --------------------------------
         const bool done = b0 == 0 && cnt == nb;
         const int part = b0 > 0 ? 0 : 1;
+        auto store_head = [&](float *o, const float (&y)[2 * MT]) {  // the lane's dimensions of a head
+            if constexpr (D == 64) {
+                store_f32(o + 8 * g, y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2 * MT; i += 4)
+                    *reinterpret_cast<float4 *>(o + (i >> 4) * 128 + 16 * rho + (i & 15)) =
+                        make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
+            }
+        };
         float *dst = part == 0 ? slot0 : reinterpret_cast<float *>(ring);
         if (part == 1 && !done)
             __syncwarp();  // every lane has read the ring
@@ -618,11 +724,11 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1) kv_attention_kernel
                 y[2 * mt + 1] = fmaf(o[nt][mt][3], LOW_PART, o[nt][mt][2]) * f;
             }
             if (!done) {
-                store_f32(dst + r * D + 2 * MT * g, y);
+                store_head(dst + r * D, y);
                 if (g == 0)
                     s_ml[(warp * 2 + part) * R + r] = make_float2(m[nt], l[nt]);
             } else if (r < gr.rows) {
-                store_f32(a.out + row_offset(a, sq.row0, head, cg * R + r, a.out_stride, D) + 2 * MT * g, y);
+                store_head(a.out + row_offset(a, sq.row0, head, cg * R + r, a.out_stride, D), y);
             }
         }
         // the item's first cut in this CTA makes the job of joining it
@@ -836,6 +942,18 @@ static qmd_status launch_att(const AttnArgs &a, const DeviceInfo &dev, cudaStrea
             opted[dev.device] = true;
         }
     }
+    const TensorMapEncodeFn enc = tensor_map_encoder();
+    if (!enc)
+        return fail(QMD_ERR_LAUNCH, "cuTensorMapEncodeTiled entry point", cudaErrorNotSupported);
+    AttnMaps maps;
+    const cuuint64_t dim[3] = {(cuuint64_t)D, KV_BLOCK, (cuuint64_t)a.kv.pages * a.kv.heads * a.kv.page_blocks};
+    const cuuint64_t str[2] = {(cuuint64_t)D, (cuuint64_t)D * KV_BLOCK};
+    const cuuint32_t box[3] = {(cuuint32_t)C::BOX, KV_BLOCK, 1}, one[3] = {1, 1, 1};
+    for (int i = 0; i < 2; ++i)
+        if (enc(i ? &maps.v : &maps.k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, i ? a.kv.v : a.kv.k, dim, str, box, one,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return fail(QMD_ERR_LAUNCH, "tensor map of the cache", cudaErrorInvalidValue);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)dev.sm_count);
     cfg.blockDim = dim3(C::W * 32);
@@ -846,7 +964,7 @@ static qmd_status launch_att(const AttnArgs &a, const DeviceInfo &dev, cudaStrea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (launch_flags() & LAUNCH_NO_PDL) ? 0 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, NT>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, NT>, a, maps);
     return e == cudaSuccess ? QMD_OK : fail(QMD_ERR_LAUNCH, "kv_attention launch", e);
 }
 
@@ -863,7 +981,7 @@ qmd_status launch_kv_attention(const KvParams &kv, int head_dim, const float *q,
                                const DeviceInfo &dev, cudaStream_t s)
 {
     const AttnArgs a = {kv, q, out, reinterpret_cast<float *>(static_cast<char *>(ws) + counter_bytes(dev)),
-                        static_cast<unsigned *>(ws), q_stride, out_stride, window, q_heads / kv.heads,
+                        static_cast<unsigned *>(ws), q_stride, out_stride, window, wait_limit_ns(), q_heads / kv.heads,
                         fast_div((unsigned)(q_heads / kv.heads)), fast_div((unsigned)kv.page_blocks),
                         scale * 1.4426950408889634f};
     // rows per item: the least of 4, 8, 16 that holds a sequence's rows of one key/value head

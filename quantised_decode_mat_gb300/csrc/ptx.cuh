@@ -146,6 +146,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int 
         : "memory");
 }
 
+// The same with the default L2 policy, for data that is read again soon (the key/value cache).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
 // Order this thread's earlier generic-proxy shared-memory accesses before later async-proxy
 // (bulk / tensor copy) writes to the same bytes.
 __device__ __forceinline__ void fence_proxy_async_smem()

@@ -54,6 +54,7 @@
 #include <cuda.h>
 
 #include "qmv.cuh"
+#include "tensor_map.h"
 
 namespace qmd {
 
@@ -819,27 +820,6 @@ qmd_status launch_tc_stages(const TcParams &tp, const QmvPlan &plan, int mode, c
     return mode == QMV_PACK   ? launch_kernel<qmv_tc_kernel<F, QMV_PACK, STAGES, MULTI>>(tp, plan, s)
            : mode == QMV_DUMP ? launch_kernel<qmv_tc_kernel<F, QMV_DUMP, STAGES, MULTI>>(tp, plan, s)
                               : launch_kernel<qmv_tc_kernel<F, QMV_PLAIN, STAGES, MULTI>>(tp, plan, s);
-}
-
-// The driver's tensor-map encoder, looked up once through the runtime (no link to the driver
-// library); NULL if this driver does not provide it.
-using TensorMapEncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                       const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,
-                                       CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                       CUtensorMapFloatOOBfill);
-inline TensorMapEncodeFn tensor_map_encoder()
-{
-    static TensorMapEncodeFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<TensorMapEncodeFn>(f);
-    });
-    return fn;
 }
 
 // Tensor maps of one call: W as bytes [rows][row_bytes] in boxes of one block x th rows (rows

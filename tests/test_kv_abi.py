@@ -33,7 +33,7 @@ BAD_CACHE = [(dict(k=None), 1), (dict(v=None), 1), (dict(k_scale=None), 1), (dic
              (dict(v=A + 4), 5), (dict(k_scale=A + 2), 5), (dict(pages=0), 6), (dict(pages=1 << 31), 6),
              (dict(kv_heads=0), 6), (dict(kv_heads=1025), 6), (dict(page_tokens=0), 6), (dict(page_tokens=24), 6),
              (dict(page_tokens=65552), 6), (dict(head_dim=96), 6), (dict(head_dim=0), 6)]
-BAD_BATCH = [(dict(page_table=None), 1), (dict(kv_len=None), 1), (dict(seqs=0), 6), (dict(seqs=4097), 6), (dict(max_q=0), 6),
+BAD_BATCH = [(dict(page_table=None), 1), (dict(kv_len=None), 1), (dict(seqs=0), 6), (dict(seqs=2049), 6), (dict(max_q=0), 6),
              (dict(max_q=(1 << 20) + 1), 6), (dict(rows=0), 6), (dict(rows=(1 << 24) + 1), 6), (dict(table_stride=0), 6),
              (dict(q_start=None), 6),  # three sequences of two rows in five rows
              (dict(kv_len=A + 2), 5), (dict(page_table=A + 1), 5), (dict(q_start=A + 2), 5)]
