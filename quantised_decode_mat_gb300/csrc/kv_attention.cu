@@ -810,6 +810,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
             if (r >= s_job[jj].rows)
                 continue;
             float y[4] = {};
+#pragma unroll 4
             for (int w = wa; w <= wb; ++w) {
                 const bool one = w == wa && jj > 0;
                 const float f = s_ml[(w * 2 + one) * R + r].x;
@@ -854,35 +855,53 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
             const int c0 = (u0 + s_job[jj].start) / per, c1 = (u0 + s_job[jj].end - 1) / per;
             __threadfence();
             last = atomicAdd(a.ctr + c0, 1u) == (unsigned)(c1 - c0);
-            if (last)
+            if (last) {
                 a.ctr[c0] = 0;  // every part has come: left as it was found
-            __threadfence();
+                __threadfence();
+            }
         }
         s_last[tid] = last ? jj + 1 : 0;
     }
     __syncthreads();
-    constexpr int EL = R * D / 4, NG = W * 32 / EL > 0 ? W * 32 / EL : 1;  // groups of threads share the parts
-    float *s_f = reinterpret_cast<float *>(smem);  // [parts][R] factors
-    float4 *s_y = reinterpret_cast<float4 *>(smem + (size_t)gridDim.x * R * 4);  // [NG][EL]
+    // NG groups of threads share an item's parts; a thread adds IT places of 4 values, their loads
+    // and the maxima's in flight together
+    constexpr int EL = R * D / 4, NG = W * 32 / EL > 0 ? W * 32 / EL : 1, IT = (NG * EL + W * 32 - 1) / (W * 32);
+    float2 *s_p = reinterpret_cast<float2 *>(smem);  // [parts][R] maxima and sums, then factors
+    float4 *s_y = reinterpret_cast<float4 *>(smem + (size_t)gridDim.x * R * 8);  // [NG][EL]
     for (int x = 0; x < 2; ++x) {
         if (!s_last[x])
             continue;
         const Job j = s_job[s_last[x] - 1];
         const int c0 = (u0 + j.start) / per, parts = (u0 + j.end - 1) / per - c0 + 1;
-        const float2 *ml = reinterpret_cast<const float2 *>(a.part + part_ml);
         // part i lies with CTA c0 + i, as its part 1 if the item began there
+        auto slot = [&](int i) { return ((int64_t)(c0 + i) * 2 + (i == 0)) * R; };
+        const float2 *ml = reinterpret_cast<const float2 *>(a.part + part_ml);
+        auto value = [&](int i, int it) {
+            const int e = tid + it * W * 32;
+            return __ldcg(reinterpret_cast<const float4 *>(a.part + slot(i) * D) + e % EL);
+        };
+        auto holds = [&](int it) { return NG * EL % (W * 32) == 0 || tid + it * W * 32 < NG * EL; };
+        const int n0 = NG > 1 ? tid / EL : 0;  // this thread's first part (its IT places share the group, or NG = 1)
+        float4 v[IT];
+#pragma unroll
+        for (int it = 0; it < IT; ++it)
+            if (holds(it) && n0 < parts)
+                v[it] = value(n0, it);
+        for (int i = tid; i < parts * R; i += W * 32)
+            s_p[i] = __ldcg(&ml[slot(i / R) + i % R]);
+        __syncthreads();
         for (int r = warp; r < j.rows; r += W) {
             float M = ATT_NONE, L = 0.0f;
             for (int i = lane; i < parts; i += 32)
-                M = fmaxf(M, __ldcg(&ml[((int64_t)(c0 + i) * 2 + (i == 0)) * R + r]).x);
+                M = fmaxf(M, s_p[i * R + r].x);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
             for (int i = lane; i < parts; i += 32) {
-                const float2 v = __ldcg(&ml[((int64_t)(c0 + i) * 2 + (i == 0)) * R + r]);
-                const float f = ex2(v.x - M);
-                s_f[i * R + r] = f;
-                L = fmaf(v.y, f, L);
+                const float2 w = s_p[i * R + r];
+                const float f = ex2(w.x - M);
+                s_p[i * R + r].x = f;
+                L = fmaf(w.y, f, L);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
@@ -891,33 +910,41 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
                 s_tot[r].y = L;
         }
         __syncthreads();
-        for (int e = tid; e < NG * EL; e += W * 32) {
-            const int n = e / EL, r = e % EL / (D / 4);
-            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (r < j.rows)
-#pragma unroll 8
-                for (int i = n; i < parts; i += NG) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(
-                                                a.part + ((int64_t)(c0 + i) * 2 + (i == 0)) * R * D) + e % EL);
-                    const float f = s_f[i * R + r];
-                    y.x = fmaf(v.x, f, y.x), y.y = fmaf(v.y, f, y.y), y.z = fmaf(v.z, f, y.z), y.w = fmaf(v.w, f, y.w);
+        float4 y[IT];
+#pragma unroll
+        for (int it = 0; it < IT; ++it)
+            y[it] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int i = n0; i < parts; i += NG) {
+#pragma unroll
+            for (int it = 0; it < IT; ++it)
+                if (holds(it)) {
+                    const int r = (tid + it * W * 32) % EL / (D / 4);
+                    const float f = r < j.rows ? s_p[i * R + r].x : 0.0f;
+                    const float4 u = i == n0 ? v[it] : value(i, it);
+                    y[it].x = fmaf(u.x, f, y[it].x), y[it].y = fmaf(u.y, f, y[it].y);
+                    y[it].z = fmaf(u.z, f, y[it].z), y[it].w = fmaf(u.w, f, y[it].w);
                 }
-            s_y[e] = y;
         }
-        __syncthreads();
-        for (int e = tid; e < EL; e += W * 32) {
-            const int r = e / (D / 4), d = e % (D / 4) * 4;
-            if (r >= j.rows)
+        if (NG > 1) {
+            if (holds(0))
+                s_y[tid] = y[0];
+            __syncthreads();
+        }
+#pragma unroll
+        for (int it = 0; it < IT; ++it) {
+            const int e = tid + it * W * 32, r = e / (D / 4), d = e % (D / 4) * 4;
+            if (e >= EL || r >= j.rows)
                 continue;
-            float4 y = s_y[e];
+            float4 z = y[it];
 #pragma unroll
             for (int n = 1; n < NG; ++n) {
-                const float4 v = s_y[n * EL + e];
-                y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+                const float4 u = s_y[n * EL + e];
+                z.x += u.x, z.y += u.y, z.z += u.z, z.w += u.w;
             }
             const float f = s_tot[r].y == 0.0f ? 0.0f : 1.0f / s_tot[r].y;
             *reinterpret_cast<float4 *>(a.out + row_offset(a, j.row0, j.head, j.first + r, a.out_stride, D) + d) =
-                make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+                make_float4(z.x * f, z.y * f, z.z * f, z.w * f);
         }
         __syncthreads();
     }
