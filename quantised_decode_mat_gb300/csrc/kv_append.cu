@@ -14,6 +14,10 @@
 // leader of a block if it is the first of the call's rows in it; the block's task is done by the
 // leader's chunk, so no two warps touch a block's scale and no atomics are needed.  Lane l owns
 // head_dim / 32 neighbouring values; a rotation partner half a head away comes by a shuffle.
+#include <mutex>
+#include <set>
+#include <utility>
+
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -24,6 +28,7 @@ namespace qmd {
 
 constexpr int APP_WARPS = 8;
 constexpr int APP_CHUNK = 16;  // rows a CTA looks up
+constexpr int APP_HEADS = 4;   // query heads of a task: their loads in flight together, the table's row read once
 
 struct KvRow {
     int seq;   // -1: a row that no sequence owns
@@ -73,39 +78,58 @@ struct RopeArgs {
     int rot, pairs;
 };
 
-// Rotate this lane's E values of a head at position pos (the warp holds the head).
+// This lane's cosines and sines of a position.
 template <int E>
-__device__ __forceinline__ void rotate(float (&x)[E], const RopeArgs &r, int pos, int lane)
+struct Angles {
+    float c[E], s[E];
+};
+
+template <int E>
+__device__ __forceinline__ void load_angles(Angles<E> &a, const RopeArgs &r, int pos, int lane)
 {
     const float *row = r.table + (int64_t)pos * r.rot;
     const int half = r.rot >> 1;
     if (r.pairs == QMD_ROPE_HALVES) {
         const int off = half / E;  // lanes between the two of a pair
-        const bool first = lane < off, second = !first && lane < 2 * off;
-        float o[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            o[i] = __shfl_sync(0xffffffffu, x[i], first ? lane + off : second ? lane - off : lane);
-        if (first || second) {
-            float c[E], s[E];
-            const int at = E * (first ? lane : lane - off);
-            load_f32(c, row + at);
-            load_f32(s, row + half + at);
-#pragma unroll
-            for (int i = 0; i < E; ++i) {
-                const float xc = __fmul_rn(x[i], c[i]), os = __fmul_rn(o[i], s[i]);
-                x[i] = first ? __fsub_rn(xc, os) : __fadd_rn(xc, os);
-            }
+        if (lane < 2 * off) {
+            const int at = E * (lane < off ? lane : lane - off);
+            load_f32(a.c, row + at);
+            load_f32(a.s, row + half + at);
         }
     } else if (E * lane < r.rot) {
         float c[E / 2], s[E / 2];
         load_f32(c, row + E / 2 * lane);
         load_f32(s, row + half + E / 2 * lane);
 #pragma unroll
+        for (int i = 0; i < E / 2; ++i)
+            a.c[i] = c[i], a.s[i] = s[i];
+    }
+}
+
+// Rotate this lane's E values of a head (the warp holds the head).
+template <int E>
+__device__ __forceinline__ void rotate(float (&x)[E], const RopeArgs &r, const Angles<E> &a, int lane)
+{
+    if (r.pairs == QMD_ROPE_HALVES) {
+        const int off = (r.rot >> 1) / E;
+        const bool first = lane < off, second = !first && lane < 2 * off;
+        float o[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            o[i] = __shfl_sync(0xffffffffu, x[i], first ? lane + off : second ? lane - off : lane);
+        if (first || second) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float xc = __fmul_rn(x[i], a.c[i]), os = __fmul_rn(o[i], a.s[i]);
+                x[i] = first ? __fsub_rn(xc, os) : __fadd_rn(xc, os);
+            }
+        }
+    } else if (E * lane < r.rot) {
+#pragma unroll
         for (int i = 0; i < E / 2; ++i) {
-            const float a = x[2 * i], b = x[2 * i + 1];
-            x[2 * i] = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
-            x[2 * i + 1] = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
+            const float p = x[2 * i], q = x[2 * i + 1];
+            x[2 * i] = __fsub_rn(__fmul_rn(p, a.c[i]), __fmul_rn(q, a.s[i]));
+            x[2 * i + 1] = __fadd_rn(__fmul_rn(q, a.c[i]), __fmul_rn(p, a.s[i]));
         }
     }
 }
@@ -142,6 +166,8 @@ template <int D>
 __global__ void __launch_bounds__(APP_WARPS * 32) kv_append_kernel(const AppendArgs a)
 {
     constexpr int E = D / 32;
+    constexpr int RB = 4;  // rows whose loads are in flight together
+    extern __shared__ __align__(16) float s_x[];  // [warps][16][D]: a block's new rows until its scale is known
     __shared__ KvRow s_row[APP_CHUNK];
     __shared__ int s_order[APP_CHUNK], s_count;
     pdl_launch_dependents();
@@ -151,10 +177,11 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv_append_kernel(const AppendA
     chunk_rows(p, t0, s_row, s_order, &s_count);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int blocks = s_count * p.heads * 2;
-    const int tasks = blocks + (a.q ? APP_CHUNK * a.q_heads : 0);
+    const int groups = (a.q_heads + APP_HEADS - 1) / APP_HEADS;
+    const int tasks = blocks + (a.q ? APP_CHUNK * groups : 0);
     for (int task = blockIdx.y * APP_WARPS + warp; task < tasks; task += gridDim.y * APP_WARPS) {
-        if (task >= blocks) {  // a query head
-            const int i = (task - blocks) / a.q_heads, h = (task - blocks) % a.q_heads;
+        if (task >= blocks) {  // APP_HEADS query heads of a row
+            const int i = (task - blocks) / groups, h = (task - blocks) % groups * APP_HEADS;
             const KvRow r = s_row[i];
             if (r.seq < 0)
                 continue;
@@ -162,11 +189,23 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv_append_kernel(const AppendA
                 kv_index_error(p);
                 continue;
             }
-            float x[E];
-            load_f32(x, a.q + (t0 + i) * a.q_stride + h * D + E * lane);
+            const float *src = a.q + (t0 + i) * a.q_stride + h * D + E * lane;
+            float *dst = a.q_out + (t0 + i) * a.q_out_stride + h * D + E * lane;
+            float x[APP_HEADS][E];
+#pragma unroll
+            for (int j = 0; j < APP_HEADS; ++j)
+                if (h + j < a.q_heads)
+                    load_f32(x[j], src + j * D);
+            Angles<E> ang;
             if (a.rope.table)
-                rotate(x, a.rope, r.pos, lane);
-            store_f32(a.q_out + (t0 + i) * a.q_out_stride + h * D + E * lane, x);
+                load_angles(ang, a.rope, r.pos, lane);
+#pragma unroll
+            for (int j = 0; j < APP_HEADS; ++j)
+                if (h + j < a.q_heads) {
+                    if (a.rope.table)
+                        rotate(x[j], a.rope, ang, lane);
+                    store_f32(dst + j * D, x[j]);
+                }
             continue;
         }
         const int i = s_order[task / (2 * p.heads)], h = task / 2 % p.heads;
@@ -187,16 +226,28 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv_append_kernel(const AppendA
         int8_t *codes = (is_v ? p.v : p.k) + blk * (KV_BLOCK * D) + E * lane;
         float *scale = (is_v ? p.vs : p.ks) + blk;
 
+        float *keep = s_x + warp * KV_BLOCK * D + E * lane;  // each lane reads back its own
         float top = 0.0f;
-#pragma unroll 2
-        for (int j = 0; j < m; ++j) {
-            float x[E];
-            load_f32(x, src + j * stride);
-            if (turn)
-                rotate(x, a.rope, r.pos + j, lane);
+        for (int j0 = 0; j0 < m; j0 += RB) {
+            float x[RB][E];
+            Angles<E> ang[RB];
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                top = fmaxf(top, fabsf(x[e]));
+            for (int j = 0; j < RB; ++j)
+                if (j0 + j < m) {
+                    load_f32(x[j], src + (j0 + j) * stride);
+                    if (turn)
+                        load_angles(ang[j], a.rope, r.pos + j0 + j, lane);
+                }
+#pragma unroll
+            for (int j = 0; j < RB; ++j)
+                if (j0 + j < m) {
+                    if (turn)
+                        rotate(x[j], a.rope, ang[j], lane);
+                    store_f32(keep + (j0 + j) * D, x[j]);
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        top = fmaxf(top, fabsf(x[j][e]));
+                }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -208,20 +259,18 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv_append_kernel(const AppendA
             // the block's earlier tokens in steps of the larger scale
 #pragma unroll 2
             for (int j = 0; j < tok0; ++j) {
-                float x[E];
-                load_codes(x, codes + j * D);
+                float y[E];
+                load_codes(y, codes + j * D);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    x[e] = __fmul_rn(x[e], d0);
-                store_codes(codes + j * D, x, inv);
+                    y[e] = __fmul_rn(y[e], d0);
+                store_codes(codes + j * D, y, inv);
             }
         }
-#pragma unroll 2
+#pragma unroll 4
         for (int j = 0; j < m; ++j) {
             float x[E];
-            load_f32(x, src + j * stride);
-            if (turn)
-                rotate(x, a.rope, r.pos + j, lane);
+            load_f32(x, keep + j * D);
             store_codes(codes + (tok0 + j) * D, x, inv);
         }
         __syncwarp();  // every lane has read the old scale
@@ -229,6 +278,8 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv_append_kernel(const AppendA
             *scale = d;
     }
 }
+
+constexpr int READ_HEADS = 4;
 
 struct ReadArgs {
     KvParams kv;
@@ -248,22 +299,35 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv_read_kernel(const ReadArgs 
     const int64_t t0 = (int64_t)blockIdx.x * APP_CHUNK;
     chunk_rows(p, t0, s_row, s_order, &s_count);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int tasks = APP_CHUNK * p.heads * 2;
+    // a warp takes READ_HEADS neighbouring heads of a row, keys or values: their loads in flight together
+    const int groups = (p.heads + READ_HEADS - 1) / READ_HEADS;
+    const int tasks = APP_CHUNK * groups * 2;
     for (int task = blockIdx.y * APP_WARPS + warp; task < tasks; task += gridDim.y * APP_WARPS) {
-        const int i = task / (2 * p.heads), h = task / 2 % p.heads;
+        const int i = task / (2 * groups), h = task / 2 % groups * READ_HEADS;
         const bool is_v = task & 1;
         const KvRow r = s_row[i];
         float *out = is_v ? a.v : a.k;
         if (r.seq < 0 || r.page < 0 || !out)
             continue;
         const int64_t blk = kv_block_offset(p, r.page, h, r.pos / KV_BLOCK);
-        float x[E];
-        load_codes(x, (is_v ? p.v : p.k) + (blk * KV_BLOCK + r.pos % KV_BLOCK) * D + E * lane);
-        const float d = (is_v ? p.vs : p.ks)[blk];
+        const int8_t *codes = (is_v ? p.v : p.k) + (blk * KV_BLOCK + r.pos % KV_BLOCK) * D + E * lane;
+        const float *scale = (is_v ? p.vs : p.ks) + blk;
+        float x[READ_HEADS][E], d[READ_HEADS];
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            x[e] = __fmul_rn(x[e], d);
-        store_f32(out + (t0 + i) * (is_v ? a.v_stride : a.k_stride) + h * D + E * lane, x);
+        for (int j = 0; j < READ_HEADS; ++j)
+            if (h + j < p.heads) {
+                load_codes(x[j], codes + (int64_t)j * p.page_blocks * (KV_BLOCK * D));
+                d[j] = scale[j * p.page_blocks];
+            }
+        float *dst = out + (t0 + i) * (is_v ? a.v_stride : a.k_stride) + h * D + E * lane;
+#pragma unroll
+        for (int j = 0; j < READ_HEADS; ++j)
+            if (h + j < p.heads) {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    x[j][e] = __fmul_rn(x[j][e], d[j]);
+                store_f32(dst + j * D, x[j]);
+            }
     }
 }
 
@@ -278,13 +342,30 @@ static unsigned chunk_ctas(int64_t chunks, int64_t tasks, int sms)
 }
 
 template <class Args>
-static qmd_status launch_chunks(void (*kernel)(const Args), const Args &a, int64_t tasks, int sms, const char *what,
-                                cudaStream_t s)
+static qmd_status launch_chunks(void (*kernel)(const Args), const Args &a, int64_t tasks, int sms, size_t smem,
+                                const char *what, cudaStream_t s)
 {
+    if (smem > 48 * 1024) {
+        // opt in once per device and kernel; host threads may race here
+        static std::mutex mu;
+        static std::set<std::pair<int, const void *>> opted;
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess)
+            return QMD_ERR_DEVICE;
+        std::lock_guard<std::mutex> lock(mu);
+        if (opted.insert({dev, reinterpret_cast<const void *>(kernel)}).second) {
+            const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) {
+                opted.erase({dev, reinterpret_cast<const void *>(kernel)});
+                return fail(QMD_ERR_LAUNCH, what, e);
+            }
+        }
+    }
     const int64_t chunks = (a.kv.rows + APP_CHUNK - 1) / APP_CHUNK;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)chunks, chunk_ctas(chunks, tasks, sms));
     cfg.blockDim = dim3(APP_WARPS * 32);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -303,10 +384,11 @@ qmd_status launch_kv_append(const KvParams &kv, int head_dim, const float *k, in
     const AppendArgs a = {kv, {rope, rope_rows, rot, pairs}, k, v, q, q_out, k_stride, v_stride, q_stride,
                           q_out_stride, q_heads};
     const int64_t rows = kv.rows < APP_CHUNK ? kv.rows : APP_CHUNK;
-    const int64_t tasks = rows * (2 * kv.heads + q_heads);
-    return head_dim == 64    ? launch_chunks(kv_append_kernel<64>, a, tasks, sms, "kv_append launch", s)
-           : head_dim == 128 ? launch_chunks(kv_append_kernel<128>, a, tasks, sms, "kv_append launch", s)
-                             : launch_chunks(kv_append_kernel<256>, a, tasks, sms, "kv_append launch", s);
+    const int64_t tasks = rows * (2 * kv.heads + (q_heads + APP_HEADS - 1) / APP_HEADS);
+    const size_t smem = (size_t)APP_WARPS * KV_BLOCK * head_dim * 4;
+    return head_dim == 64    ? launch_chunks(kv_append_kernel<64>, a, tasks, sms, smem, "kv_append launch", s)
+           : head_dim == 128 ? launch_chunks(kv_append_kernel<128>, a, tasks, sms, smem, "kv_append launch", s)
+                             : launch_chunks(kv_append_kernel<256>, a, tasks, sms, smem, "kv_append launch", s);
 }
 
 qmd_status launch_kv_read(const KvParams &kv, int head_dim, float *k, int64_t k_stride, float *v, int64_t v_stride,
@@ -314,10 +396,10 @@ qmd_status launch_kv_read(const KvParams &kv, int head_dim, float *k, int64_t k_
 {
     const ReadArgs a = {kv, k, v, k_stride, v_stride};
     const int64_t rows = kv.rows < APP_CHUNK ? kv.rows : APP_CHUNK;
-    const int64_t tasks = rows * 2 * kv.heads;
-    return head_dim == 64    ? launch_chunks(kv_read_kernel<64>, a, tasks, sms, "kv_read launch", s)
-           : head_dim == 128 ? launch_chunks(kv_read_kernel<128>, a, tasks, sms, "kv_read launch", s)
-                             : launch_chunks(kv_read_kernel<256>, a, tasks, sms, "kv_read launch", s);
+    const int64_t tasks = rows * 2 * ((kv.heads + READ_HEADS - 1) / READ_HEADS);
+    return head_dim == 64    ? launch_chunks(kv_read_kernel<64>, a, tasks, sms, 0, "kv_read launch", s)
+           : head_dim == 128 ? launch_chunks(kv_read_kernel<128>, a, tasks, sms, 0, "kv_read launch", s)
+                             : launch_chunks(kv_read_kernel<256>, a, tasks, sms, 0, "kv_read launch", s);
 }
 
 }  // namespace qmd
