@@ -293,9 +293,11 @@ def _stream_on(stream, t, what: str) -> int:
 # a refusal.
 def _array(t, dtype, shape, device, what: str) -> int:
     """The address of a contiguous tensor of this type and shape (None: any extent) on this device."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise QmdError(2, f"{what}: {dtype} is wanted, got {t.dtype}")
-    if t.shape != shape and (t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape))):
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
         raise QmdError(6, f"{what}: shape {tuple(shape)} is wanted, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise QmdError(6, f"{what} must be contiguous")

@@ -8,9 +8,13 @@
 //
 // A cluster of 8 CTAs serves one vector and a share of its rows.  Each CTA multiplies its eighth of
 // x with all rows of A, the partial sums go to all 8 CTAs' shared memory, and after the cluster's
-// barrier each CTA adds the eighths in order and multiplies its rows of B, whose first loads were
-// issued before the barrier.  With few vectors several clusters share a vector's rows; each then
+// barrier each CTA adds the eighths in order and multiplies its rows of B.  Those come by bulk
+// copies, 4 KB of whole rows at a time into a ring of each warp, the first of them asked for before
+// A x is begun (registers hold 32 KB a CTA less: 14.5 us for 8 adapters of rank 64 on 28672 x 4096).
+// With few vectors several clusters share a vector's rows; each then
 // computes A x for itself (A is small beside B, and comes from L2).
+#include <mutex>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -22,7 +26,13 @@ namespace qmd {
 
 constexpr int LORA_CLUSTER = 8;
 constexpr int LORA_WARPS = 16;
-constexpr int LORA_AHEAD = 4;  // 16-byte loads of B a lane has in flight before the barrier, and after it
+constexpr int LORA_STAGES = 2;
+constexpr int LORA_CHUNK = 4096;                // bytes of B's rows that a copy takes, at most
+constexpr int LORA_CHUNK_ROWS = LORA_CHUNK / 16;  // and the most rows in them
+constexpr int LORA_PASSES = 8;                  // passes of 32 lanes over a chunk, at most (512 bytes each where
+                                                // the row's pieces are a power of two, else more)
+constexpr int LORA_STAGE_BYTES = LORA_CHUNK + LORA_CHUNK_ROWS * 4;  // with the rows' base values
+constexpr int LORA_SMEM = LORA_WARPS * LORA_STAGES * LORA_STAGE_BYTES;
 
 struct LoraArgs {
     const float *x, *base;
@@ -33,7 +43,9 @@ struct LoraArgs {
     int rows, K, rank, adapters;
     int shares;       // clusters per vector
     int lanes_shift;  // log2 of the lanes that share a row of B
+    int chunk_rows;   // rows of B in a full copy
     unsigned *err;
+    uint64_t wait_ns;
 };
 
 __device__ __forceinline__ float2 widen(uint32_t w, __half) { return __half22float2(*reinterpret_cast<__half2 *>(&w)); }
@@ -62,11 +74,21 @@ __global__ void __launch_bounds__(LORA_WARPS * 32, 1) lora_add_kernel(const Lora
 {
     __shared__ __align__(16) float s_part[LORA_CLUSTER][QMD_LORA_MAX_RANK];
     __shared__ __align__(16) float s_t[QMD_LORA_MAX_RANK];
+    __shared__ __align__(8) uint64_t s_bar[LORA_WARPS][LORA_STAGES];
+    extern __shared__ __align__(16) unsigned char s_ring[];
     // every CTA of the cluster runs before its shared memory is written from another
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t bar0 = smem_addr(&s_bar[warp][0]);
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < LORA_STAGES; ++i)
+            mbar_init(bar0 + 8 * i, 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x % LORA_CLUSTER, cl = blockIdx.x / LORA_CLUSTER;
     const int v = cl / a.shares, share = cl % a.shares;
     const int id = a.adapter[v];
@@ -85,6 +107,30 @@ __global__ void __launch_bounds__(LORA_WARPS * 32, 1) lora_add_kernel(const Lora
                 out[i] = base[i];
         return;
     }
+
+    // ---- this warp's chunks of the CTA's rows of B, and of base -----------------------------------
+    const T *B = static_cast<const T *>(a.B) + (int64_t)id * a.rows * a.rank;
+    unsigned char *ring = s_ring + warp * LORA_STAGES * LORA_STAGE_BYTES;
+    const int nchunks = (r1 - r0 + a.chunk_rows - 1) / a.chunk_rows;
+    auto ask = [&](int j) {  // chunk j of the CTA into this warp's stage (j / LORA_WARPS) % LORA_STAGES
+        if (j < nchunks) {
+            const int stage = j / LORA_WARPS % LORA_STAGES;
+            const int row = r0 + j * a.chunk_rows, n = min(a.chunk_rows, r1 - row);
+            const uint32_t dst = smem_addr(ring + stage * LORA_STAGE_BYTES);
+            if (lane == 0) {
+                const uint32_t bytes = (uint32_t)(n * a.rank * 2);
+                mbar_arrive_expect_tx(bar0 + 8 * stage, bytes);
+                bulk_copy_g2s(dst, B + (int64_t)row * a.rank, bytes, bar0 + 8 * stage);
+            }
+            for (int i = lane; i < n; i += 32)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + LORA_CHUNK + 4 * i), "l"(base + row + i)
+                             : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < LORA_STAGES; ++i)
+        ask(warp + i * LORA_WARPS);
 
     // ---- A x over this CTA's eighth of K, in pieces of 32 ---------------------------------------
     const int pieces = a.K / 32;
@@ -105,18 +151,6 @@ __global__ void __launch_bounds__(LORA_WARPS * 32, 1) lora_add_kernel(const Lora
             if (warp + LORA_WARPS * i < a.rank)  // (x may be NaN or infinite: 0 times it is not 0)
                 acc[i] = dot8<T>(u[i], x0, x1, acc[i]);
     }
-
-    // the first loads of this CTA's rows of B, while the sums meet
-    const int per = 1 << a.lanes_shift, sub = lane & (per - 1), chunks = a.rank / 8;
-    const int step = LORA_WARPS * 32 >> a.lanes_shift;  // rows the CTA takes at once
-    const int my = r0 + (int)(threadIdx.x >> a.lanes_shift);
-    const T *B = static_cast<const T *>(a.B) + (int64_t)id * a.rows * a.rank;
-    auto load_b = [&](int row, int ch) { return *reinterpret_cast<const uint4 *>(B + (int64_t)row * a.rank + 8 * ch); };
-    uint4 w[LORA_AHEAD];
-#pragma unroll
-    for (int i = 0; i < LORA_AHEAD; ++i)
-        if (my + i * step < r1)
-            w[i] = load_b(my + i * step, sub);
 
 #pragma unroll
     for (int i = 0; i < NR; ++i)
@@ -148,43 +182,79 @@ __global__ void __launch_bounds__(LORA_WARPS * 32, 1) lora_add_kernel(const Lora
     // ---- this CTA's rows of B --------------------------------------------------------------------
     const float s = a.scale[id];
     const float4 *t4 = reinterpret_cast<const float4 *>(s_t);
+    const int per = 1 << a.lanes_shift, sub = lane & (per - 1), pieces_b = a.rank / 8;
+    const int at_once = 32 >> a.lanes_shift;  // rows of a pass
     const float4 ta = t4[2 * sub], tb = t4[2 * sub + 1];  // the lane's first piece, the only one of most ranks
-    const int first = r0 + (warp * 32 >> a.lanes_shift);  // the warp's first row
-    for (int off = 0; first + off < r1; off += LORA_AHEAD * step) {
-        const int row = my + off;
-        float y[LORA_AHEAD];
+    uint32_t phase = 0;
+    for (int j = warp, stage = 0; j < nchunks; j += LORA_WARPS) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(LORA_STAGES - 1) : "memory");
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar0 + 8 * stage, phase, a.wait_ns))) {
+            // flag it, wait (bounded) for the copies that may be in flight, leave the rest out
+            if (lane == 0) {
+                atomicOr(a.err, (unsigned)ERRBIT_QMV_WAIT);
+                for (int i = 0; i < LORA_STAGES && j + i * LORA_WARPS < nchunks; ++i) {
+                    if (!mbar_wait_bounded(bar0 + 8 * stage, phase, a.wait_ns))
+                        atomicOr(a.err, (unsigned)ERRBIT_DRAIN_WAIT);
+                    stage = stage + 1 == LORA_STAGES ? 0 : stage + 1;
+                    phase = stage == 0 ? phase ^ 1u : phase;
+                }
+            }
+            break;
+        }
+        __syncwarp();  // every lane's base values have landed
+        const unsigned char *st = ring + stage * LORA_STAGE_BYTES;
+        const float *bs = reinterpret_cast<const float *>(st + LORA_CHUNK);
+        const int row = r0 + j * a.chunk_rows, n = min(a.chunk_rows, r1 - row);
+        float y[LORA_PASSES];
 #pragma unroll
-        for (int i = 0; i < LORA_AHEAD; ++i) {
-            const int r = row + i * step;
+        for (int i = 0; i < LORA_PASSES; ++i) {
+            const int r = i * at_once + (lane >> a.lanes_shift);
             y[i] = 0.0f;
-            if (r < r1) {
-                y[i] = dot8<T>(w[i], ta, tb, 0.0f);
-                for (int ch = sub + per; ch < chunks; ch += per)
-                    y[i] = dot8<T>(load_b(r, ch), t4[2 * ch], t4[2 * ch + 1], y[i]);
+            if (r < n) {
+                const uint4 *w = reinterpret_cast<const uint4 *>(st + r * a.rank * 2);
+                y[i] = dot8<T>(w[sub], ta, tb, 0.0f);
+                for (int ch = sub + per; ch < pieces_b; ch += per)
+                    y[i] = dot8<T>(w[ch], t4[2 * ch], t4[2 * ch + 1], y[i]);
             }
         }
-        // the next rows' loads
 #pragma unroll
-        for (int i = 0; i < LORA_AHEAD; ++i)
-            if (row + (LORA_AHEAD + i) * step < r1)
-                w[i] = load_b(row + (LORA_AHEAD + i) * step, sub);
-#pragma unroll
-        for (int i = 0; i < LORA_AHEAD; ++i) {
+        for (int i = 0; i < LORA_PASSES; ++i) {
             for (int o = per >> 1; o > 0; o >>= 1)
                 y[i] += __shfl_xor_sync(0xffffffffu, y[i], o);
-            const int r = row + i * step;
-            if (sub == 0 && r < r1)
-                out[r] = fmaf(s, y[i], base[r]);
+            // of the rows that a group of lanes holds, lane sub adds and writes rows sub, sub + per, ..
+            const int r = i * at_once + (lane >> a.lanes_shift);
+            if ((i & (per - 1)) == sub && r < n)
+                out[row + r] = fmaf(s, y[i], bs[r]);
         }
+        fence_proxy_async_smem();
+        __syncwarp();  // every lane has read the stage that is asked for again
+        ask(j + LORA_STAGES * LORA_WARPS);
+        stage = stage + 1 == LORA_STAGES ? 0 : stage + 1;
+        phase = stage == 0 ? phase ^ 1u : phase;
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <class T, int NR>
-static cudaError_t launch_lora(const LoraArgs &a, int batch, cudaStream_t s)
+static cudaError_t launch_lora(const LoraArgs &a, int batch, int device, cudaStream_t s)
 {
+    {
+        // opt in to the rings' shared memory once per device; host threads may race here
+        static std::mutex mu;
+        static bool opted[64] = {false};
+        std::lock_guard<std::mutex> lock(mu);
+        if (!opted[device]) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(lora_add_kernel<T, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, LORA_SMEM);
+            if (e != cudaSuccess)
+                return e;
+            opted[device] = true;
+        }
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(batch * a.shares * LORA_CLUSTER));
     cfg.blockDim = dim3(LORA_WARPS * 32);
+    cfg.dynamicSmemBytes = LORA_SMEM;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -199,20 +269,20 @@ static cudaError_t launch_lora(const LoraArgs &a, int batch, cudaStream_t s)
 }
 
 template <class T>
-static cudaError_t launch_lora_rank(const LoraArgs &a, int batch, cudaStream_t s)
+static cudaError_t launch_lora_rank(const LoraArgs &a, int batch, int device, cudaStream_t s)
 {
     const int nr = (a.rank + LORA_WARPS - 1) / LORA_WARPS;
-    return nr <= 1   ? launch_lora<T, 1>(a, batch, s)
-           : nr <= 2 ? launch_lora<T, 2>(a, batch, s)
-           : nr <= 4 ? launch_lora<T, 4>(a, batch, s)
-                     : launch_lora<T, 8>(a, batch, s);
+    return nr <= 1   ? launch_lora<T, 1>(a, batch, device, s)
+           : nr <= 2 ? launch_lora<T, 2>(a, batch, device, s)
+           : nr <= 4 ? launch_lora<T, 4>(a, batch, device, s)
+                     : launch_lora<T, 8>(a, batch, device, s);
 }
 
 qmd_status launch_lora_add(qmd_half type, const float *x, const float *base, const void *A, const void *B,
                            const float *scale, const int32_t *adapter, float *out, int64_t K, int64_t rows, int rank,
                            int adapters, int batch, const DeviceInfo &dev, unsigned *err, cudaStream_t s)
 {
-    LoraArgs a = {x, base, A, B, scale, adapter, out, (int)rows, (int)K, rank, adapters, 1, 0, err};
+    LoraArgs a = {x, base, A, B, scale, adapter, out, (int)rows, (int)K, rank, adapters, 1, 0, LORA_CHUNK / (rank * 2), err, wait_limit_ns()};
     // clusters per vector: as many as fill the SMs, while a CTA keeps at least 64 rows
     const int most = (int)((rows + 64 * LORA_CLUSTER - 1) / (64 * LORA_CLUSTER));
     a.shares = dev.sm_count / LORA_CLUSTER / batch;
@@ -220,7 +290,8 @@ qmd_status launch_lora_add(qmd_half type, const float *x, const float *base, con
     // lanes to a row of B: the largest power of two that divides the row's 16-byte pieces
     while (a.lanes_shift < 4 && (rank / 8) % (2 << a.lanes_shift) == 0)
         ++a.lanes_shift;
-    const cudaError_t e = type == QMD_F16 ? launch_lora_rank<__half>(a, batch, s) : launch_lora_rank<__nv_bfloat16>(a, batch, s);
+    const cudaError_t e = type == QMD_F16 ? launch_lora_rank<__half>(a, batch, dev.device, s)
+                                          : launch_lora_rank<__nv_bfloat16>(a, batch, dev.device, s);
     return e == cudaSuccess ? QMD_OK : fail(QMD_ERR_LAUNCH, "lora_add launch", e);
 }
 

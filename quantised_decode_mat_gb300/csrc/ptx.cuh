@@ -120,6 +120,15 @@ __device__ __forceinline__ void bulk_copy_g2s(uint32_t dst, const void *src, uin
         : "memory");
 }
 
+// The same with the default L2 policy.
+__device__ __forceinline__ void bulk_copy_g2s(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
 // 2-D tiled tensor copy (TMA) global -> this CTA's shared memory: the box the tensor map
 // describes, starting at element coordinates (x, y), completing the box's bytes on the barrier.
 // x times the element size must be a multiple of 16 bytes; dst 128-byte aligned.
