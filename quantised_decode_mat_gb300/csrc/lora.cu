@@ -10,9 +10,14 @@
 // x with all rows of A, the partial sums go to all 8 CTAs' shared memory, and after the cluster's
 // barrier each CTA adds the eighths in order and multiplies its rows of B.  Those come by bulk
 // copies, 4 KB of whole rows at a time into a ring of each warp, the first of them asked for before
-// A x is begun (registers hold 32 KB a CTA less: 14.5 us for 8 adapters of rank 64 on 28672 x 4096).
-// With few vectors several clusters share a vector's rows; each then
-// computes A x for itself (A is small beside B, and comes from L2).
+// A x is begun.  With few vectors several clusters share a vector's rows; each then computes A x for
+// itself (A is small beside B, and comes from L2).
+//
+// B (A x) runs on the tensor cores (mma.sync m16n8k16, 16 rows of B by columns that hold the parts
+// of t = A x: two f16 parts of t over a power of two, or three bf16 parts, 22 or 24 bits; f32 sums):
+// as f32 multiply-adds it took 45 instructions for 512 bytes and set the time (8 adapters of rank 64
+// on 28672 x 4096: 13.2 us).  The order of the ranks inside a product is free, so a lane takes 16
+// neighbouring bytes of a row for two products.
 #include <mutex>
 
 #include <cuda_bf16.h>
@@ -29,8 +34,6 @@ constexpr int LORA_WARPS = 16;
 constexpr int LORA_STAGES = 2;
 constexpr int LORA_CHUNK = 4096;                // bytes of B's rows that a copy takes, at most
 constexpr int LORA_CHUNK_ROWS = LORA_CHUNK / 16;  // and the most rows in them
-constexpr int LORA_PASSES = 8;                  // passes of 32 lanes over a chunk, at most (512 bytes each where
-                                                // the row's pieces are a power of two, else more)
 constexpr int LORA_STAGE_BYTES = LORA_CHUNK + LORA_CHUNK_ROWS * 4;  // with the rows' base values
 constexpr int LORA_SMEM = LORA_WARPS * LORA_STAGES * LORA_STAGE_BYTES;
 
@@ -42,7 +45,6 @@ struct LoraArgs {
     float *out;
     int rows, K, rank, adapters;
     int shares;       // clusters per vector
-    int lanes_shift;  // log2 of the lanes that share a row of B
     int chunk_rows;   // rows of B in a full copy
     unsigned *err;
     uint64_t wait_ns;
@@ -66,6 +68,34 @@ __device__ __forceinline__ float dot8(const uint4 &u, const float4 &a, const flo
     acc = fmaf(f.x, b.x, acc), acc = fmaf(f.y, b.y, acc);
     f = widen(u.w, T());
     return fmaf(f.y, b.w, fmaf(f.x, b.z, acc));
+}
+
+// The parts of a value of t that columns 0, 1 (and 2) hold.
+constexpr float LORA_LOW = 1.0f / 2048.0f;
+__device__ __forceinline__ uint32_t part_bits(float x, int col, __half)
+{
+    const __half h = __float2half_rn(x), l = __float2half_rn((x - __half2float(h)) * 2048.0f);
+    return __half_as_ushort(col == 0 ? h : col == 1 ? l : __half(0.0f));
+}
+__device__ __forceinline__ uint32_t part_bits(float x, int col, __nv_bfloat16)
+{
+    const __nv_bfloat16 h = __float2bfloat16_rn(x);
+    const float r = x - __bfloat162float(h);
+    const __nv_bfloat16 m = __float2bfloat16_rn(r), l = __float2bfloat16_rn(r - __bfloat162float(m));
+    return __bfloat16_as_ushort(col == 0 ? h : col == 1 ? m : col == 2 ? l : __nv_bfloat16(0.0f));
+}
+
+__device__ __forceinline__ void mma_half(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_half(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __nv_bfloat16)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // NR: rows of A that a warp multiplies (rank / 16, rounded up)
@@ -180,11 +210,33 @@ __global__ void __launch_bounds__(LORA_WARPS * 32, 1) lora_add_kernel(const Lora
     __syncthreads();
 
     // ---- this CTA's rows of B --------------------------------------------------------------------
-    const float s = a.scale[id];
-    const float4 *t4 = reinterpret_cast<const float4 *>(s_t);
-    const int per = 1 << a.lanes_shift, sub = lane & (per - 1), pieces_b = a.rank / 8;
-    const int at_once = 32 >> a.lanes_shift;  // rows of a pass
-    const float4 ta = t4[2 * sub], tb = t4[2 * sub + 1];  // the lane's first piece, the only one of most ranks
+    float s = a.scale[id];
+    // Lane (g, t) holds column g of the products' second operand: the parts of ranks 8 (t + 4 i) + 0..7
+    // of group i, zeros past the rank and in the columns without a part.
+    constexpr bool F16 = sizeof(T) == 2 && __is_same(T, __half);
+    constexpr int NI = (NR * LORA_WARPS + 31) / 32;  // groups of 32 ranks
+    const int g = lane >> 2, q = lane & 3, pieces_b = a.rank / 8;
+    float up = 1.0f;  // f16: t is taken over a power of two, its largest value in [0.5, 1)
+    if constexpr (F16) {
+        float top = 0.0f;
+        for (int i = lane; i < a.rank; i += 32)
+            top = fmaxf(top, fabsf(s_t[i]));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int ex = min(252, (int)(__float_as_uint(top) >> 23));
+        up = __uint_as_float((uint32_t)(253 - ex) << 23);
+        s *= __uint_as_float((uint32_t)max(1, ex + 1) << 23);
+    }
+    uint32_t tb[NI][4];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int r = 8 * (q + 4 * i) + 2 * w;
+            tb[i][w] = q + 4 * i < pieces_b
+                           ? part_bits(s_t[r] * up, g, T()) | part_bits(s_t[r + 1] * up, g, T()) << 16 : 0u;
+        }
     uint32_t phase = 0;
     for (int j = warp, stage = 0; j < nchunks; j += LORA_WARPS) {
         asm volatile("cp.async.wait_group %0;" ::"n"(LORA_STAGES - 1) : "memory");
@@ -205,26 +257,31 @@ __global__ void __launch_bounds__(LORA_WARPS * 32, 1) lora_add_kernel(const Lora
         const unsigned char *st = ring + stage * LORA_STAGE_BYTES;
         const float *bs = reinterpret_cast<const float *>(st + LORA_CHUNK);
         const int row = r0 + j * a.chunk_rows, n = min(a.chunk_rows, r1 - row);
-        float y[LORA_PASSES];
+        for (int r = 0; r < n; r += 16) {
+            // rows r + g and r + g + 8 (past n the last row again, not written)
+            float c[4] = {};
+            const unsigned char *wa = st + min(r + g, n - 1) * a.rank * 2, *wb = st + min(r + g + 8, n - 1) * a.rank * 2;
 #pragma unroll
-        for (int i = 0; i < LORA_PASSES; ++i) {
-            const int r = i * at_once + (lane >> a.lanes_shift);
-            y[i] = 0.0f;
-            if (r < n) {
-                const uint4 *w = reinterpret_cast<const uint4 *>(st + r * a.rank * 2);
-                y[i] = dot8<T>(w[sub], ta, tb, 0.0f);
-                for (int ch = sub + per; ch < pieces_b; ch += per)
-                    y[i] = dot8<T>(w[ch], t4[2 * ch], t4[2 * ch + 1], y[i]);
+            for (int i = 0; i < NI; ++i) {
+                const bool has = q + 4 * i < pieces_b;
+                const uint4 x0 = has ? lds128(wa + 16 * (q + 4 * i)) : make_uint4(0, 0, 0, 0);
+                const uint4 x1 = has ? lds128(wb + 16 * (q + 4 * i)) : make_uint4(0, 0, 0, 0);
+                const uint32_t f0[4] = {x0.x, x1.x, x0.y, x1.y}, f1[4] = {x0.z, x1.z, x0.w, x1.w};
+                mma_half(c, f0, tb[i][0], tb[i][1], T());
+                mma_half(c, f1, tb[i][2], tb[i][3], T());
             }
-        }
-#pragma unroll
-        for (int i = 0; i < LORA_PASSES; ++i) {
-            for (int o = per >> 1; o > 0; o >>= 1)
-                y[i] += __shfl_xor_sync(0xffffffffu, y[i], o);
-            // of the rows that a group of lanes holds, lane sub adds and writes rows sub, sub + per, ..
-            const int r = i * at_once + (lane >> a.lanes_shift);
-            if ((i & (per - 1)) == sub && r < n)
-                out[row + r] = fmaf(s, y[i], bs[r]);
+            float ya, yb;
+            if constexpr (F16) {
+                ya = fmaf(c[1], LORA_LOW, c[0]);
+                yb = fmaf(c[3], LORA_LOW, c[2]);
+            } else {
+                ya = c[0] + (c[1] + __shfl_down_sync(0xffffffffu, c[0], 1));
+                yb = c[2] + (c[3] + __shfl_down_sync(0xffffffffu, c[2], 1));
+            }
+            if (q == 0 && r + g < n)
+                out[row + r + g] = fmaf(s, ya, bs[r + g]);
+            if (q == 0 && r + g + 8 < n)
+                out[row + r + g + 8] = fmaf(s, yb, bs[r + g + 8]);
         }
         fence_proxy_async_smem();
         __syncwarp();  // every lane has read the stage that is asked for again
@@ -282,14 +339,11 @@ qmd_status launch_lora_add(qmd_half type, const float *x, const float *base, con
                            const float *scale, const int32_t *adapter, float *out, int64_t K, int64_t rows, int rank,
                            int adapters, int batch, const DeviceInfo &dev, unsigned *err, cudaStream_t s)
 {
-    LoraArgs a = {x, base, A, B, scale, adapter, out, (int)rows, (int)K, rank, adapters, 1, 0, LORA_CHUNK / (rank * 2), err, wait_limit_ns()};
+    LoraArgs a = {x, base, A, B, scale, adapter, out, (int)rows, (int)K, rank, adapters, 1, LORA_CHUNK / (rank * 2), err, wait_limit_ns()};
     // clusters per vector: as many as fill the SMs, while a CTA keeps at least 64 rows
     const int most = (int)((rows + 64 * LORA_CLUSTER - 1) / (64 * LORA_CLUSTER));
     a.shares = dev.sm_count / LORA_CLUSTER / batch;
     a.shares = a.shares < 1 ? 1 : a.shares > most ? most : a.shares;
-    // lanes to a row of B: the largest power of two that divides the row's 16-byte pieces
-    while (a.lanes_shift < 4 && (rank / 8) % (2 << a.lanes_shift) == 0)
-        ++a.lanes_shift;
     const cudaError_t e = type == QMD_F16 ? launch_lora_rank<__half>(a, batch, dev.device, s)
                                           : launch_lora_rank<__nv_bfloat16>(a, batch, dev.device, s);
     return e == cudaSuccess ? QMD_OK : fail(QMD_ERR_LAUNCH, "lora_add launch", e);
