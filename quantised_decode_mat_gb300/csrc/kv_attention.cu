@@ -85,10 +85,11 @@ struct AttnArgs {
 };
 
 // Warps, ring depth and shared memory of an instance.
-template <int D, int NT>
+template <int D, int R>
 struct AttnCfg {
-    static constexpr int R = 4 * NT;
-    static constexpr int W = D == 256 ? (NT == 1 ? 6 : 5) : NT == 1 ? 14 : NT == 2 ? (D == 64 ? 12 : 10) : 7;
+    // up to 4 query rows: columns of the products, two to a row; up to 8 or 16: their rows
+    static constexpr bool WIDE = R > 4;
+    static constexpr int W = D == 256 ? (R == 4 ? 6 : 5) : R == 4 ? 14 : D == 64 ? (R == 8 ? 14 : 12) : 8;
     static constexpr int STAGES = 3;
     static constexpr int META = 64 * 16;  // block index and scales of two chunks of 32 blocks
     static constexpr int BOX = D < 128 ? D : 128;  // bytes of a row that one copy takes
@@ -96,10 +97,10 @@ struct AttnCfg {
     static constexpr int BLOCK_BYTES = 32 * D;  // keys and values of 16 positions
     static constexpr int RING = STAGES * BLOCK_BYTES;
     static constexpr int SLOT = R * D * 4;
-    // query fragments stay in registers until the sums alone take 64 of them
-    static constexpr bool PIPE = NT <= 2;
-    static constexpr bool QS = R * D >= 1024;
+    // query fragments stay in registers but for 256 dimensions, whose sums take 64 or 128 of them
+    static constexpr bool QS = D == 256;
     static constexpr int QBYTES = QS ? R * D * 4 : 0;  // two f16 parts
+    static constexpr int QN = D / 16 * (R == 4 ? 2 : R == 8 ? 4 : 8);  // registers of them
     static_assert(RING >= SLOT, "a warp's last part lies in its ring");
     // rings, first parts, query fragments, maxima and sums of 2 W parts and W + 1 joins, jobs,
     // barriers, scans
@@ -153,6 +154,17 @@ __device__ __forceinline__ void split_f16(float x, float y, uint32_t &px, uint32
     py = __byte_perm(hw, lw, 0x7632);
 }
 
+// The same as two pairs, the rest at its own size: for values up to 2^15 that matter down to 2^-31 of
+// the largest.
+__device__ __forceinline__ void split_pairs(float x, float y, uint32_t &hi, uint32_t &lo)
+{
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 b = __half22float2(h);
+    const __half2 l = __floats2half2_rn(x - b.x, y - b.y);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
 constexpr float LOW_PART = 1.0f / 2048.0f;
 
 struct Group {  // the rows of a row group and what they see
@@ -195,14 +207,17 @@ struct AttnMaps {  // the pools as [block][16][head_dim] bytes
     CUtensorMap k, v;
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
+template <int D, int R>
+__global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
     kv_attention_kernel(const AttnArgs a, const __grid_constant__ AttnMaps maps)
 {
-    using C = AttnCfg<D, NT>;
-    constexpr int R = C::R, W = C::W, S = C::STAGES;
+    using C = AttnCfg<D, R>;
+    constexpr int W = C::W, S = C::STAGES;
     constexpr int KH = D / 64;   // 64-byte parts of a key, 16 bytes to a lane
     constexpr int MT = D / 16;   // 16-row tiles of V^T
+    constexpr bool WIDE = C::WIDE;
+    constexpr int QR = R == 16 ? 2 : 1;          // query rows whose scores a lane holds
+    constexpr int OT = WIDE ? 2 * MT : MT, CT = WIDE ? 2 : 1;  // tiles of sums, of scores
     constexpr int VW = D / 32;   // words of a value row that a lane holds
     extern __shared__ __align__(1024) unsigned char smem[];
     float2 *s_ml = reinterpret_cast<float2 *>(smem + W * (C::RING + C::SLOT + C::QBYTES + C::META));  // [W][2][R] maximum, weight sum
@@ -353,16 +368,18 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
         }
         int rem = at - pre;
         const KvSeq sq = seq_at(s);
-        int nb;
+        // the row groups of a head lie together: they read the same keys and values
+        const int of_head = (few ? __shfl_sync(0xffffffffu, my_units, s) : s_pre[s + 1] - pre) / p.heads;
+        head = rem / of_head;
+        rem -= head * of_head;
         for (;; ++cg) {
             const Group gr = group_of<R>(a, sq, cg);
-            nb = max(1, gr.hi - gr.lo);
-            if (rem < p.heads * nb)
+            const int nb = max(1, gr.hi - gr.lo);
+            if (rem < nb)
                 break;
-            rem -= p.heads * nb;
+            rem -= nb;
         }
-        head = rem / nb;
-        b0 = rem - head * nb;
+        b0 = rem;
     }
     while (u < w1) {
         const KvSeq sq = seq_at(s);
@@ -387,19 +404,17 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
         };
         const int page_c = page_of(lane), page_n = page_of(32 + lane);
         int page_nn = page_of(64 + lane);
-        // lane (g, t) holds columns g of the query tiles, dimensions 64 h + 16 t + 0..15; a column past
-        // the rows repeats the last one
-        float x[NT][KH][16];
-        auto load_q = [&](int nt) {
-            const int r = cg * R + min(4 * nt + (g >> 1), gr.rows - 1);
+        // lane (g, t) takes dimensions 64 h + 16 t + 0..15 of a query row: that of column g (two columns to
+        // a row), or rows g and g + 8; past the rows the last one again
+        float x[QR][KH][16];
+#pragma unroll
+        for (int i = 0; i < QR; ++i) {
+            const int r = cg * R + min(WIDE ? g + 8 * i : g >> 1, gr.rows - 1);
             const float *qp = a.q + row_offset(a, sq.row0, head, r, a.q_stride, D) + 16 * t;
 #pragma unroll
             for (int h = 0; h < KH; ++h)
-                load_f32(x[nt][h], qp + 64 * h);
-        };
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            load_q(nt);
+                load_f32(x[i][h], qp + 64 * h);
+        }
         int bi_n = block_of(lane, page_c);
         float ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
         int bi_1 = -1;
@@ -408,6 +423,7 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
             bi_1 = block_of(32 + lane, page_n);
             ks_1 = bi_1 >= 0 ? p.ks[bi_1] : 0.0f, vs_1 = bi_1 >= 0 ? p.vs[bi_1] : 0.0f;
         }
+        fence_proxy_async_smem();
         __syncwarp();  // every lane has read the last item's
         meta[lane] = make_int4(bi_n, __float_as_int(ks_n), __float_as_int(vs_n), 0);
         meta[32 + lane] = make_int4(bi_1, __float_as_int(ks_1), __float_as_int(vs_1), 0);
@@ -443,64 +459,83 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
         }
 
         // ---- the queries as two f16 parts ------------------------------------------------------
-        uint32_t qf[C::QS ? 1 : NT][KH * 4][2];
-        float qscale[NT];  // of query row 4 nt + t
+        uint32_t qf[C::QN];   // of word w of part h: [4 h + w][column] or [4 h + w][row, dimension]
+        float qscale[QR];     // of query row t, or rows g and g + 8
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int i = 0; i < QR; ++i) {
             float top = 0.0f;
 #pragma unroll
             for (int h = 0; h < KH; ++h)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    top = fmaxf(top, fabsf(x[nt][h][e]));
+                    top = fmaxf(top, fabsf(x[i][h][e]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // q times a power of two, the largest value in [0.5, 1)
-            const int ex = min(252, (int)(__float_as_uint(top) >> 23));
-            const float f = __uint_as_float((uint32_t)(253 - ex) << 23);
+            // q times a power of two: the largest value in [0.5, 1), or in [2^14, 2^15)
+            const int ex = (int)(__float_as_uint(top) >> 23);
+            const int field = WIDE ? min(253, 268 - ex) : min(253, max(1, 253 - ex));
+            const float f = __uint_as_float((uint32_t)field << 23);
+            const float back = __uint_as_float((uint32_t)(254 - field) << 23) * a.scale_log2e;
 #pragma unroll
             for (int h = 0; h < KH; ++h)
 #pragma unroll
                 for (int w = 0; w < 4; ++w)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        uint32_t lo, hi;
-                        split_f16(x[nt][h][4 * w + 2 * e] * f, x[nt][h][4 * w + 2 * e + 1] * f, lo, hi);
-                        qf[C::QS ? 0 : nt][4 * h + w][e] = __byte_perm(lo, hi, (g & 1) ? 0x7632 : 0x5410);
+                        const float x0 = x[i][h][4 * w + 2 * e] * f, x1 = x[i][h][4 * w + 2 * e + 1] * f;
+                        uint32_t hi, lo;
+                        if constexpr (!WIDE) {
+                            split_f16(x0, x1, lo, hi);
+                            qf[(4 * h + w) * 2 + e] = __byte_perm(lo, hi, (g & 1) ? 0x7632 : 0x5410);
+                        } else {
+                            split_pairs(x0, x1, hi, lo);
+                            if constexpr (R == 8) {  // rows 0-7 the first parts, rows 8-15 the second
+                                qf[(4 * h + w) * 4 + 2 * e] = hi;
+                                qf[(4 * h + w) * 4 + 2 * e + 1] = lo;
+                            } else {
+                                qf[(4 * h + w) * 8 + 2 * e + i] = hi;
+                                qf[(4 * h + w) * 8 + 4 + 2 * e + i] = lo;
+                            }
+                        }
                     }
-            if constexpr (C::QS) {
-                uint4 *dst = reinterpret_cast<uint4 *>(smem + W * (C::RING + C::SLOT) + warp * C::QBYTES) + lane;
-#pragma unroll
-                for (int i = 0; i < KH * 2; ++i)
-                    dst[(nt * KH * 2 + i) * 32] =
-                        make_uint4(qf[0][2 * i][0], qf[0][2 * i][1], qf[0][2 * i + 1][0], qf[0][2 * i + 1][1]);
-            }
-            const float back = __uint_as_float((uint32_t)max(1, ex + 1) << 23) * a.scale_log2e;
-            qscale[nt] = __shfl_sync(0xffffffffu, back, 8 * t);
+            qscale[i] = WIDE ? back : __shfl_sync(0xffffffffu, back, 8 * t);
         }
+        uint4 *q_keep = reinterpret_cast<uint4 *>(smem + W * (C::RING + C::SLOT) + warp * C::QBYTES) + lane;
+        if constexpr (C::QS) {
+#pragma unroll
+            for (int i = 0; i < C::QN / 4; ++i)
+                q_keep[i * 32] = make_uint4(qf[4 * i], qf[4 * i + 1], qf[4 * i + 2], qf[4 * i + 3]);
+        }
+        auto query = [&](int i) {  // registers 4 i .. 4 i + 3 of the fragments
+            if constexpr (C::QS)
+                return q_keep[i * 32];
+            else
+                return make_uint4(qf[4 * i], qf[4 * i + 1], qf[4 * i + 2], qf[4 * i + 3]);
+        };
         // positions in [all_from, all_to) are seen by every row of the group
         const int all_to = row_end(sq, cg * R / a.by_group);
         const int all_from = row_begin(a, row_end(sq, (cg * R + gr.rows - 1) / a.by_group));
 
-        float o[NT][MT][4];
-        float m[NT], l[NT];
-        float vref = 1.17549435e-38f, vinv = 8.50705917e37f;  // 2^-126, 2^126
+        float o[OT][4];
+        float m[QR], l[QR];
+        // value scales are taken over vref; wide rows' weights times 2^6 besides, so that what f16 loses
+        // below its smallest value is 2^-31 of the largest weight
+        constexpr float LIFT = WIDE ? 64.0f : 1.0f;
+        float vref = 7.52316385e-37f, vinv = 1.32922800e36f * LIFT;  // 2^-120, 2^120
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            m[nt] = ATT_NONE;
-            l[nt] = 0.0f;
+        for (int i = 0; i < QR; ++i)
+            m[i] = ATT_NONE, l[i] = 0.0f;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-                o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.0f;
-        }
+        for (int i = 0; i < OT; ++i)
+            o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
 
-        // S^T = K Q^T of the block in a ring stage
-        auto scores = [&](float (&c)[NT][4], const unsigned char *st) {
+        // the first product of the block in a ring stage: K Q^T (16 positions by columns), or Q K^T (rows
+        // by two tiles of 8 positions)
+        auto scores = [&](float (&c)[CT][4], const unsigned char *st) {
+            float c2[4] = {};  // two chains of sums
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                c[nt][0] = c[nt][1] = c[nt][2] = c[nt][3] = 0.0f;
-            // one column tile: two chains of sums
-            float c2[4] = {};
+            for (int i = 0; i < CT; ++i)
+                c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.0f;
 #pragma unroll
             for (int h = 0; h < KH; ++h) {
                 const unsigned char *kp = st + (h >> 1) * C::TILE + (k_at ^ (h & 1) << 6);
@@ -515,29 +550,31 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
                         f[e][0] = codes_f16<0x4140>(x), f[e][1] = codes_f16<0x4140>(y);
                         f[e][2] = codes_f16<0x4342>(x), f[e][3] = codes_f16<0x4342>(y);
                     }
+                    if constexpr (!WIDE) {
+                        const uint4 qv = query(2 * h + w2 / 2);
+                        mma_16816(c[0], f[0], qv.x, qv.y);
+                        mma_16816(c2, f[1], qv.z, qv.w);
+                    } else {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if constexpr (C::QS) {
-                            const uint4 qv = lds128(smem + W * (C::RING + C::SLOT) + warp * C::QBYTES + 16 * lane +
-                                                    (nt * KH * 2 + 2 * h + w2 / 2) * 512);
-                            mma_16816(c[nt], f[0], qv.x, qv.y);
-                            mma_16816(NT == 1 ? c2 : c[nt], f[1], qv.z, qv.w);
-                        } else {
-                            mma_16816(c[nt], f[0], qf[nt][4 * h + w2][0], qf[nt][4 * h + w2][1]);
-                            mma_16816(NT == 1 ? c2 : c[nt], f[1], qf[nt][4 * h + w2 + 1][0], qf[nt][4 * h + w2 + 1][1]);
-                        }
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int part = 0; part < R / 8; ++part) {
+                                const uint4 qv = query((4 * h + w2 + e) * (R / 8) + part);
+                                const uint32_t qa[4] = {qv.x, qv.y, qv.z, qv.w};
+                                mma_16816(c[0], qa, f[e][0], f[e][2]);
+                                mma_16816(c[CT - 1], qa, f[e][1], f[e][3]);
+                            }
                     }
                 }
             }
-
-            if (NT == 1)
+            if constexpr (!WIDE)
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     c[0][e] += c2[e];
         };
-        // With up to two column tiles, the next block's first product runs beside this block's weights and second product: two
-        // chains of dependent instructions for the scheduler instead of one.
-        float c[NT][4];
+        // The next block's first product runs beside this block's weights and second product: two chains
+        // of dependent instructions for the scheduler instead of one.
+        float c[CT][4];
         // wait for the block in stage use (phase use_phase), or the one after it
         auto landed = [&](uint32_t stage, uint32_t phase) {
             if (__all_sync(0xffffffffu, mbar_wait_bounded(bar0 + 8 * stage, phase, a.wait_ns)))
@@ -545,10 +582,8 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
             dead = true;
             return false;
         };
-        if constexpr (C::PIPE) {
-            if (real > 0 && landed(use, use_phase))
-                scores(c, ring + use * C::BLOCK_BYTES);
-        }
+        if (real > 0 && landed(use, use_phase))
+            scores(c, ring + use * C::BLOCK_BYTES);
         for (int idx = 0; idx < real && !dead; ++idx) {
             if ((idx & 31) == 0 && idx > 0 && idx + 32 < real) {
                 __syncwarp();
@@ -563,40 +598,47 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
             __syncwarp();  // every lane has read the stage that is asked for again
             issue(idx + S - 1, put);
             put = put + 1 == S ? 0 : put + 1;
-            float cn[NT][4];
-            if constexpr (C::PIPE) {
-                if (idx + 1 < real && !landed(next, next_phase))
-                    break;
-                scores(cn, ring + next * C::BLOCK_BYTES);  // past the last block: of what the ring holds, not used
-            } else {
-                if (!landed(use, use_phase))
-                    break;
-                scores(c, ring + use * C::BLOCK_BYTES);
-            }
+            float cn[CT][4];
+            if (idx + 1 < real && !landed(next, next_phase))
+                break;
+            scores(cn, ring + next * C::BLOCK_BYTES);  // past the last block: of what the ring holds, not used
             const int4 md = meta[idx & 63];
             const int bi = md.x;
             const float ks = __int_as_float(md.y), vs = __int_as_float(md.z);
             const unsigned char *st = ring + use * C::BLOCK_BYTES;
 
-            // scores of positions pos + rho and pos + rho + 8 against query row 4 nt + t, in log2 units
+            // The scores in log2 units.  sc[i][e] is of query row t at position pos + rho + 8 e; or of row
+            // g + 8 i at position pos + 8 (e >> 1) + (what rho deals to column 2 t + (e & 1)).
+            constexpr int SN = WIDE ? 4 : 2;
             const int pos = (first_blk + idx) * KV_BLOCK;
             const bool whole = pos >= all_from && pos + KV_BLOCK <= all_to && bi >= 0;
-            float sc[NT][2];
+            float sc[QR][SN];
             bool up = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float f = qscale[nt] * ks;
-                sc[nt][0] = fmaf(c[nt][1], LOW_PART, c[nt][0]) * f;
-                sc[nt][1] = fmaf(c[nt][3], LOW_PART, c[nt][2]) * f;
-                if (!whole) {
-                    const int end = row_end(sq, (cg * R + min(4 * nt + t, gr.rows - 1)) / a.by_group);
-                    const int begin = row_begin(a, end), j = pos + rho;
-                    if (bi < 0 || j < begin || j >= end)
-                        sc[nt][0] = -INFINITY;
-                    if (bi < 0 || j + 8 < begin || j + 8 >= end)
-                        sc[nt][1] = -INFINITY;
+            for (int i = 0; i < QR; ++i) {
+                const float f = qscale[i] * ks;
+                if constexpr (!WIDE) {
+                    sc[i][0] = fmaf(c[0][1], LOW_PART, c[0][0]) * f;
+                    sc[i][1] = fmaf(c[0][3], LOW_PART, c[0][2]) * f;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < SN; ++e)
+                        sc[i][e] = (R == 8 ? c[CT * e / SN][e & 1] + c[CT * e / SN][2 + (e & 1)]
+                                           : c[CT * e / SN][2 * i + (e & 1)]) * f;
                 }
-                up |= fmaxf(sc[nt][0], sc[nt][1]) > m[nt] + ATT_SLACK;
+                if (!whole) {
+                    const int end = row_end(sq, (cg * R + min(WIDE ? g + 8 * i : t, gr.rows - 1)) / a.by_group);
+                    const int begin = row_begin(a, end);
+#pragma unroll
+                    for (int e = 0; e < SN; ++e) {
+                        const int j = pos + (!WIDE ? rho + 8 * e : 8 * (e >> 1) + (D > 64 ? t + 4 * (e & 1) : 2 * t + (e & 1)));
+                        if (bi < 0 || j < begin || j >= end)
+                            sc[i][e] = -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < SN; ++e)
+                    up |= sc[i][e] > m[i] + ATT_SLACK;
             }
             if (__any_sync(0xffffffffu, up) || vs > vref) {
                 float fv = 1.0f;
@@ -604,39 +646,65 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
                     const float r = __uint_as_float((__float_as_uint(vs) + 0x7fffffu) & 0x7f800000u);
                     fv = vref / r;
                     vref = r;
-                    vinv = 1.0f / r;
+                    vinv = LIFT / r;
+                }
+                float fo[QR];
+#pragma unroll
+                for (int i = 0; i < QR; ++i) {
+                    float top = sc[i][0];
+#pragma unroll
+                    for (int e = 1; e < SN; ++e)
+                        top = fmaxf(top, sc[i][e]);
+                    // over the lanes that hold the row's other positions
+#pragma unroll
+                    for (int x = WIDE ? 1 : 4; x < (WIDE ? 4 : 32); x <<= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    const float mn = top > m[i] ? top : m[i];
+                    const float f = ex2(m[i] - mn);
+                    m[i] = mn;
+                    l[i] *= f;
+                    fo[i] = f * fv;
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float top = fmaxf(sc[nt][0], sc[nt][1]);
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    const float mn = top > m[nt] ? top : m[nt];
-                    const float f = ex2(m[nt] - mn);
-                    m[nt] = mn;
-                    l[nt] *= f;
-                    const float fo = f * fv;
+                for (int i = 0; i < OT; ++i)
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            o[nt][mt][e] *= fo;
-                }
+                    for (int e = 0; e < 4; ++e)
+                        o[i][e] *= fo[R == 16 ? e >> 1 : 0];
             }
             const float vr = vs * vinv;
-            uint32_t pb[NT][2];
+            // the weights, as the second product's operand: columns, or rows
+            uint32_t pb[WIDE ? R / 8 : 1][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float w0 = ex2(sc[nt][0] - m[nt]), w1 = ex2(sc[nt][1] - m[nt]);
-                l[nt] += w0 + w1;
-                uint32_t a0, a1;
-                split_f16(w0 * vr, w1 * vr, a0, a1);
-                pb[nt][0] = transpose_8x8(a0);
-                pb[nt][1] = transpose_8x8(a1);
+            for (int i = 0; i < QR; ++i) {
+                float w[SN];
+#pragma unroll
+                for (int e = 0; e < SN; ++e) {
+                    w[e] = ex2(sc[i][e] - m[i]);
+                    l[i] += w[e];
+                    w[e] *= vr;
+                }
+                if constexpr (!WIDE) {
+                    uint32_t a0, a1;
+                    split_f16(w[0], w[1], a0, a1);
+                    pb[0][0] = transpose_8x8(a0);
+                    pb[0][1] = transpose_8x8(a1);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        uint32_t hi, lo;
+                        split_pairs(w[(2 * n) % SN], w[(2 * n + 1) % SN], hi, lo);
+                        if constexpr (R == 8) {
+                            pb[0][2 * n] = hi;
+                            pb[0][2 * n + 1] = lo;
+                        } else {
+                            pb[0][2 * n + i] = hi;
+                            pb[(R / 8) - 1][2 * n + i] = lo;
+                        }
+                    }
+                }
             }
 
-            // O^T += V^T P^T
+            // the second product: V^T P^T (16 dimensions by columns), or P V (rows by 8 dimensions)
             const unsigned char *sv = st + 16 * D;
 #pragma unroll
             for (int y = 0; y < (VW + 3) / 4; ++y) {
@@ -661,19 +729,26 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
                                             codes_f16<0x4342>(e23)};
                     const uint32_t fb[4] = {codes_f16<0x4140>(f01), codes_f16<0x4342>(f01), codes_f16<0x4140>(f23),
                                             codes_f16<0x4342>(f23)};
+                    const int i = 8 * y + 2 * w;
+                    if constexpr (!WIDE) {
+                        mma_16816(o[i], fa, pb[0][0], pb[0][1]);
+                        mma_16816(o[i + 1], fb, pb[0][0], pb[0][1]);
+                    } else {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_16816(o[nt][8 * y + 2 * w], fa, pb[nt][0], pb[nt][1]);
-                        mma_16816(o[nt][8 * y + 2 * w + 1], fb, pb[nt][0], pb[nt][1]);
+                        for (int part = 0; part < R / 8; ++part) {
+                            mma_16816(o[(2 * i) % OT], pb[part % (WIDE ? R / 8 : 1)], fa[0], fa[2]);
+                            mma_16816(o[(2 * i + 1) % OT], pb[part % (WIDE ? R / 8 : 1)], fa[1], fa[3]);
+                            mma_16816(o[(2 * i + 2) % OT], pb[part % (WIDE ? R / 8 : 1)], fb[0], fb[2]);
+                            mma_16816(o[(2 * i + 3) % OT], pb[part % (WIDE ? R / 8 : 1)], fb[1], fb[3]);
+                        }
                     }
                 }
             }
-            if constexpr (C::PIPE)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int i = 0; i < CT; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        c[nt][e] = cn[nt][e];
+                for (int e = 0; e < 4; ++e)
+                    c[i][e] = cn[i][e];
             use = next;
             use_phase = next_phase;
         }
@@ -697,38 +772,37 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
         // ---- the item's part: finished, or laid down for the join --------------------------------
         const bool done = b0 == 0 && cnt == nb;
         const int part = b0 > 0 ? 0 : 1;
-        auto store_head = [&](float *o, const float (&y)[2 * MT]) {  // the lane's dimensions of a head
-            if constexpr (D == 64) {
-                store_f32(o + 8 * g, y);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 2 * MT; i += 4)
-                    *reinterpret_cast<float4 *>(o + (i >> 4) * 128 + 16 * rho + (i & 15)) =
-                        make_float4(y[i], y[i + 1], y[i + 2], y[i + 3]);
-            }
-        };
         float *dst = part == 0 ? slot0 : reinterpret_cast<float *>(ring);
         if (part == 1 && !done)
             __syncwarp();  // every lane has read the ring
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 4);
-            l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 8);
-            l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 16);
-            const int r = 4 * nt + t;
-            const float f = done ? (l[nt] == 0.0f ? 0.0f : vref / l[nt]) : vref;
-            float y[2 * MT];
+        for (int i = 0; i < QR; ++i) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                y[2 * mt] = fmaf(o[nt][mt][1], LOW_PART, o[nt][mt][0]) * f;
-                y[2 * mt + 1] = fmaf(o[nt][mt][3], LOW_PART, o[nt][mt][2]) * f;
-            }
-            if (!done) {
-                store_head(dst + r * D, y);
-                if (g == 0)
-                    s_ml[(warp * 2 + part) * R + r] = make_float2(m[nt], l[nt]);
-            } else if (r < gr.rows) {
-                store_head(a.out + row_offset(a, sq.row0, head, cg * R + r, a.out_stride, D), y);
+            for (int x = WIDE ? 1 : 4; x < (WIDE ? 4 : 32); x <<= 1)
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+            const int r = WIDE ? g + 8 * i : t;
+            const float f = (done ? (l[i] == 0.0f ? 0.0f : vref / l[i]) : vref) * (1.0f / LIFT);
+            if (!done && (WIDE ? t : g) == 0)
+                s_ml[(warp * 2 + part) * R + r] = make_float2(m[i], l[i]);
+            if (done && r >= gr.rows)
+                continue;
+            float *to = done ? a.out + row_offset(a, sq.row0, head, cg * R + r, a.out_stride, D) : dst + r * D;
+            // runs of RUN neighbouring dimensions: 16 of those that rho deals to a lane (of a 64-wide head
+            // 8), for columns 2 t and 2 t + 1 where rows are rows
+            constexpr int RUN = D == 64 ? 8 : 16;
+#pragma unroll
+            for (int n = 0; n < (WIDE ? 2 : 1); ++n) {
+                const int piece = WIDE ? (D == 64 ? 2 * t + n : t + 4 * n) : rho;
+#pragma unroll
+                for (int d = 0; d < D / 8; d += 4) {
+                    float y[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[e] = (!WIDE ? fmaf(o[(d + e) / 2 % OT][((d + e) & 1) * 2 + 1], LOW_PART, o[(d + e) / 2 % OT][((d + e) & 1) * 2])
+                                : R == 8 ? o[(d + e) % OT][n] + o[(d + e) % OT][2 + n]
+                                         : o[(d + e) % OT][2 * i + n]) * f;
+                    *reinterpret_cast<float4 *>(to + d / RUN * 128 + piece * RUN + d % RUN) = make_float4(y[0], y[1], y[2], y[3]);
+                }
             }
         }
         // the item's first cut in this CTA makes the job of joining it
@@ -743,10 +817,10 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
         }
         u += cnt;
         b0 = 0;
-        if (u < w1 && ++head == p.heads) {  // on to the next row group, or the next sequence with rows
-            head = 0;
-            if (++cg * R >= sq.n * a.group) {
-                cg = 0;
+        if (u < w1 && ++cg * R >= sq.n * a.group) {  // on to the next head, or the next sequence with rows
+            cg = 0;
+            if (++head == p.heads) {
+                head = 0;
                 if (few) {
                     s = __ffs(__ballot_sync(0xffffffffu, my_units > 0) & ~((2u << s) - 1)) - 1;
                 } else {
@@ -950,10 +1024,10 @@ __global__ void __launch_bounds__(AttnCfg<D, NT>::W * 32, 1)
     }
 }
 
-template <int D, int NT>
+template <int D, int R>
 static qmd_status launch_att(const AttnArgs &a, const DeviceInfo &dev, cudaStream_t s)
 {
-    using C = AttnCfg<D, NT>;
+    using C = AttnCfg<D, R>;
     const size_t smem = C::FIXED + ((size_t)a.kv.seqs + 1) * sizeof(int);
     if (smem + 256 > (size_t)dev.smem_optin)
         return QMD_ERR_SHAPE;
@@ -962,7 +1036,7 @@ static qmd_status launch_att(const AttnArgs &a, const DeviceInfo &dev, cudaStrea
         static bool opted[64] = {false};
         std::lock_guard<std::mutex> lock(mu);
         if (!opted[dev.device]) {
-            const cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<D, NT>,
+            const cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<D, R>,
                                                        cudaFuncAttributeMaxDynamicSharedMemorySize, dev.smem_optin - 256);
             if (e != cudaSuccess)
                 return fail(QMD_ERR_LAUNCH, "kv_attention smem attribute", e);
@@ -991,7 +1065,7 @@ static qmd_status launch_att(const AttnArgs &a, const DeviceInfo &dev, cudaStrea
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (launch_flags() & LAUNCH_NO_PDL) ? 0 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, NT>, a, maps);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attention_kernel<D, R>, a, maps);
     return e == cudaSuccess ? QMD_OK : fail(QMD_ERR_LAUNCH, "kv_attention launch", e);
 }
 
@@ -1014,12 +1088,12 @@ qmd_status launch_kv_attention(const KvParams &kv, int head_dim, const float *q,
     // rows per item: the least of 4, 8, 16 that holds a sequence's rows of one key/value head
     const int64_t rows = (int64_t)a.group * kv.max_q;
     if (head_dim == 64)
-        return rows <= 4 ? launch_att<64, 1>(a, dev, s) : rows <= 8 ? launch_att<64, 2>(a, dev, s) : launch_att<64, 4>(a, dev, s);
+        return rows <= 4 ? launch_att<64, 4>(a, dev, s) : rows <= 8 ? launch_att<64, 8>(a, dev, s) : launch_att<64, 16>(a, dev, s);
     if (head_dim == 128)
-        return rows <= 4   ? launch_att<128, 1>(a, dev, s)
-               : rows <= 8 ? launch_att<128, 2>(a, dev, s)
-                           : launch_att<128, 4>(a, dev, s);
-    return rows <= 4 ? launch_att<256, 1>(a, dev, s) : launch_att<256, 2>(a, dev, s);
+        return rows <= 4   ? launch_att<128, 4>(a, dev, s)
+               : rows <= 8 ? launch_att<128, 8>(a, dev, s)
+                           : launch_att<128, 16>(a, dev, s);
+    return rows <= 4 ? launch_att<256, 4>(a, dev, s) : launch_att<256, 8>(a, dev, s);
 }
 
 }  // namespace qmd
