@@ -80,7 +80,7 @@ struct AttnArgs {
     int64_t q_stride, out_stride, window;
     uint64_t wait_ns;
     int group;  // query heads to a key/value head
-    FastDiv by_group, by_blocks;  // blocks of a page
+    FastDiv by_group, by_blocks, by_heads, by_grid;  // blocks of a page, key/value heads, CTAs
     float scale_log2e;
 };
 
@@ -89,7 +89,7 @@ template <int D, int R>
 struct AttnCfg {
     // up to 4 query rows: columns of the products, two to a row; up to 8 or 16: their rows
     static constexpr bool WIDE = R > 4;
-    static constexpr int W = D == 256 ? (R == 4 ? 6 : 5) : R == 4 ? 14 : D == 64 ? (R == 8 ? 14 : 12) : 8;
+    static constexpr int W = D == 256 ? (R == 4 ? 6 : 5) : R == 4 ? (D == 64 ? 16 : 14) : D == 64 ? (R == 8 ? 14 : 12) : 8;
     static constexpr int STAGES = 3;
     static constexpr int META = 64 * 16;  // block index and scales of two chunks of 32 blocks
     static constexpr int BOX = D < 128 ? D : 128;  // bytes of a row that one copy takes
@@ -102,9 +102,8 @@ struct AttnCfg {
     static constexpr int QBYTES = QS ? R * D * 4 : 0;  // two f16 parts
     static constexpr int QN = D / 16 * (R == 4 ? 2 : R == 8 ? 4 : 8);  // registers of them
     static_assert(RING >= SLOT, "a warp's last part lies in its ring");
-    // rings, first parts, query fragments, maxima and sums of 2 W parts and W + 1 joins, jobs,
-    // barriers, scans
-    static constexpr int FIXED = W * (RING + SLOT + QBYTES + META) + (3 * W + 1) * R * 8 + (W + 1) * 32 + W * (STAGES + 1) * 8 + 8;
+    // rings, first parts, query fragments, maxima and sums of 2 W parts, jobs, barriers, scans
+    static constexpr int FIXED = W * (RING + SLOT + QBYTES + META) + 2 * W * R * 8 + (W + 1) * 32 + W * (STAGES + 1) * 8 + 8;
     static_assert(FIXED + 256 + (QMD_KV_MAX_SEQS + 1) * 4 <= 227 * 1024, "fits beside the sums of the most sequences");
 };
 
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
     constexpr int VW = D / 32;   // words of a value row that a lane holds
     extern __shared__ __align__(1024) unsigned char smem[];
     float2 *s_ml = reinterpret_cast<float2 *>(smem + W * (C::RING + C::SLOT + C::QBYTES + C::META));  // [W][2][R] maximum, weight sum
-    Job *s_job = reinterpret_cast<Job *>(s_ml + (3 * W + 1) * R);                // [1 + W]
+    Job *s_job = reinterpret_cast<Job *>(s_ml + 2 * W * R);                      // [1 + W]
     uint64_t *s_bar = reinterpret_cast<uint64_t *>(s_job + W + 1);               // [W][STAGES]
     int64_t *s_warp = reinterpret_cast<int64_t *>(s_bar + W * S);                // [W]
     int *s_last = reinterpret_cast<int *>(s_warp + W);                           // [2]
@@ -323,7 +322,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
 
     // ---- this CTA's range, this warp's range ---------------------------------------------------
     // at least a unit for every warp, so that short items are cut inside a CTA, not between CTAs
-    const int per = max(W, (int)(((unsigned)units + gridDim.x - 1) / gridDim.x));
+    const int per = max(W, (units - 1) / a.by_grid + 1);
     if ((int64_t)blockIdx.x * per >= units)
         return;
     const int u0 = blockIdx.x * per;
@@ -369,7 +368,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
         int rem = at - pre;
         const KvSeq sq = seq_at(s);
         // the row groups of a head lie together: they read the same keys and values
-        const int of_head = (few ? __shfl_sync(0xffffffffu, my_units, s) : s_pre[s + 1] - pre) / p.heads;
+        const int of_head = (few ? __shfl_sync(0xffffffffu, my_units, s) : s_pre[s + 1] - pre) / a.by_heads;
         head = rem / of_head;
         rem -= head * of_head;
         for (;; ++cg) {
@@ -416,6 +415,28 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
                 load_f32(x[i][h], qp + 64 * h);
         }
         int bi_n = block_of(lane, page_c);
+        fence_proxy_async_smem();
+        __syncwarp();  // every lane has read the last item's ring and meta
+
+        auto issue = [&](int j, int bi, uint32_t stage) {  // copy the item's j-th block, bi, into a ring stage
+            if (j < real && lane == 0) {
+                const uint32_t dst = ring_a + stage * C::BLOCK_BYTES, bar = bar0 + 8 * stage;
+                mbar_arrive_expect_tx(bar, bi >= 0 ? C::BLOCK_BYTES : 0);  // (nothing to wait for)
+                if (bi >= 0) {
+#pragma unroll
+                    for (int x = 0; x < D / C::BOX; ++x) {
+                        tma_load_3d(dst + x * C::TILE, &maps.k, x * C::BOX, 0, bi, bar);
+                        tma_load_3d(dst + 16 * D + x * C::TILE, &maps.v, x * C::BOX, 0, bi, bar);
+                    }
+                }
+            }
+        };
+        uint32_t put = use;  // the ring stage of the next block to ask for
+#pragma unroll
+        for (int j = 0; j < S - 1; ++j) {
+            issue(j, __shfl_sync(0xffffffffu, bi_n, j), put);
+            put = put + 1 == S ? 0 : put + 1;
+        }
         float ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
         int bi_1 = -1;
         float ks_1 = 0.0f, vs_1 = 0.0f;
@@ -423,8 +444,6 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             bi_1 = block_of(32 + lane, page_n);
             ks_1 = bi_1 >= 0 ? p.ks[bi_1] : 0.0f, vs_1 = bi_1 >= 0 ? p.vs[bi_1] : 0.0f;
         }
-        fence_proxy_async_smem();
-        __syncwarp();  // every lane has read the last item's
         meta[lane] = make_int4(bi_n, __float_as_int(ks_n), __float_as_int(vs_n), 0);
         meta[32 + lane] = make_int4(bi_1, __float_as_int(ks_1), __float_as_int(vs_1), 0);
         if (real > 64) {
@@ -433,30 +452,6 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             page_nn = page_of(96 + lane);
         }
         __syncwarp();
-
-        auto issue = [&](int j, uint32_t stage) {  // copy the item's j-th block into a ring stage
-            if (j < real) {
-                const int bi = meta[j & 63].x;
-                if (bi >= 0) {
-                    if (lane == 0) {
-                        const uint32_t dst = ring_a + stage * C::BLOCK_BYTES, bar = bar0 + 8 * stage;
-                        mbar_arrive_expect_tx(bar, C::BLOCK_BYTES);
-#pragma unroll
-                        for (int x = 0; x < D / C::BOX; ++x) {
-                            tma_load_3d(dst + x * C::TILE, &maps.k, x * C::BOX, 0, bi, bar);
-                            tma_load_3d(dst + 16 * D + x * C::TILE, &maps.v, x * C::BOX, 0, bi, bar);
-                        }
-                    }
-                } else if (lane == 0) {
-                    mbar_arrive_expect_tx(bar0 + 8 * stage, 0);  // nothing to wait for
-                }
-            }
-        };
-        uint32_t put = use;  // the ring stage of the next block to ask for
-        for (int j = 0; j < S - 1; ++j) {
-            issue(j, put);
-            put = put + 1 == S ? 0 : put + 1;
-        }
 
         // ---- the queries as two f16 parts ------------------------------------------------------
         uint32_t qf[C::QN];   // of word w of part h: [4 h + w][column] or [4 h + w][row, dimension]
@@ -596,7 +591,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             const uint32_t next = use + 1 == S ? 0 : use + 1, next_phase = next == 0 ? use_phase ^ 1u : use_phase;
             fence_proxy_async_smem();
             __syncwarp();  // every lane has read the stage that is asked for again
-            issue(idx + S - 1, put);
+            issue(idx + S - 1, meta[(idx + S - 1) & 63].x, put);
             put = put + 1 == S ? 0 : put + 1;
             float cn[CT][4];
             if (idx + 1 < real && !landed(next, next_phase))
@@ -836,19 +831,32 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
     // ---- joins inside the CTA -------------------------------------------------------------------
     // Job 0 is the item that began before the CTA's range (parts 0 of warps 0 ..), job 1 + w the one
     // that warp w's range cut (its part 1, parts 0 of the warps after it).
-    float2 *s_tot = s_ml + 2 * W * R;  // [1 + W][R] a job's maximum and weight sum
     const int64_t part_ml = (int64_t)gridDim.x * 2 * R * D;
     const unsigned live = __ballot_sync(0xffffffffu, lane <= W && s_job[lane <= W ? lane : 0].rows > 0);
     if (live == 0)
         return;
-    // the parts' factors: 16 lanes to a job's row, a lane to a part
-    for (int i = tid >> 4; i < (W + 1) * R; i += 2 * W) {
-        const int jj = i / R, r = i % R, k = tid & 15;
-        const unsigned half = 0xffffu << (tid & 16);
-        if (live >> jj & 1) {
-            const int wa = max(0, jj - 1), wb = (min(s_job[jj].end, span) - 1) / pw;
-            const int at = ((wa + k) * 2 + (k == 0 && jj > 0)) * R + r;
-            const float2 ml = wa + k <= wb ? s_ml[at] : make_float2(ATT_NONE, 0.0f);
+    const int k = lane & 15;                          // a half warp's lane: a part, and 4 of 64 values
+    const unsigned half = 0xffffu << (lane & 16);
+    constexpr int SEG = D / 64;                       // half warps to a row
+    bool cut = false;  // some item goes on in another CTA
+    int tail = -1;     // the item that goes on after this CTA's range
+    {
+        const int njobs = __popc(live);
+        unsigned left = live;
+        int jj = -1, seen = 0;
+        for (int i = tid >> 4; i < njobs * R * SEG; i += 2 * W) {
+            while (seen <= i / (R * SEG)) {
+                jj = __ffs(left) - 1;
+                left &= left - 1;
+                ++seen;
+            }
+            const int r = i / SEG % R, d = i % SEG * 64 + 4 * k;
+            const int start = s_job[jj].start, end = s_job[jj].end;
+            if (r >= s_job[jj].rows)
+                continue;
+            const int wa = max(0, jj - 1), wb = (min(end, span) - 1) / pw;
+            // lane k has part k's maximum and sum, and makes its factor
+            const float2 ml = wa + k <= wb ? s_ml[((wa + k) * 2 + (k == 0 && jj > 0)) * R + r] : make_float2(ATT_NONE, 0.0f);
             float M = ml.x;
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1)
@@ -858,55 +866,29 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1)
                 L += __shfl_xor_sync(half, L, o);
-            if (wa + k <= wb)
-                s_ml[at].x = f;
-            if (k == 0)
-                s_tot[jj * R + r] = make_float2(M, L);
-        }
-    }
-    __syncthreads();
-    bool cut = false;  // some item goes on in another CTA
-    int tail = -1;     // the item that goes on after this CTA's range
-    {
-        constexpr int EL = R * D / 4;  // 4 neighbouring values to a thread
-        const int njobs = __popc(live);
-        unsigned left = live;
-        int jj = -1, seen = 0;
-        for (int e = tid; e < njobs * EL; e += W * 32) {
-            while (seen <= e / EL) {
-                jj = __ffs(left) - 1;
-                left &= left - 1;
-                ++seen;
-            }
-            const int r = e % EL / (D / 4), d = e % (D / 4) * 4;
-            const int start = s_job[jj].start, end = s_job[jj].end;
-            const int wa = max(0, jj - 1), wb = (min(end, span) - 1) / pw;
-            if (r >= s_job[jj].rows)
-                continue;
             float y[4] = {};
 #pragma unroll 4
             for (int w = wa; w <= wb; ++w) {
                 const bool one = w == wa && jj > 0;
-                const float f = s_ml[(w * 2 + one) * R + r].x;
+                const float fw = __shfl_sync(half, f, (lane & 16) + w - wa);
                 float v[4];
                 load_f32(v, reinterpret_cast<const float *>(one ? smem + w * C::RING : smem + W * C::RING + w * C::SLOT) +
                                 r * D + d);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    y[i] = fmaf(v[i], f, y[i]);
+                for (int e = 0; e < 4; ++e)
+                    y[e] = fmaf(v[e], fw, y[e]);
             }
-            const float2 tot = s_tot[jj * R + r];
             if (start >= 0 && end <= span) {
-                const float f = tot.y == 0.0f ? 0.0f : 1.0f / tot.y;
+                const float g1 = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    y[i] *= f;
+                for (int e = 0; e < 4; ++e)
+                    y[e] *= g1;
                 store_f32(a.out + row_offset(a, s_job[jj].row0, s_job[jj].head, s_job[jj].first + r, a.out_stride, D) + d, y);
             } else {
                 const int64_t at = ((int64_t)blockIdx.x * 2 + (start < 0 ? 0 : 1)) * R + r;
                 store_f32(a.part + at * D + d, y);
                 if (d == 0)
-                    reinterpret_cast<float2 *>(a.part + part_ml)[at] = tot;
+                    reinterpret_cast<float2 *>(a.part + part_ml)[at] = make_float2(M, L);
             }
         }
         for (unsigned x = live; x; x &= x - 1) {
@@ -937,11 +919,10 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
         s_last[tid] = last ? jj + 1 : 0;
     }
     __syncthreads();
-    // NG groups of threads share an item's parts; a thread adds IT places of 4 values, their loads
-    // and the maxima's in flight together
-    constexpr int EL = R * D / 4, NG = W * 32 / EL > 0 ? W * 32 / EL : 1, IT = (NG * EL + W * 32 - 1) / (W * 32);
-    float2 *s_p = reinterpret_cast<float2 *>(smem);  // [parts][R] maxima and sums, then factors
-    float4 *s_y = reinterpret_cast<float4 *>(smem + (size_t)gridDim.x * R * 8);  // [NG][EL]
+    // A half warp takes 64 values of a row from every NG-th part; its maxima and sums and its first
+    // values are in flight together.
+    constexpr int TASKS = R * SEG, NG = 2 * W / TASKS > 0 ? 2 * W / TASKS : 1, AHEAD = 4;
+    float4 *s_y = reinterpret_cast<float4 *>(smem);  // [NG][R * D / 4]
     for (int x = 0; x < 2; ++x) {
         if (!s_last[x])
             continue;
@@ -950,77 +931,67 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
         // part i lies with CTA c0 + i, as its part 1 if the item began there
         auto slot = [&](int i) { return ((int64_t)(c0 + i) * 2 + (i == 0)) * R; };
         const float2 *ml = reinterpret_cast<const float2 *>(a.part + part_ml);
-        auto value = [&](int i, int it) {
-            const int e = tid + it * W * 32;
-            return __ldcg(reinterpret_cast<const float4 *>(a.part + slot(i) * D) + e % EL);
-        };
-        auto holds = [&](int it) { return NG * EL % (W * 32) == 0 || tid + it * W * 32 < NG * EL; };
-        const int n0 = NG > 1 ? tid / EL : 0;  // this thread's first part (its IT places share the group, or NG = 1)
-        float4 v[IT];
+        for (int i = tid >> 4; i < NG * TASKS; i += 2 * W) {
+            const int n0 = i / TASKS, r = i / SEG % R, e4 = i % SEG * 16 + k;
+            if (r >= j.rows)
+                continue;
+            auto value = [&](int q) { return __ldcg(reinterpret_cast<const float4 *>(a.part + (slot(q) + r) * D) + e4); };
+            float4 v[AHEAD];
+            float vm[AHEAD];
 #pragma unroll
-        for (int it = 0; it < IT; ++it)
-            if (holds(it) && n0 < parts)
-                v[it] = value(n0, it);
-        for (int i = tid; i < parts * R; i += W * 32)
-            s_p[i] = __ldcg(&ml[slot(i / R) + i % R]);
-        __syncthreads();
-        for (int r = warp; r < j.rows; r += W) {
-            float M = ATT_NONE, L = 0.0f;
-            for (int i = lane; i < parts; i += 32)
-                M = fmaxf(M, s_p[i * R + r].x);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-            for (int i = lane; i < parts; i += 32) {
-                const float2 w = s_p[i * R + r];
-                const float f = ex2(w.x - M);
-                s_p[i * R + r].x = f;
-                L = fmaf(w.y, f, L);
+            for (int q = 0; q < AHEAD; ++q)
+                if (n0 + q * NG < parts) {
+                    v[q] = value(n0 + q * NG);
+                    vm[q] = __ldcg(&ml[slot(n0 + q * NG) + r]).x;
+                }
+            float M = ATT_NONE, L = 0.0f;  // the lane's parts k, k + 16, .., then all
+            for (int q = k; q < parts; q += 16) {
+                const float2 w = __ldcg(&ml[slot(q) + r]);
+                const float mn = fmaxf(M, w.x);
+                L = fmaf(w.y, ex2(w.x - mn), L * ex2(M - mn));
+                M = mn;
             }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                L += __shfl_xor_sync(0xffffffffu, L, o);
-            if (lane == 0)
-                s_tot[r].y = L;
-        }
-        __syncthreads();
-        float4 y[IT];
+            for (int o = 8; o > 0; o >>= 1) {
+                const float m2 = __shfl_xor_sync(half, M, o), l2 = __shfl_xor_sync(half, L, o), mn = fmaxf(M, m2);
+                // the same expression on both lanes of a pair: the same bits
+                L = fmaf(fminf(M, m2) == M ? L : l2, ex2(fminf(M, m2) - mn), fminf(M, m2) == M ? l2 : L);
+                M = mn;
+            }
+            float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            auto add = [&](const float4 &u, float m) {
+                const float f = ex2(m - M);
+                y.x = fmaf(u.x, f, y.x), y.y = fmaf(u.y, f, y.y), y.z = fmaf(u.z, f, y.z), y.w = fmaf(u.w, f, y.w);
+            };
 #pragma unroll
-        for (int it = 0; it < IT; ++it)
-            y[it] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int q = 0; q < AHEAD; ++q)
+                if (n0 + q * NG < parts)
+                    add(v[q], vm[q]);
 #pragma unroll 4
-        for (int i = n0; i < parts; i += NG) {
-#pragma unroll
-            for (int it = 0; it < IT; ++it)
-                if (holds(it)) {
-                    const int r = (tid + it * W * 32) % EL / (D / 4);
-                    const float f = r < j.rows ? s_p[i * R + r].x : 0.0f;
-                    const float4 u = i == n0 ? v[it] : value(i, it);
-                    y[it].x = fmaf(u.x, f, y[it].x), y[it].y = fmaf(u.y, f, y[it].y);
-                    y[it].z = fmaf(u.z, f, y[it].z), y[it].w = fmaf(u.w, f, y[it].w);
-                }
+            for (int q = n0 + AHEAD * NG; q < parts; q += NG)
+                add(value(q), __ldcg(&ml[slot(q) + r]).x);
+            const float g1 = L == 0.0f ? 0.0f : 1.0f / L;
+            y.x *= g1, y.y *= g1, y.z *= g1, y.w *= g1;
+            if (NG > 1)
+                s_y[(n0 * R + r) * (D / 4) + e4] = y;
+            else
+                *reinterpret_cast<float4 *>(a.out + row_offset(a, j.row0, j.head, j.first + r, a.out_stride, D) + 4 * e4) = y;
         }
         if (NG > 1) {
-            if (holds(0))
-                s_y[tid] = y[0];
+            __syncthreads();
+            for (int e = tid; e < j.rows * (D / 4); e += W * 32) {
+                float4 z = s_y[e];
+#pragma unroll
+                for (int n = 1; n < NG; ++n) {
+                    const float4 u = s_y[n * R * (D / 4) + e];
+                    z.x += u.x, z.y += u.y, z.z += u.z, z.w += u.w;
+                }
+                const int r = e / (D / 4);
+                *reinterpret_cast<float4 *>(a.out + row_offset(a, j.row0, j.head, j.first + r, a.out_stride, D) +
+                                            e % (D / 4) * 4) = z;
+            }
             __syncthreads();
         }
-#pragma unroll
-        for (int it = 0; it < IT; ++it) {
-            const int e = tid + it * W * 32, r = e / (D / 4), d = e % (D / 4) * 4;
-            if (e >= EL || r >= j.rows)
-                continue;
-            float4 z = y[it];
-#pragma unroll
-            for (int n = 1; n < NG; ++n) {
-                const float4 u = s_y[n * EL + e];
-                z.x += u.x, z.y += u.y, z.z += u.z, z.w += u.w;
-            }
-            const float f = s_tot[r].y == 0.0f ? 0.0f : 1.0f / s_tot[r].y;
-            *reinterpret_cast<float4 *>(a.out + row_offset(a, j.row0, j.head, j.first + r, a.out_stride, D) + d) =
-                make_float4(z.x * f, z.y * f, z.z * f, z.w * f);
-        }
-        __syncthreads();
     }
 }
 
@@ -1084,6 +1055,7 @@ qmd_status launch_kv_attention(const KvParams &kv, int head_dim, const float *q,
     const AttnArgs a = {kv, q, out, reinterpret_cast<float *>(static_cast<char *>(ws) + counter_bytes(dev)),
                         static_cast<unsigned *>(ws), q_stride, out_stride, window, wait_limit_ns(), q_heads / kv.heads,
                         fast_div((unsigned)(q_heads / kv.heads)), fast_div((unsigned)kv.page_blocks),
+                        fast_div((unsigned)kv.heads), fast_div((unsigned)dev.sm_count),
                         scale * 1.4426950408889634f};
     // rows per item: the least of 4, 8, 16 that holds a sequence's rows of one key/value head
     const int64_t rows = (int64_t)a.group * kv.max_q;
