@@ -8,6 +8,11 @@ fused gate|up launches).  Capturing the step's launches once and replaying them 
 form of the pages' deferred streams ("One kernel, any device", §1; "The scheduler: what runs
 when, beside what", §3), which issue a whole decode step as one graph.
 
+An AttentionBlock is the attention half of a layer as one chain: the fused q|k|v projection, the
+requests' adapters beside it, the rotation and the append to the 8-bit key/value cache, attention
+over the cache, the o projection and its adapters ("Language models on the device: the cajeta-llm
+kernels", §2.5 attention over the key/value cache, §2.6 rope).
+
 All activations of the step live in one device buffer and all outputs in another, so an
 end-to-end step moves its inputs in with one host-to-device copy and its outputs out with one
 device-to-host copy.
@@ -19,7 +24,8 @@ from dataclasses import dataclass, field
 
 import numpy as np
 
-from . import Q4_K, Q6_K_SPLIT, QMD_QK, Q8K, bind_q6k, q6k_prefix_stride, q8k_pack, qmatvec, qmatvec_x
+from . import (Q4_K, Q6_K_SPLIT, QMD_QK, ROPE_HALVES, KVBatch, KVCache, Q8K, bind_q6k, kv_append, kv_attention,
+               kv_workspace, lora_add, q6k_prefix_stride, q8k_pack, qmatvec, qmatvec_x, rope_table)
 from . import synth
 
 
@@ -303,3 +309,81 @@ def host_activation(step: DecodeStep, p: Projection) -> np.ndarray:
     """The activation a projection was given (regenerated on the host from its seed)."""
     names = [n for (n, _, _, _) in synth.STEP_PROJECTIONS]
     return synth.activations(synth.step_seed(p.layer), step.batch, p.K, p.layer, names.index(p.name))
+
+
+@dataclass
+class Adapters:
+    """The low-rank adapters of one projection: A f16 or bf16 [adapters, rank, K], B [adapters, rows,
+    rank], scale f32 [adapters]."""
+    A: "object"
+    B: "object"
+    scale: "object"
+
+
+@dataclass
+class AttentionBlock:
+    """The attention half of a decoder layer for up to 8 rows: x [rows, hidden] (normalised) to
+    o(attention(rope(q), cache)) [rows, hidden].  W_qkv holds the rows of q, then k, then v; every
+    buffer belongs to the block, so a captured run can be replayed."""
+    heads: int
+    W_qkv: "object"             # Q4_K blocks, uint8 [(heads + 2 kv_heads) * head_dim, ..]
+    W_o: "object"               # Q4_K blocks, uint8 [hidden, ..]
+    rope: "object"              # f32 [positions, rot], or None
+    cache: KVCache
+    rows: int                   # rows of a call, at most 8
+    hidden: int
+    pairs: int = ROPE_HALVES
+    window: int = 0
+    qkv_adapters: Adapters | None = None
+    o_adapters: Adapters | None = None
+    qkv: "object" = None        # f32 [rows, (heads + 2 kv_heads) * head_dim]; q is rotated in place
+    attended: "object" = None   # f32 [rows, heads * head_dim]
+    y: "object" = None          # f32 [rows, hidden]
+    ws: "object" = None         # attention's workspace (one stream)
+
+    def __post_init__(self):
+        import torch
+        dev, D = self.cache.device, self.cache.head_dim
+        self.q_width, self.kv_width = self.heads * D, self.cache.kv_heads * D
+        f32 = dict(dtype=torch.float32, device=dev)
+        self.qkv = torch.empty((self.rows, self.q_width + 2 * self.kv_width), **f32)
+        self.attended = torch.empty((self.rows, self.q_width), **f32)
+        self.y = torch.empty((self.rows, self.hidden), **f32)
+        self.ws = kv_workspace(dev)
+        k = self.q_width + self.kv_width
+        self.q, self.k, self.v = self.qkv[:, :self.q_width], self.qkv[:, self.q_width:k], self.qkv[:, k:]
+
+    def run(self, x, batch: KVBatch, adapter=None, stream=None):
+        """One call's rows through the block: x f32 [rows, hidden]; batch says which sequences they
+        belong to (kv_len counts them in); adapter int32 [rows] picks each row's adapter (below 0:
+        none) where the block has adapters.  Returns y."""
+        qmatvec_x(Q4_K, self.W_qkv, None, x, self.qkv, stream=stream)
+        if self.qkv_adapters is not None:
+            a = self.qkv_adapters
+            lora_add(x, self.qkv, a.A, a.B, adapter, a.scale, out=self.qkv, stream=stream)
+        kv_append(self.cache, batch, self.k, self.v, self.rope, self.q, self.q, self.pairs, stream=stream)
+        kv_attention(self.cache, batch, self.q, self.cache.head_dim ** -0.5, self.ws, self.window, self.attended, stream=stream)
+        qmatvec_x(Q4_K, self.W_o, None, self.attended, self.y, stream=stream)
+        if self.o_adapters is not None:
+            a = self.o_adapters
+            lora_add(self.attended, self.y, a.A, a.B, adapter, a.scale, out=self.y, stream=stream)
+        return self.y
+
+
+def make_attention_block(rows: int, seqs: int, max_tokens: int, heads: int = 32, kv_heads: int = 8, head_dim: int = 128,
+                         hidden: int = 4096, page_tokens: int = 64, rope_base: float = 500000.0, layer: int = 0,
+                         device="cuda"):
+    """A block of the 7B-shaped step (q|k|v 6144 x 4096 and o 4096 x 4096 by default) with the
+    step's seeded weights, and the page table (int32 [seqs, columns]) of an empty cache that holds
+    max_tokens of each sequence."""
+    import torch
+    dev = torch.device(device)
+    seed = synth.step_seed(layer)
+    qkv_rows, width = (heads + 2 * kv_heads) * head_dim, heads * head_dim
+    Ws = [torch.from_numpy(synth.weights("q4k", seed, n, K, layer, t).reshape(n, -1)).to(dev)
+          for n, K, t in ((qkv_rows, hidden, 0), (hidden, width, 1))]
+    columns = -(-max_tokens // page_tokens)
+    cache = KVCache.empty(seqs * columns, kv_heads, page_tokens, head_dim, dev)
+    table = torch.arange(seqs * columns, dtype=torch.int32, device=dev).view(seqs, columns)
+    block = AttentionBlock(heads, Ws[0], Ws[1], rope_table(max_tokens, head_dim, rope_base, device=dev), cache, rows, hidden)
+    return block, table
