@@ -340,7 +340,7 @@ qmd_status qmd_bind_q5k(const void *gguf, int64_t rows, int64_t K);
  *   seqs 1..QMD_KV_MAX_SEQS, max_q 1..2^20, rows 1..2^24, table_stride 1..2^24.
  * The arrays are read on the device when the call runs, so a captured call sees their contents at
  * replay.  What they hold is checked there: a page outside [0, pages), a length above
- * table_stride * page_tokens or below 0, offsets outside [0, rows], a sequence with more than
+ * table_stride * page_tokens or 2^30, or below 0, offsets outside [0, rows], a sequence with more than
  * max_q rows.  A kernel that meets one sets the device error word (qmd_get_device_error then
  * returns QMD_ERR_INDEX), leaves out the sequence or page it concerns and touches no memory for it.
  */
@@ -388,7 +388,8 @@ typedef enum qmd_rope_pairs { QMD_ROPE_HALVES = 0, QMD_ROPE_ADJACENT = 1 } qmd_r
  *           (then rot 0): nothing is rotated and q is copied.  A position at or past rope_rows is
  *           an index error: that row is not stored.
  *   rot     a multiple of 32, at most head_dim
- * A sequence shorter than its rows is an index error (none of its rows is stored).
+ * A sequence shorter than its rows is an index error (none of its rows is stored); one without
+ * tokens (kv_len 0) pads the batch: its rows are neither read nor written, and nothing is reported.
  * Row pointers 16-byte aligned, strides (in f32 values) multiples of 4 and at least a row long.
  * A block that is appended to must belong to one sequence: the same block under two sequences of
  * one call, or of calls that overlap on the GPU, is a race.
@@ -403,7 +404,8 @@ qmd_status qmd_kv_append(const qmd_kv_cache *cache, const qmd_kv_batch *batch, c
  * qmd_kv_read -- the call's rows as the cache holds them: k_out and v_out receive code * scale
  * (one rounding) of every row's position, f32 [rows][kv_heads][head_dim] with the given row
  * strides.  Either may be NULL (not both).  A descriptor with other q_start than the append's
- * reads any last part of each sequence.  A sequence shorter than its rows is an index error.
+ * reads any last part of each sequence.  A sequence shorter than its rows is an index error, but for
+ * one without tokens (as in qmd_kv_append); the rows of neither are written.
  * Pointers 16-byte aligned, strides (in f32 values) multiples of 4 and at least kv_heads * head_dim.
  * Errors: NULL, SHAPE, MISALIGNED, VALUE (k_out and v_out overlap), DEVICE, LAUNCH.
  */
@@ -427,9 +429,12 @@ qmd_status qmd_kv_read(const qmd_kv_cache *cache, const qmd_kv_batch *batch, flo
  *   workspace device, qmd_kv_workspace_bytes() bytes, 16-byte aligned, owned by the caller.  Zero
  *             it once; every call that completes leaves its counters zeroed again.  Calls ordered in
  *             one stream may share it; calls that may run at the same time on the GPU (other
- *             streams, two captured graphs) need their own.
+ *             streams, two captured graphs) need their own.  After a call reports
+ *             QMD_ERR_DEVICE_TIMEOUT (qmd_get_device_error) zero it again.
  * q_heads a multiple of kv_heads, at most 64 to one.  Pointers 16-byte aligned, strides (in f32
- * values) multiples of 4 and at least q_heads * head_dim.  The same inputs on the same device give
+ * values) multiples of 4 and at least q_heads * head_dim.  The blocks that the groups of up to 16 (8
+ * at head_dim 256) rows of all sequences see, times kv_heads, number at most 2^31 - 1 in a call (more
+ * is an index error).  The same inputs on the same device give
  * the same bits.  Built for the few rows of a decode step: the work of a long prompt's rows is
  * done right but not at a prompt kernel's rate.
  * Errors: NULL, SHAPE, MISALIGNED, VALUE (scale, window, overlap), DEVICE, LAUNCH.

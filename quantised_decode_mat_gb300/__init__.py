@@ -289,6 +289,17 @@ def _stream_on(stream, t, what: str) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty(shape, device, stream):
+    """A new f32 tensor for a call on `stream`: its memory belongs to that stream."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=torch.float32, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=torch.float32, device=device)
+
+
 # The checks below run on every call of a decode step's small operators: messages are made only for
 # a refusal.
 def _array(t, dtype, shape, device, what: str) -> int:
@@ -407,7 +418,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, rope=None, q=None, q_out=Non
     if q is not None:
         heads, qs = _rows_of(q, T, None, D, dev, "q")
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.float32, device=dev)
+            q_out = _empty(q.shape, dev, stream)
         _, os_ = _rows_of(q_out, T, heads, D, dev, "q_out")
     n = rot = 0
     if rope is not None:
@@ -421,13 +432,12 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, rope=None, q=None, q_out=Non
 def kv_read(cache: KVCache, batch: KVBatch, k_out=None, v_out=None, stream=None):
     """qmd_kv_read: the rows' keys and values as the cache holds them, code * scale, f32
     [rows, kv_heads, head_dim] each (new tensors by default)."""
-    import torch
     st = _kv_stream(cache, batch, stream)
     H, D, dev, T = cache.kv_heads, cache.head_dim, cache.device, batch.rows
     if k_out is None:
-        k_out = torch.empty((T, H, D), dtype=torch.float32, device=dev)
+        k_out = _empty((T, H, D), dev, stream)
     if v_out is None:
-        v_out = torch.empty((T, H, D), dtype=torch.float32, device=dev)
+        v_out = _empty((T, H, D), dev, stream)
     _, ks = _rows_of(k_out, T, H, D, dev, "k_out")
     _, vs = _rows_of(v_out, T, H, D, dev, "v_out")
     _check(lib().qmd_kv_read(cache.ptrs, batch.ptrs, k_out.data_ptr(), ks, v_out.data_ptr(), vs, st))
@@ -452,7 +462,7 @@ def kv_attention(cache: KVCache, batch: KVBatch, q, scale: float, workspace, win
     D, dev, T = cache.head_dim, cache.device, batch.rows
     heads, qs = _rows_of(q, T, None, D, dev, "q")
     if out is None:
-        out = torch.empty((T, heads * D), dtype=torch.float32, device=dev)
+        out = _empty((T, heads * D), dev, stream)
     _, os_ = _rows_of(out, T, heads, D, dev, "out")
     L = lib()
     ws = _array(workspace, torch.int32, (L.qmd_kv_workspace_bytes() // 4,), dev, "workspace")
@@ -477,7 +487,7 @@ def lora_add(x, base, A, B, adapter, scale, out=None, stream=None):
         raise QmdError(6, "x [batch, K], base [batch, rows] and A [adapters, rank, K] are wanted")
     (n, rank, K), batch, rows = A.shape, x.shape[0], base.shape[1]
     if out is None:
-        out = torch.empty((batch, rows), dtype=torch.float32, device=dev)
+        out = _empty((batch, rows), dev, stream)
     f32 = torch.float32
     _check(lib().qmd_lora_add(half, _array(x, f32, (batch, K), dev, "x"), _array(base, f32, (batch, rows), dev, "base"),
                               _array(A, A.dtype, (n, rank, K), dev, "A"), _array(B, A.dtype, (n, rows, rank), dev, "B"),

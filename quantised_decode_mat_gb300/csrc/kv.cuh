@@ -14,6 +14,7 @@
 namespace qmd {
 
 constexpr int KV_BLOCK = QMD_KV_BLOCK;
+constexpr int KV_MAX_LEN = 1 << 30;  // so that positions rounded up to a block stay in 31 bits
 
 struct KvParams {
     int8_t *k, *v;
@@ -49,7 +50,7 @@ __device__ __forceinline__ KvSeq kv_seq(const KvParams &p, int s)
     q.len = p.len[s];
     q.n = end - q.row0;
     const bool ok = q.row0 >= 0 && end >= q.row0 && end <= p.rows && q.n <= p.max_q && q.len >= 0 &&
-                    q.len <= p.table_stride * p.page_blocks * KV_BLOCK;
+                    q.len <= KV_MAX_LEN && q.len <= p.table_stride * p.page_blocks * KV_BLOCK;
     if (!ok) {
         kv_index_error(p);
         q.row0 = q.n = q.len = 0;
@@ -57,9 +58,7 @@ __device__ __forceinline__ KvSeq kv_seq(const KvParams &p, int s)
     return q;
 }
 
-// Index of block `blk` (16 positions) of sequence s among all [page][block] pairs of the pool, or
-// -1 for a page outside it.  The block of head h starts at code offset
-// kv_block_offset(...) * 16 * head_dim and has its scale at that offset itself.
+// The page of block `blk` (16 positions) of sequence s, or -1 for one outside the pool.
 __device__ __forceinline__ int kv_page(const KvParams &p, int s, int blk)
 {
     const int32_t page = p.table[(int64_t)s * p.table_stride + blk / p.page_blocks];
@@ -70,6 +69,8 @@ __device__ __forceinline__ int kv_page(const KvParams &p, int s, int blk)
     return page;
 }
 
+// Where that block of a head lies in the pool, counted in blocks: its scale's place; its codes begin
+// 16 * head_dim times as far.
 __device__ __forceinline__ int64_t kv_block_offset(const KvParams &p, int page, int head, int blk)
 {
     return ((int64_t)page * p.heads + head) * p.page_blocks + blk % p.page_blocks;

@@ -50,8 +50,9 @@ __device__ __forceinline__ void chunk_rows(const KvParams &p, int64_t t0, KvRow 
             const KvSeq q = kv_seq(p, s);
             if (t >= q.row0 && t < q.row0 + q.n) {
                 const int pos = q.len - q.n + (int)(t - q.row0);
-                if (q.len < q.n) {  // a sequence shorter than its rows
-                    kv_index_error(p);
+                if (q.len < q.n) {  // a sequence shorter than its rows; one without tokens pads the batch
+                    if (q.len > 0)
+                        kv_index_error(p);
                 } else {
                     r.seq = s;
                     r.pos = pos;

@@ -261,23 +261,30 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
     };
     // up to 32 sequences: every warp for itself, a lane a sequence; else through shared memory
     const bool few = p.seqs <= 32;
-    KvSeq mine = {0, 0, 0};
     int my_pre = 0, my_units = 0;
-    int64_t total = 0;
+    int units = 0;
+    bool too_many = false;
     if (few) {
-        if (lane < p.seqs)
-            mine = kv_seq(p, lane);
-        my_units = (int)min(units_of(mine), (int64_t)INT_MAX / 32 + 1);
-        int sum = my_units;
+        int64_t u = lane < p.seqs ? units_of(kv_seq(p, lane)) : 0;
+        my_units = (int)min(u, (int64_t)INT_MAX);
+        const bool big = __any_sync(0xffffffffu, u > INT_MAX / 32);  // the 32-bit sum may run over
+        if (big) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                u += __shfl_xor_sync(0xffffffffu, u, o);
+            too_many = u > INT_MAX;
+        }
+        unsigned sum = (unsigned)my_units;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, sum, o);
+            const unsigned x = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o)
                 sum += x;
         }
-        my_pre = sum - my_units;
-        total = __any_sync(0xffffffffu, my_units > INT_MAX / 32) ? INT64_MAX : __shfl_sync(0xffffffffu, sum, 31);
+        my_pre = (int)(sum - (unsigned)my_units);
+        units = (int)__shfl_sync(0xffffffffu, sum, 31);
     } else {
+        int64_t total = 0;
         for (int s0 = 0; s0 < p.seqs; s0 += W * 32) {
             const int s = s0 + tid;
             const int64_t u = s < p.seqs ? units_of(kv_seq(p, s)) : 0;
@@ -301,25 +308,16 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             if (s < p.seqs)
                 s_pre[s] = (int)(base + sum - u);
         }
-    }
-    if (total > INT_MAX) {  // more blocks than a launch counts
-        kv_index_error(p);
-        return;
-    }
-    const int units = (int)total;
-    if (!few) {
+        units = (int)total;
+        too_many = total > INT_MAX;
         if (tid == 0)
             s_pre[p.seqs] = units;
         __syncthreads();
     }
-    auto seq_at = [&](int s) {
-        if (!few)
-            return kv_seq(p, s);
-        const KvSeq q = {__shfl_sync(0xffffffffu, mine.row0, s), __shfl_sync(0xffffffffu, mine.n, s),
-                         __shfl_sync(0xffffffffu, mine.len, s)};
-        return q;
-    };
-
+    if (too_many) {  // more blocks than a launch counts
+        kv_index_error(p);
+        return;
+    }
     // ---- this CTA's range, this warp's range ---------------------------------------------------
     // at least a unit for every warp, so that short items are cut inside a CTA, not between CTAs
     const int per = max(W, (units - 1) / a.by_grid + 1);
@@ -331,7 +329,6 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
     const int w1 = min(span, u + pw);
 
     unsigned char *ring = smem + warp * C::RING;
-    float *slot0 = reinterpret_cast<float *>(smem + W * C::RING + warp * C::SLOT);
     const uint32_t ring_a = smem_addr(ring);
     uint32_t use = 0, use_phase = 0;  // the ring stage of the next block to read, and its barrier's phase
     bool dead = false;                // a copy did not land in time
@@ -366,7 +363,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             pre = s_pre[s];
         }
         int rem = at - pre;
-        const KvSeq sq = seq_at(s);
+        const KvSeq sq = kv_seq(p, s);
         // the row groups of a head lie together: they read the same keys and values
         const int of_head = (few ? __shfl_sync(0xffffffffu, my_units, s) : s_pre[s + 1] - pre) / a.by_heads;
         head = rem / of_head;
@@ -381,7 +378,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
         b0 = rem;
     }
     while (u < w1) {
-        const KvSeq sq = seq_at(s);
+        const KvSeq sq = kv_seq(p, s);
         const Group gr = group_of<R>(a, sq, cg);
         const int nb = max(1, gr.hi - gr.lo);
         const int cnt = min(nb - b0, w1 - u);              // units of this item in the range
@@ -767,7 +764,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
         // ---- the item's part: finished, or laid down for the join --------------------------------
         const bool done = b0 == 0 && cnt == nb;
         const int part = b0 > 0 ? 0 : 1;
-        float *dst = part == 0 ? slot0 : reinterpret_cast<float *>(ring);
+        float *dst = reinterpret_cast<float *>(part == 0 ? smem + W * C::RING + warp * C::SLOT : ring);
         if (part == 1 && !done)
             __syncwarp();  // every lane has read the ring
 #pragma unroll

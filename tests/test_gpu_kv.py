@@ -63,7 +63,7 @@ class Scene:
             for p0 in range(0, l, 16):
                 pg, t0, m = self.table[s, p0 // page], p0 % page, min(16, l - p0)
                 for codes, sc in ((self.c.k, self.c.ks), (self.c.v, self.c.vs)):
-                    codes[pg, :, t0:t0 + m] = rng.integers(-127, 128, (kv, m, dim))
+                    codes[pg, :, t0:t0 + m] = rng.integers(-128, 128, (kv, m, dim))
                     sc[pg, :, t0 // 16] = rng.uniform(0.005, 0.03, kv) * spread ** rng.uniform(-1, 1, kv)
         self.q_start = np.concatenate(([0], np.cumsum(rows))).astype(np.int32)
         self.T = int(self.q_start[-1]) + extra_rows
@@ -320,6 +320,58 @@ def test_two_streams_with_their_own_workspaces():
     assert all(torch.equal(a, b) for a, b in zip(want, outs))
 
 
+def test_lengths_past_what_positions_count_are_reported(ws):
+    # a table that puts 2^31 positions on one page: the sequence is left out, the other is not
+    s = Scene([40, 20], [1, 1], 4, 2, 64, 16, seed=21)
+    x = s.queries()
+    ref, bound = P.attention(s.c, s.table, s.lens, s.q_start, x, 0.1)
+    wide = torch.zeros((2, 1 << 24), dtype=torch.int32, device=DEV)
+    wide[1, :2] = s.table_d[1, :2]
+    batch = q.KVBatch(wide, torch.tensor([(1 << 28) - 1 + (1 << 30), 20], dtype=torch.int32, device=DEV), s.start_d, 1, 2)
+    out = torch.full((2, 256), np.nan, device=DEV)
+    q.kv_attention(s.cache, batch, dev(x), 0.1, ws, out=out)
+    with pytest.raises(q.QmdError, match="QMD_ERR_INDEX"):
+        q.get_device_error()
+    got = out.reshape(2, 4, 64).cpu().numpy()
+    assert np.isnan(got[0]).all() and (np.abs(got[1] - ref[1]) <= bound[1]).all()
+
+
+def test_outputs_on_another_stream(ws):
+    s = Scene([300, 41], [1, 1], 8, 2, 128, 32, seed=22)
+    x = s.queries()
+    xd = dev(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = q.kv_attention(s.cache, s.batch, xd, 0.1, ws, stream=side)
+    k, v = q.kv_read(s.cache, s.batch, stream=side.cuda_stream)
+    side.synchronize()
+    s.close(got, *P.attention(s.c, s.table, s.lens, s.q_start, x, 0.1))
+    K, V = s.c.values(s.table, 0, 299, 300)
+    assert np.array_equal(bits(k[0:1].cpu().numpy()), bits(K.astype(np.float32)))
+    assert np.array_equal(bits(v[0:1].cpu().numpy()), bits(V.astype(np.float32)))
+
+
+def test_graphs_that_overlap_with_their_own_workspaces():
+    s = Scene([5000, 300, 77], [1] * 3, 32, 8, 128, 64, seed=23)
+    x = dev(s.queries())
+    want = q.kv_attention(s.cache, s.batch, x, 0.1, q.kv_workspace())
+    graphs = []
+    for _ in range(2):
+        w, o, st = q.kv_workspace(), torch.zeros_like(want), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            for _ in range(4):
+                q.kv_attention(s.cache, s.batch, x, 0.1, w, out=o)
+        graphs.append((g, o, st, w))
+    for _ in range(10):
+        for g, _, st, _ in graphs:
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(want, o) for _, o, _, _ in graphs)
+
+
 # ---- append and read ---------------------------------------------------------------------------
 
 def rope_np(n, rot):
@@ -398,6 +450,30 @@ def test_append_zeros_tiny_and_large():
     q.kv_append(s.cache, s.batch, dev(k), dev(v))
     q.get_device_error()
     same_cache(s)
+
+
+def test_padded_batch_keeps_quiet(ws):
+    # slots without a request: kv_len 0, a row each, and a page table of rubbish
+    s = Scene([21, 1, 1, 60], [1] * 4, 8, 2, 128, 16, seed=24, uniform=True)
+    real = [0, 3]
+    s.len_d[1:3] = 0
+    s.table_d[1:3] = 12345
+    k, v = (s.rng.standard_normal((4, 2, 128)).astype(np.float32) for _ in "kv")
+    x = s.queries()
+    want = s.c
+    rope = rope_np(64, 128)
+    ref = P.append(want, s.table[real], [21, 60], [0, 1, 2], k[real], v[real], rope, x[real], 128)
+    qr = torch.full((4, 8, 128), np.nan, device=DEV)
+    q.kv_append(s.cache, s.batch, dev(k), dev(v), dev(rope), dev(x), qr)
+    out = q.kv_attention(s.cache, s.batch, qr, 0.1, ws)
+    ko = torch.full((4, 2, 128), 5.0, device=DEV)
+    q.kv_read(s.cache, s.batch, ko, torch.empty_like(ko))
+    q.get_device_error()
+    same_cache(s)
+    assert np.array_equal(bits(qr.cpu().numpy()[real]), bits(ref)) and qr[1:3].isnan().all() and (ko[1:3] == 5).all()
+    att, bound = P.attention(want, s.table[real], [21, 60], [0, 1, 2], ref, 0.1)
+    got = out.reshape(4, 8, 128).cpu().numpy()
+    assert (np.abs(got[real] - att) <= bound).all() and (got[1:3] == 0).all()
 
 
 def test_append_parts_of_a_fused_projection_and_read_back():

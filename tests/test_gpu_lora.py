@@ -114,3 +114,18 @@ def test_beside_a_quantised_projection_and_in_a_graph():
         g.replay()
         q.get_device_error()
         check(t, y, c)
+
+
+def test_two_streams_and_large_and_small_values():
+    """Two calls at once (a call holds no state), with sums far above and below f16's range."""
+    jobs = []
+    for i, f in enumerate((1e20, 1e-20, 1.0)):
+        t = list(make(8, 5, 32, 2048, 3001, torch.float16 if i % 2 else torch.bfloat16, seed=10 + i))
+        t[0] *= f
+        t[1] *= f
+        jobs.append((t, [a.to(DEV) for a in t], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[q.lora_add(*d[:4], d[4], d[5], stream=st) for t, d, st in jobs] for _ in range(8)][-1]
+    torch.cuda.synchronize()
+    for (t, _, _), o in zip(jobs, outs):
+        check(t, o)
