@@ -89,8 +89,11 @@ template <int D, int R>
 struct AttnCfg {
     // up to 4 query rows: columns of the products, two to a row; up to 8 or 16: their rows
     static constexpr bool WIDE = R > 4;
-    static constexpr int W = D == 256 ? (R == 4 ? 6 : 5) : R == 4 ? (D == 64 ? 16 : 14) : D == 64 ? (R == 8 ? 14 : 12) : 8;
-    static constexpr int STAGES = 3;
+    // Warps: as many as registers and shared memory hold (at 128 dimensions and 4 rows 16 with rings of
+    // 2 against 14 with rings of 3: 1 x 32768 23.0 against 25.2 us, 48 ragged sequences 124 against 127;
+    // at 256 and 4 rows 8 against 6: 16 x 8100 90.6 against 104 us).
+    static constexpr int W = D == 256 ? (R == 4 ? 8 : 6) : R == 4 ? 16 : D == 64 ? (R == 8 ? 16 : 12) : R == 8 ? 12 : 8;
+    static constexpr int STAGES = D == 256 || (D == 128 && R == 4) ? 2 : 3;
     static constexpr int META = 64 * 16;  // block index and scales of two chunks of 32 blocks
     static constexpr int BOX = D < 128 ? D : 128;  // bytes of a row that one copy takes
     static constexpr int TILE = 16 * BOX;          // a copy: BOX bytes of 16 rows
@@ -524,7 +527,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
         // the first product of the block in a ring stage: K Q^T (16 positions by columns), or Q K^T (rows
         // by two tiles of 8 positions)
         auto scores = [&](float (&c)[CT][4], const unsigned char *st) {
-            float c2[4] = {};  // two chains of sums
+            float c2[CT][4] = {};  // twice as many chains of sums (at 8 rows the registers cost more)
 #pragma unroll
             for (int i = 0; i < CT; ++i)
                 c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0.0f;
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
                     if constexpr (!WIDE) {
                         const uint4 qv = query(2 * h + w2 / 2);
                         mma_16816(c[0], f[0], qv.x, qv.y);
-                        mma_16816(c2, f[1], qv.z, qv.w);
+                        mma_16816(c2[0], f[1], qv.z, qv.w);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
@@ -553,29 +556,27 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
                             for (int part = 0; part < R / 8; ++part) {
                                 const uint4 qv = query((4 * h + w2 + e) * (R / 8) + part);
                                 const uint32_t qa[4] = {qv.x, qv.y, qv.z, qv.w};
-                                mma_16816(c[0], qa, f[e][0], f[e][2]);
-                                mma_16816(c[CT - 1], qa, f[e][1], f[e][3]);
+                                mma_16816(part ? c2[0] : c[0], qa, f[e][0], f[e][2]);
+                                mma_16816(part ? c2[CT - 1] : c[CT - 1], qa, f[e][1], f[e][3]);
                             }
                     }
                 }
             }
-            if constexpr (!WIDE)
+            if constexpr (R != 8)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    c[0][e] += c2[e];
+                for (int i = 0; i < CT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        c[i][e] += c2[i][e];
         };
-        // The next block's first product runs beside this block's weights and second product: two chains
-        // of dependent instructions for the scheduler instead of one.
         float c[CT][4];
-        // wait for the block in stage use (phase use_phase), or the one after it
+        // wait for the block in a stage
         auto landed = [&](uint32_t stage, uint32_t phase) {
             if (__all_sync(0xffffffffu, mbar_wait_bounded(bar0 + 8 * stage, phase, a.wait_ns)))
                 return true;
             dead = true;
             return false;
         };
-        if (real > 0 && landed(use, use_phase))
-            scores(c, ring + use * C::BLOCK_BYTES);
         for (int idx = 0; idx < real && !dead; ++idx) {
             if ((idx & 31) == 0 && idx > 0 && idx + 32 < real) {
                 __syncwarp();
@@ -590,10 +591,9 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             __syncwarp();  // every lane has read the stage that is asked for again
             issue(idx + S - 1, meta[(idx + S - 1) & 63].x, put);
             put = put + 1 == S ? 0 : put + 1;
-            float cn[CT][4];
-            if (idx + 1 < real && !landed(next, next_phase))
+            if (!landed(use, use_phase))
                 break;
-            scores(cn, ring + next * C::BLOCK_BYTES);  // past the last block: of what the ring holds, not used
+            scores(c, ring + use * C::BLOCK_BYTES);
             const int4 md = meta[idx & 63];
             const int bi = md.x;
             const float ks = __int_as_float(md.y), vs = __int_as_float(md.z);
@@ -736,11 +736,6 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
                     }
                 }
             }
-#pragma unroll
-            for (int i = 0; i < CT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    c[i][e] = cn[i][e];
             use = next;
             use_phase = next_phase;
         }
