@@ -26,7 +26,7 @@
 
 namespace qmd {
 
-constexpr int APP_WARPS = 8;
+constexpr int APP_WARPS = 4;
 constexpr int APP_CHUNK = 16;  // rows a CTA looks up
 constexpr int APP_HEADS = 8;   // query heads of a task: their loads in flight together, the table's row read once
 
