@@ -14,6 +14,10 @@
 // leader of a block if it is the first of the call's rows in it; the block's task is done by the
 // leader's chunk, so no two warps touch a block's scale and no atomics are needed.  Lane l owns
 // head_dim / 32 neighbouring values; a rotation partner half a head away comes by a shuffle.
+//
+// Bound: memory for prompts (11739 rows of 32 + 2 x 8 heads of 128: 95 us for 511 MB, 5.4 TB/s; with
+// their blocks read back 131, 121 and 160 us at 4, 8 and 16 query heads a task; a read back of 32000
+// rows 61 us, 5.4 TB/s, with streaming stores 72), launch latency for single tokens (8 rows 3.5 us).
 #include <mutex>
 #include <set>
 #include <utility>
