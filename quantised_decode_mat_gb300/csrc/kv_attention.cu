@@ -121,6 +121,16 @@ constexpr int ATT_MAX_ROWS_FLOATS = 16 * 128;  // the largest R x D of an instan
 constexpr float ATT_NONE = -3.0e38f;           // the maximum before any score
 constexpr float ATT_SLACK = 8.0f;              // how far (log2) a score may pass the running maximum
 
+// tma_load_3d with the default L2 policy: the cache is read again in the next step.
+__device__ __forceinline__ void load_tile(uint32_t dst, const void *tmap, int x, int block, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(0), "r"(block), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -432,8 +442,8 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
                 if (bi >= 0) {
 #pragma unroll
                     for (int x = 0; x < D / C::BOX; ++x) {
-                        tma_load_3d(dst + x * C::TILE, &maps.k, x * C::BOX, 0, bi, bar);
-                        tma_load_3d(dst + 16 * D + x * C::TILE, &maps.v, x * C::BOX, 0, bi, bar);
+                        load_tile(dst + x * C::TILE, &maps.k, x * C::BOX, bi, bar);
+                        load_tile(dst + 16 * D + x * C::TILE, &maps.v, x * C::BOX, bi, bar);
                     }
                 }
             }
@@ -639,10 +649,11 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
                 for (int e = 0; e < SN; ++e)
                     up |= sc[i][e] > m[i] + ATT_SLACK;
             }
-            if (__any_sync(0xffffffffu, up) || vs > vref) {
+            const float va = fabsf(vs);
+            if (__any_sync(0xffffffffu, up) || va > vref) {
                 float fv = 1.0f;
-                if (vs > vref) {
-                    const float r = __uint_as_float((__float_as_uint(vs) + 0x7fffffu) & 0x7f800000u);
+                if (va > vref) {
+                    const float r = __uint_as_float((__float_as_uint(va) + 0x7fffffu) & 0x7f800000u);
                     fv = vref / r;
                     vref = r;
                     vinv = LIFT / r;

@@ -50,6 +50,15 @@ struct LoraArgs {
     uint64_t wait_ns;
 };
 
+// bulk_copy_g2s with the default L2 policy: adapters are read again in the next step.
+__device__ __forceinline__ void load_chunk(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ float2 widen(uint32_t w, __half) { return __half22float2(*reinterpret_cast<__half2 *>(&w)); }
 __device__ __forceinline__ float2 widen(uint32_t w, __nv_bfloat16)
 {
@@ -150,7 +159,7 @@ __global__ void __launch_bounds__(LORA_WARPS * 32, 1) lora_add_kernel(const Lora
             if (lane == 0) {
                 const uint32_t bytes = (uint32_t)(n * a.rank * 2);
                 mbar_arrive_expect_tx(bar0 + 8 * stage, bytes);
-                bulk_copy_g2s(dst, B + (int64_t)row * a.rank, bytes, bar0 + 8 * stage);
+                load_chunk(dst, B + (int64_t)row * a.rank, bytes, bar0 + 8 * stage);
             }
             for (int i = lane; i < n; i += 32)
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + LORA_CHUNK + 4 * i), "l"(base + row + i)

@@ -186,6 +186,8 @@ def test_block_scales_far_apart(ws):
     s.c.vs[s.table[0, 2], :, 0] = 0
     s.c.ks[s.table[0, 3], :, 1] = 0
     s.c.vs[s.table[1, :3]] = 0  # a sequence of nothing but zeros
+    s.c.vs[s.table[0, 5]] *= -1  # a scale is a factor, whatever its sign
+    s.c.ks[s.table[0, 6]] *= -1
     s.place()
     got = s.check(s.queries(), ws)
     assert (got[2:] == 0).all()
