@@ -919,12 +919,12 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
         int last = 0;
         if (jj >= 0) {
             const int c0 = (u0 + s_job[jj].start) / per, c1 = (u0 + s_job[jj].end - 1) / per;
-            __threadfence();
-            last = atomicAdd(a.ctr + c0, 1u) == (unsigned)(c1 - c0);
-            if (last) {
+            // releases the CTA's parts (ordered before it by the barrier) and acquires the others'
+            unsigned come;
+            asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(come) : "l"(a.ctr + c0) : "memory");
+            last = come == (unsigned)(c1 - c0);
+            if (last)
                 a.ctr[c0] = 0;  // every part has come: left as it was found
-                __threadfence();
-            }
         }
         s_last[tid] = last ? jj + 1 : 0;
     }
