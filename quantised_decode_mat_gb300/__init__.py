@@ -278,14 +278,23 @@ def _need(ok: bool, status: int, detail: str) -> None:
         raise QmdError(status, detail)
 
 
-def _stream_on(stream, t, what: str) -> int:
-    """The stream of a call on tensor t's device, which has to be the current one."""
+# torch's names that every call below uses, looked up with the first cache or adapter call.
+_F32 = _I32 = _device_now = _stream_now = None
+
+
+def _torch_names() -> None:
+    global _F32, _I32, _device_now, _stream_now
     import torch
-    index = t.get_device()
-    if index < 0 or index != torch._C._cuda_getDevice():
+    _F32, _I32 = torch.float32, torch.int32
+    _device_now, _stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _stream_on(stream, index: int, what: str) -> int:
+    """The stream of a call on the device with this index, which has to be the current one."""
+    if index < 0 or index != _device_now():
         raise QmdError(9, f"{what} must be on the current CUDA device")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
+        return _stream_now(index)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -302,43 +311,42 @@ def _empty(shape, device, stream):
 
 # The checks below run on every call of a decode step's small operators: messages are made only for
 # a refusal.
-def _array(t, dtype, shape, device, what: str) -> int:
-    """The address of a contiguous tensor of this type and shape (None: any extent) on this device."""
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+def _array(t, dtype, shape, index: int, what: str) -> int:
+    """The address of a contiguous tensor of this type and shape on the device with this index."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
         return t.data_ptr()
     if t.dtype is not dtype:
         raise QmdError(2, f"{what}: {dtype} is wanted, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+    if t.shape != shape:
         raise QmdError(6, f"{what}: shape {tuple(shape)} is wanted, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise QmdError(6, f"{what} must be contiguous")
-    if t.device != device:
-        raise QmdError(9, f"{what} is on {t.device}, not on {device}")
-    return t.data_ptr()
+    raise QmdError(9, f"{what} is on {t.device}, not on the device of the others")
 
 
-def _rows_of(t, rows: int, heads: int | None, dim: int, device, what: str) -> tuple[int, int]:
+def _rows_of(t, rows: int, heads: int | None, dim: int, index: int, what: str) -> tuple[int, int]:
     """(heads, row stride) of f32 rows [rows or more, heads, dim] or [rows or more, heads * dim],
     strided by rows only."""
-    import torch
-    if t.dtype is not torch.float32:
+    if t.dtype is _F32 and t.get_device() == index:
+        shape = t.shape
+        if len(shape) == 3:
+            n, h, d = shape
+            a, b, c = t.stride()
+            width, ok = h * d, d == dim and c == 1 and (b == dim or h == 1)
+        elif len(shape) == 2:
+            n, width = shape
+            a, b = t.stride()
+            ok = b == 1 and width % dim == 0
+        else:
+            ok = False
+        if ok and n >= rows and (width > 0 if heads is None else width == heads * dim):
+            return width // dim, a if n > 1 else (width + 3) // 4 * 4
+    if t.dtype is not _F32:
         raise QmdError(2, f"{what}: float32 is wanted, got {t.dtype}")
-    if t.device != device:
-        raise QmdError(9, f"{what} is on {t.device}, not on {device}")
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 3:
-        n, h, d = shape
-        width = h * d
-        ok = d == dim and stride[2] == 1 and (stride[1] == dim or h == 1)
-    elif len(shape) == 2:
-        n, width = shape
-        ok = width % dim == 0 and stride[1] == 1
-    else:
-        ok = False
-    if not ok or width == 0 or n < rows or (heads is not None and width != heads * dim):
-        raise QmdError(6, f"{what}: {rows} or more rows of {heads or 'some'} heads of {dim} values are wanted, "
-                          f"strided by rows only; got shape {tuple(shape)}, strides {tuple(stride)}")
-    return width // dim, stride[0] if n > 1 else (width + 3) // 4 * 4
+    if t.get_device() != index:
+        raise QmdError(9, f"{what} is on {t.device}, not on the cache's device")
+    raise QmdError(6, f"{what}: {rows} or more rows of {heads or 'some'} heads of {dim} values are wanted, strided by "
+                      f"rows only; got shape {tuple(t.shape)}, strides {tuple(t.stride())}")
 
 
 class KVCache:
@@ -347,12 +355,14 @@ class KVCache:
 
     def __init__(self, k, v, k_scale, v_scale):
         import torch
+        _torch_names()
         _need(k.dim() == 4, 6, "k: [pages, kv_heads, page_tokens, head_dim] is wanted")
         pages, heads, tokens, dim = k.shape
-        _array(k, torch.int8, k.shape, k.device, "k")
-        _array(v, torch.int8, k.shape, k.device, "v")
+        self.index = k.get_device()
+        for t, what in ((k, "k"), (v, "v")):
+            _array(t, torch.int8, k.shape, self.index, what)
         for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            _array(t, torch.float32, (pages, heads, tokens // QMD_KV_BLOCK), k.device, what)
+            _array(t, torch.float32, (pages, heads, tokens // QMD_KV_BLOCK), self.index, what)
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.kv_heads, self.head_dim, self.device = heads, dim, k.device
         self.ptrs = KVCachePtrs(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), pages, heads, tokens, dim)
@@ -372,23 +382,24 @@ class KVBatch:
     rows of the call's tensors; without q_start every sequence has max_q rows."""
 
     def __init__(self, page_table, kv_len, q_start=None, max_q: int = 1, rows: int | None = None):
-        import torch
+        _torch_names()
         _need(page_table.dim() == 2, 6, "page_table: [seqs, columns] is wanted")
         seqs = page_table.shape[0]
-        _array(page_table, torch.int32, page_table.shape, page_table.device, "page_table")
-        _array(kv_len, torch.int32, (seqs,), page_table.device, "kv_len")
+        self.index = page_table.get_device()
+        _array(page_table, _I32, page_table.shape, self.index, "page_table")
+        _array(kv_len, _I32, (seqs,), self.index, "kv_len")
         if q_start is not None:
-            _array(q_start, torch.int32, (seqs + 1,), page_table.device, "q_start")
+            _array(q_start, _I32, (seqs + 1,), self.index, "q_start")
             _need(rows is not None, 6, "rows: the rows of the call's tensors are wanted with q_start")
         self.page_table, self.kv_len, self.q_start = page_table, kv_len, q_start
-        self.max_q, self.rows, self.device = max_q, seqs * max_q if rows is None else rows, page_table.device
+        self.max_q, self.rows = max_q, seqs * max_q if rows is None else rows
         self.ptrs = KVBatchPtrs(_ptr(page_table), _ptr(kv_len), _ptr(q_start), page_table.shape[1], self.rows, seqs, max_q)
 
 
 def _kv_stream(cache: KVCache, batch: KVBatch, stream) -> int:
-    if batch.device != cache.device:
-        raise QmdError(9, f"the batch is on {batch.device}, the cache on {cache.device}")
-    return _stream_on(stream, cache.k, "the cache")
+    if batch.index != cache.index:
+        raise QmdError(9, f"the batch is on {batch.page_table.device}, the cache on {cache.device}")
+    return _stream_on(stream, cache.index, "the cache")
 
 
 def rope_table(positions: int, rot: int, base: float = 10000.0, inv_freq=None, device="cuda"):
@@ -409,23 +420,25 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, rope=None, q=None, q_out=Non
     values into the cache and returns the rotated queries (q_out, by default a new tensor; None
     without q).  k, v f32 [rows, kv_heads, head_dim], q f32 [rows, heads, head_dim], strided by rows
     only (parts of one fused projection's output); q_out may be q."""
-    import torch
     st = _kv_stream(cache, batch, stream)
-    D, dev, T = cache.head_dim, cache.device, batch.rows
+    D, dev, T = cache.head_dim, cache.index, batch.rows
     _, ks = _rows_of(k, T, cache.kv_heads, D, dev, "k")
     _, vs = _rows_of(v, T, cache.kv_heads, D, dev, "v")
     heads = qs = os_ = 0
     if q is not None:
         heads, qs = _rows_of(q, T, None, D, dev, "q")
         if q_out is None:
-            q_out = _empty(q.shape, dev, stream)
-        _, os_ = _rows_of(q_out, T, heads, D, dev, "q_out")
+            q_out = _empty(q.shape, cache.device, stream)
+        os_ = qs if q_out is q else _rows_of(q_out, T, heads, D, dev, "q_out")[1]
     n = rot = 0
     if rope is not None:
-        _array(rope, torch.float32, (None, None), dev, "rope")
+        _need(rope.dim() == 2, 6, "rope: [positions, rot] is wanted")
         n, rot = rope.shape
-    _check(lib().qmd_kv_append(cache.ptrs, batch.ptrs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, heads,
-                               _ptr(q_out), os_, _ptr(rope), n, rot, pairs, st))
+        _array(rope, _F32, (n, rot), dev, "rope")
+    st = lib().qmd_kv_append(cache.ptrs, batch.ptrs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, heads,
+                             _ptr(q_out), os_, _ptr(rope), n, rot, pairs, st)
+    if st:
+        _check(st)
     return q_out
 
 
@@ -433,15 +446,20 @@ def kv_read(cache: KVCache, batch: KVBatch, k_out=None, v_out=None, stream=None)
     """qmd_kv_read: the rows' keys and values as the cache holds them, code * scale, f32
     [rows, kv_heads, head_dim] each (new tensors by default)."""
     st = _kv_stream(cache, batch, stream)
-    H, D, dev, T = cache.kv_heads, cache.head_dim, cache.device, batch.rows
+    H, D, dev, T = cache.kv_heads, cache.head_dim, cache.index, batch.rows
     if k_out is None:
-        k_out = _empty((T, H, D), dev, stream)
+        k_out = _empty((T, H, D), cache.device, stream)
     if v_out is None:
-        v_out = _empty((T, H, D), dev, stream)
+        v_out = _empty((T, H, D), cache.device, stream)
     _, ks = _rows_of(k_out, T, H, D, dev, "k_out")
     _, vs = _rows_of(v_out, T, H, D, dev, "v_out")
-    _check(lib().qmd_kv_read(cache.ptrs, batch.ptrs, k_out.data_ptr(), ks, v_out.data_ptr(), vs, st))
+    st = lib().qmd_kv_read(cache.ptrs, batch.ptrs, k_out.data_ptr(), ks, v_out.data_ptr(), vs, st)
+    if st:
+        _check(st)
     return k_out, v_out
+
+
+_workspace_words: dict = {}  # of qmd_kv_workspace_bytes on the devices called so far
 
 
 def kv_workspace(device="cuda"):
@@ -457,16 +475,19 @@ def kv_attention(cache: KVCache, batch: KVBatch, q, scale: float, workspace, win
     """qmd_kv_attention: attention of the rows' queries (rotated; f32 [rows, heads, head_dim], strided
     by rows only) over the cached keys and values of their sequences.  out f32, by default
     [rows, heads * head_dim]; rows that no sequence owns are not written."""
-    import torch
     st = _kv_stream(cache, batch, stream)
-    D, dev, T = cache.head_dim, cache.device, batch.rows
+    D, dev, T = cache.head_dim, cache.index, batch.rows
     heads, qs = _rows_of(q, T, None, D, dev, "q")
     if out is None:
-        out = _empty((T, heads * D), dev, stream)
+        out = _empty((T, heads * D), cache.device, stream)
     _, os_ = _rows_of(out, T, heads, D, dev, "out")
     L = lib()
-    ws = _array(workspace, torch.int32, (L.qmd_kv_workspace_bytes() // 4,), dev, "workspace")
-    _check(L.qmd_kv_attention(cache.ptrs, batch.ptrs, q.data_ptr(), qs, heads, scale, window, out.data_ptr(), os_, ws, st))
+    if dev not in _workspace_words:
+        _workspace_words[dev] = (int(L.qmd_kv_workspace_bytes()) // 4,)
+    ws = _array(workspace, _I32, _workspace_words[dev], dev, "workspace")
+    st = L.qmd_kv_attention(cache.ptrs, batch.ptrs, q.data_ptr(), qs, heads, scale, window, out.data_ptr(), os_, ws, st)
+    if st:
+        _check(st)
     return out
 
 
@@ -475,24 +496,26 @@ def lora_add(x, base, A, B, adapter, scale, out=None, stream=None):
     where a < 0.  x f32 [batch, K]; base, out f32 [batch, rows] (out may be base); A f16 or bf16
     [adapters, rank, K], B [adapters, rows, rank]; adapter int32 [batch]; scale f32 [adapters]."""
     import torch
-    st = _stream_on(stream, x, "x")
-    dev = x.device
-    if A.dtype is torch.float16:
-        half = F16
-    elif A.dtype is torch.bfloat16:
-        half = BF16
-    else:
-        raise QmdError(2, f"A: float16 or bfloat16 is wanted, got {A.dtype}")
+    if _F32 is None:
+        _torch_names()
+    dev = x.get_device()
+    st = _stream_on(stream, dev, "x")
+    half = A.dtype
+    if half is not torch.float16 and half is not torch.bfloat16:
+        raise QmdError(2, f"A: float16 or bfloat16 is wanted, got {half}")
     if A.dim() != 3 or x.dim() != 2 or base.dim() != 2:
         raise QmdError(6, "x [batch, K], base [batch, rows] and A [adapters, rank, K] are wanted")
-    (n, rank, K), batch, rows = A.shape, x.shape[0], base.shape[1]
+    (n, rank, K), (batch, rows) = A.shape, base.shape
+    y = _array(base, _F32, (batch, rows), dev, "base")
     if out is None:
-        out = _empty((batch, rows), dev, stream)
-    f32 = torch.float32
-    _check(lib().qmd_lora_add(half, _array(x, f32, (batch, K), dev, "x"), _array(base, f32, (batch, rows), dev, "base"),
-                              _array(A, A.dtype, (n, rank, K), dev, "A"), _array(B, A.dtype, (n, rows, rank), dev, "B"),
-                              _array(scale, f32, (n,), dev, "scale"), _array(adapter, torch.int32, (batch,), dev, "adapter"),
-                              _array(out, f32, (batch, rows), dev, "out"), K, rows, rank, n, batch, st))
+        out = _empty((batch, rows), x.device, stream)
+    o = y if out is base else _array(out, _F32, (batch, rows), dev, "out")
+    st = lib().qmd_lora_add(F16 if half is torch.float16 else BF16, _array(x, _F32, (batch, K), dev, "x"), y,
+                            _array(A, half, (n, rank, K), dev, "A"), _array(B, half, (n, rows, rank), dev, "B"),
+                            _array(scale, _F32, (n,), dev, "scale"), _array(adapter, _I32, (batch,), dev, "adapter"), o,
+                            K, rows, rank, n, batch, st)
+    if st:
+        _check(st)
     return out
 
 

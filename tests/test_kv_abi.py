@@ -149,10 +149,10 @@ def test_python_side_refuses_what_the_library_cannot_see():
     with pytest.raises(q.QmdError, match="QMD_ERR_DEVICE"):
         q.lora_add(torch.zeros((1, 256)), torch.zeros((1, 8)), torch.zeros((1, 8, 256)), torch.zeros((1, 8, 8)), n[:1], torch.zeros(1))
     rows = torch.zeros((2, 4 * 64 + 8))
-    assert q._rows_of(rows[:, :256], 2, 4, 64, rows.device, "x") == (4, 264)
+    assert q._rows_of(rows[:, :256], 2, 4, 64, -1, "x") == (4, 264)
     for bad in (rows[:, :250], rows[:1, :256], rows[:, :256].double(), rows[:, 0:256:2], rows[:, :256].unflatten(1, (4, 64)).transpose(1, 2)):
         with pytest.raises(q.QmdError):
-            q._rows_of(bad, 2, None, 64, rows.device, "x")
+            q._rows_of(bad, 2, None, 64, -1, "x")
 
 
 def test_rope_table():
