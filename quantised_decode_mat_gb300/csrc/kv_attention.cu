@@ -418,8 +418,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             const int blk = first_blk + i;
             return (page * p.heads + head - blk / a.by_blocks) * p.page_blocks + blk;
         };
-        const int page_c = page_of(lane), page_n = page_of(32 + lane);
-        int page_nn = page_of(64 + lane);
+        int page_n = page_of(lane);
         // lane (g, t) takes dimensions 64 h + 16 t + 0..15 of a query row: that of column g (two columns to
         // a row), or rows g and g + 8; past the rows the last one again
         float x[QR][KH][16];
@@ -431,7 +430,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             for (int h = 0; h < KH; ++h)
                 load_f32(x[i][h], qp + 64 * h);
         }
-        int bi_n = block_of(lane, page_c);
+        int bi_n = block_of(lane, page_n);
         fence_proxy_async_smem();
         __syncwarp();  // every lane has read the last item's ring and meta
 
@@ -455,19 +454,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             put = put + 1 == S ? 0 : put + 1;
         }
         float ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
-        int bi_1 = -1;
-        float ks_1 = 0.0f, vs_1 = 0.0f;
-        if (real > 32) {
-            bi_1 = block_of(32 + lane, page_n);
-            ks_1 = bi_1 >= 0 ? p.ks[bi_1] : 0.0f, vs_1 = bi_1 >= 0 ? p.vs[bi_1] : 0.0f;
-        }
         meta[lane] = make_int4(bi_n, __float_as_int(ks_n), __float_as_int(vs_n), 0);
-        meta[32 + lane] = make_int4(bi_1, __float_as_int(ks_1), __float_as_int(vs_1), 0);
-        if (real > 64) {
-            bi_n = block_of(64 + lane, page_nn);
-            ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
-            page_nn = page_of(96 + lane);
-        }
         __syncwarp();
 
         // ---- the queries as two f16 parts ------------------------------------------------------
@@ -595,13 +582,18 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             return false;
         };
         for (int idx = 0; idx < real && !dead; ++idx) {
-            if ((idx & 31) == 0 && idx > 0 && idx + 32 < real) {
-                __syncwarp();
-                meta[(idx + 32 + lane) & 63] = make_int4(bi_n, __float_as_int(ks_n), __float_as_int(vs_n), 0);
-                bi_n = block_of(idx + 64 + lane, page_nn);
-                ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
-                page_nn = page_of(idx + 96 + lane);
-                __syncwarp();
+            if ((idx & 7) == 0 && (idx | 31) + 1 < real) {  // the next 32 blocks, a step of their lookup at a time
+                const int i = (idx | 31) + 1 + lane;
+                if ((idx & 24) == 0) {
+                    page_n = page_of(i);
+                } else if ((idx & 24) == 8) {
+                    bi_n = block_of(i, page_n);
+                    ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
+                } else if ((idx & 24) == 16) {
+                    __syncwarp();
+                    meta[i & 63] = make_int4(bi_n, __float_as_int(ks_n), __float_as_int(vs_n), 0);
+                    __syncwarp();
+                }
             }
             const uint32_t next = use + 1 == S ? 0 : use + 1, next_phase = next == 0 ? use_phase ^ 1u : use_phase;
             fence_proxy_async_smem();
