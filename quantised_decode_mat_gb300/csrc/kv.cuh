@@ -101,42 +101,31 @@ __device__ __forceinline__ void load_f32(float (&x)[N], const float *p)
             const float4 a = *reinterpret_cast<const float4 *>(p + i);
             x[i] = a.x, x[i + 1] = a.y, x[i + 2] = a.z, x[i + 3] = a.w;
         }
-    } else if constexpr (N == 2) {
+    } else {
+        static_assert(N == 2, "2 or a multiple of 4 values");
         const float2 a = *reinterpret_cast<const float2 *>(p);
         x[0] = a.x, x[1] = a.y;
-    } else {
-        static_assert(N == 1, "1, 2 or a multiple of 4 values");
-        x[0] = *p;
     }
 }
 
 template <int N>
 __device__ __forceinline__ void store_f32(float *p, const float (&x)[N])
 {
-    if constexpr (N % 4 == 0) {
+    static_assert(N % 4 == 0, "a multiple of 4 values");
 #pragma unroll
-        for (int i = 0; i < N; i += 4)
-            *reinterpret_cast<float4 *>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-    } else {
-        static_assert(N == 2, "2 or a multiple of 4 values");
-        *reinterpret_cast<float2 *>(p) = make_float2(x[0], x[1]);
-    }
+    for (int i = 0; i < N; i += 4)
+        *reinterpret_cast<float4 *>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
 }
 
 // N int8 codes at p as f32 (exact).
 template <int N>
 __device__ __forceinline__ void load_codes(float (&x)[N], const int8_t *p)
 {
-    if constexpr (N % 4 == 0) {
+    static_assert(N % 4 == 0, "a multiple of 4 codes");
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const char4 a = *reinterpret_cast<const char4 *>(p + i);
-            x[i] = (float)a.x, x[i + 1] = (float)a.y, x[i + 2] = (float)a.z, x[i + 3] = (float)a.w;
-        }
-    } else {
-        static_assert(N == 2, "2 or a multiple of 4 codes");
-        const char2 a = *reinterpret_cast<const char2 *>(p);
-        x[0] = (float)a.x, x[1] = (float)a.y;
+    for (int i = 0; i < N; i += 4) {
+        const char4 a = *reinterpret_cast<const char4 *>(p + i);
+        x[i] = (float)a.x, x[i + 1] = (float)a.y, x[i + 2] = (float)a.z, x[i + 3] = (float)a.w;
     }
 }
 

@@ -10,14 +10,18 @@
 // intrinsics): the same inputs give the same codes as any other program that does these steps.
 //
 // Layout: a CTA looks up a chunk of 16 rows -- the sequence, position and page of each, once --
-// and its warps take tasks: one (block, head, K or V) or one query (row, head) each.  A row is the
+// and its warps take tasks: a block of one head's K or V (two heads of 64), or 1024 query values of a
+// row.  A row is the
 // leader of a block if it is the first of the call's rows in it; the block's task is done by the
-// leader's chunk, so no two warps touch a block's scale and no atomics are needed.  Lane l owns
-// head_dim / 32 neighbouring values; a rotation partner half a head away comes by a shuffle.
+// leader's chunk, so no two warps touch a block's scale and no atomics are needed.  A lane owns 4 or 8
+// neighbouring values of a head; a rotation partner half a head away comes by a shuffle.  A block's new
+// rows wait in shared memory until its scale is known.
 //
 // Bound: memory for prompts (11739 rows of 32 + 2 x 8 heads of 128: 95 us for 511 MB, 5.4 TB/s; with
-// their blocks read back 131, 121 and 160 us at 4, 8 and 16 query heads a task; a read back of 32000
-// rows 61 us, 5.4 TB/s, with streaming stores 72), launch latency for single tokens (8 rows 3.5 us).
+// their blocks read back 131, 121 and 160 us at 4, 8 and 16 query heads a task; the rows by cp.async, all
+// in flight, 122; a read back of 32000 rows 60 us, 5.5 TB/s, with streaming stores 72), launch latency
+// for single tokens (8 rows 3.5 us).  64-wide heads two to a warp: 40 us against 47 with one (8 bytes a
+// lane); 256-wide ones with 2 rows in flight 143 against 153 with 4 (registers).
 #include <mutex>
 #include <set>
 #include <utility>
@@ -32,7 +36,16 @@ namespace qmd {
 
 constexpr int APP_WARPS = 4;
 constexpr int APP_CHUNK = 16;  // rows a CTA looks up
-constexpr int APP_HEADS = 8;   // query heads of a task: their loads in flight together, the table's row read once
+
+// How a warp holds heads: E neighbouring values to a lane (16 bytes at least), so one head, or two of 64.
+template <int D>
+struct HeadLanes {
+    static constexpr int LPH = D < 128 ? D / 4 : 32;  // lanes to a head
+    static constexpr int HPW = 32 / LPH;              // heads to a warp
+    static constexpr int E = D / LPH;
+    static constexpr int QN = 32 / E;                 // loads of a query task in flight together (4 KB)
+    static constexpr int RN = 16 / E;                 // and of a read
+};
 
 struct KvRow {
     int seq;   // -1: a row that no sequence owns
@@ -90,46 +103,43 @@ struct Angles {
 };
 
 template <int E>
-__device__ __forceinline__ void load_angles(Angles<E> &a, const RopeArgs &r, int pos, int lane)
+__device__ __forceinline__ void load_angles(Angles<E> &a, const RopeArgs &r, int pos, int l)
 {
     const float *row = r.table + (int64_t)pos * r.rot;
     const int half = r.rot >> 1;
     if (r.pairs == QMD_ROPE_HALVES) {
         const int off = half / E;  // lanes between the two of a pair
-        if (lane < 2 * off) {
-            const int at = E * (lane < off ? lane : lane - off);
+        if (l < 2 * off) {
+            const int at = E * (l < off ? l : l - off);
             load_f32(a.c, row + at);
             load_f32(a.s, row + half + at);
         }
-    } else if (E * lane < r.rot) {
+    } else if (E * l < r.rot) {
         float c[E / 2], s[E / 2];
-        load_f32(c, row + E / 2 * lane);
-        load_f32(s, row + half + E / 2 * lane);
+        load_f32(c, row + E / 2 * l);
+        load_f32(s, row + half + E / 2 * l);
 #pragma unroll
         for (int i = 0; i < E / 2; ++i)
             a.c[i] = c[i], a.s[i] = s[i];
     }
 }
 
-// Rotate this lane's E values of a head (the warp holds the head).
+// Rotate this lane's E values of a head, of which it is lane l; o: the values of the lane half a
+// rotation away (not used for adjacent pairs).
 template <int E>
-__device__ __forceinline__ void rotate(float (&x)[E], const RopeArgs &r, const Angles<E> &a, int lane)
+__device__ __forceinline__ void rotate(float (&x)[E], const float (&o)[E], const RopeArgs &r, const Angles<E> &a, int l)
 {
     if (r.pairs == QMD_ROPE_HALVES) {
         const int off = (r.rot >> 1) / E;
-        const bool first = lane < off, second = !first && lane < 2 * off;
-        float o[E];
-#pragma unroll
-        for (int i = 0; i < E; ++i)
-            o[i] = __shfl_sync(0xffffffffu, x[i], first ? lane + off : second ? lane - off : lane);
-        if (first || second) {
+        const bool first = l < off;
+        if (l < 2 * off) {
 #pragma unroll
             for (int i = 0; i < E; ++i) {
                 const float xc = __fmul_rn(x[i], a.c[i]), os = __fmul_rn(o[i], a.s[i]);
                 x[i] = first ? __fsub_rn(xc, os) : __fadd_rn(xc, os);
             }
         }
-    } else if (E * lane < r.rot) {
+    } else if (E * l < r.rot) {
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
             const float p = x[2 * i], q = x[2 * i + 1];
@@ -139,22 +149,31 @@ __device__ __forceinline__ void rotate(float (&x)[E], const RopeArgs &r, const A
     }
 }
 
+// The lane of its head that holds the other halves of lane l's pairs (l itself where it has none).
 template <int E>
+__device__ __forceinline__ int partner(const RopeArgs &r, int l)
+{
+    const int off = r.pairs == QMD_ROPE_HALVES ? (r.rot >> 1) / E : 0;
+    return l < off ? l + off : l < 2 * off ? l - off : l;
+}
+
+// The codes of E values: x * inv rounded to the nearest even integer by adding 1.5 * 2^23 (unit 1),
+// which leaves it in the low byte.  |x * inv| <= 127 (1 + 2^-22), as inv is 1 over a scale of at least
+// max |x| / 127, so nothing needs a clamp but a code of -128 that is stored again (EARLIER).
+template <bool EARLIER, int E>
 __device__ __forceinline__ void store_codes(int8_t *p, const float (&x)[E], float inv)
 {
-    uint32_t w[(E + 3) / 4] = {};
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        // NaN (an infinite value times 0) becomes 0
-        const int q = min(127, max(-127, __float2int_rn(__fmul_rn(x[i], inv))));
-        w[i / 4] |= (uint32_t)(q & 255) << (8 * (i % 4));
-    }
-    if constexpr (E == 2) {
-        *reinterpret_cast<uint16_t *>(p) = (uint16_t)w[0];
-    } else {
+    for (int i = 0; i < E; i += 4) {
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < E / 4; ++i)
-            reinterpret_cast<uint32_t *>(p)[i] = w[i];
+        for (int e = 0; e < 4; ++e)
+        {
+            const float q = __fmul_rn(x[i + e], inv);
+            w[e] = __float_as_uint(__fadd_rn(EARLIER ? fmaxf(q, -127.0f) : q, 12582912.0f));
+        }
+        *reinterpret_cast<uint32_t *>(p + i) =
+            __byte_perm(__byte_perm(w[0], w[1], 0x5140u), __byte_perm(w[2], w[3], 0x5140u), 0x5410u);
     }
 }
 
@@ -168,11 +187,12 @@ struct AppendArgs {
 };
 
 template <int D>
-__global__ void __launch_bounds__(APP_WARPS * 32) kv_append_kernel(const AppendArgs a)
+__global__ void __launch_bounds__(APP_WARPS * 32, D == 256 ? 3 : 4) kv_append_kernel(const AppendArgs a)
 {
-    constexpr int E = D / 32;
-    constexpr int RB = 4;  // rows whose loads are in flight together
-    extern __shared__ __align__(16) float s_x[];  // [warps][16][D]: a block's new rows until its scale is known
+    using H = HeadLanes<D>;
+    constexpr int E = H::E;
+    constexpr int RB = D == 256 ? 2 : 4;  // rows whose loads are in flight together
+    extern __shared__ __align__(16) float s_x[];  // [warps][16][D * HPW]: a block's new rows until its scale is known
     __shared__ KvRow s_row[APP_CHUNK];
     __shared__ int s_order[APP_CHUNK], s_count;
     pdl_launch_dependents();
@@ -181,12 +201,15 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv_append_kernel(const AppendA
     const int64_t t0 = (int64_t)blockIdx.x * APP_CHUNK;
     chunk_rows(p, t0, s_row, s_order, &s_count);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int blocks = s_count * p.heads * 2;
-    const int groups = (a.q_heads + APP_HEADS - 1) / APP_HEADS;
+    const int hl = lane / H::LPH, l = lane % H::LPH;  // which of the warp's heads, which lane of it
+    const int other = hl * H::LPH + partner<E>(a.rope, l);  // the lane with the other halves of its pairs
+    const int kv_groups = (p.heads + H::HPW - 1) / H::HPW;
+    const int blocks = s_count * kv_groups * 2;
+    const int groups = (a.q_heads + H::QN * H::HPW - 1) / (H::QN * H::HPW);
     const int tasks = blocks + (a.q ? APP_CHUNK * groups : 0);
     for (int task = blockIdx.y * APP_WARPS + warp; task < tasks; task += gridDim.y * APP_WARPS) {
-        if (task >= blocks) {  // APP_HEADS query heads of a row
-            const int i = (task - blocks) / groups, h = (task - blocks) % groups * APP_HEADS;
+        if (task >= blocks) {  // some query heads of a row: their loads in flight together, its angles read once
+            const int i = (task - blocks) / groups, h = (task - blocks) % groups * (H::QN * H::HPW);
             const KvRow r = s_row[i];
             if (r.seq < 0)
                 continue;
@@ -194,27 +217,33 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv_append_kernel(const AppendA
                 kv_index_error(p);
                 continue;
             }
-            const float *src = a.q + (t0 + i) * a.q_stride + h * D + E * lane;
-            float *dst = a.q_out + (t0 + i) * a.q_out_stride + h * D + E * lane;
-            float x[APP_HEADS][E];
+            const float *src = a.q + (t0 + i) * a.q_stride + (h + hl) * D + E * l;
+            float *dst = a.q_out + (t0 + i) * a.q_out_stride + (h + hl) * D + E * l;
+            float x[H::QN][E];
 #pragma unroll
-            for (int j = 0; j < APP_HEADS; ++j)
-                if (h + j < a.q_heads)
-                    load_f32(x[j], src + j * D);
+            for (int j = 0; j < H::QN; ++j)
+                if (h + hl + j * H::HPW < a.q_heads)
+                    load_f32(x[j], src + j * H::HPW * D);
             Angles<E> ang;
             if (a.rope.table)
-                load_angles(ang, a.rope, r.pos, lane);
+                load_angles(ang, a.rope, r.pos, l);
 #pragma unroll
-            for (int j = 0; j < APP_HEADS; ++j)
-                if (h + j < a.q_heads) {
-                    if (a.rope.table)
-                        rotate(x[j], a.rope, ang, lane);
-                    store_f32(dst + j * D, x[j]);
+            for (int j = 0; j < H::QN; ++j)
+                if (h + j * H::HPW < a.q_heads) {  // (the same for every lane)
+                    if (a.rope.table) {
+                        float o[E];
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            o[e] = __shfl_sync(0xffffffffu, x[j][e], other);
+                        rotate(x[j], o, a.rope, ang, l);
+                    }
+                    if (h + hl + j * H::HPW < a.q_heads)
+                        store_f32(dst + j * H::HPW * D, x[j]);
                 }
             continue;
         }
-        const int i = s_order[task / (2 * p.heads)], h = task / 2 % p.heads;
-        const bool is_v = task & 1;
+        const int i = s_order[task / (2 * kv_groups)], h = task / 2 % kv_groups * H::HPW + hl;
+        const bool is_v = task & 1, ok = h < p.heads;
         const KvRow r = s_row[i];
         const bool turn = a.rope.table && !is_v;
         const int tok0 = r.pos % KV_BLOCK;
@@ -225,66 +254,75 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv_append_kernel(const AppendA
             if (m <= 0)
                 continue;
         }
-        const float *src = (is_v ? a.v + (t0 + i) * a.v_stride : a.k + (t0 + i) * a.k_stride) + h * D + E * lane;
         const int64_t stride = is_v ? a.v_stride : a.k_stride;
-        const int64_t blk = kv_block_offset(p, r.page, h, r.pos / KV_BLOCK);
-        int8_t *codes = (is_v ? p.v : p.k) + blk * (KV_BLOCK * D) + E * lane;
+        const float *src = (is_v ? a.v : a.k) + (t0 + i) * stride + h * D + E * l;
+        const int64_t blk = kv_block_offset(p, r.page, ok ? h : 0, r.pos / KV_BLOCK);
+        int8_t *codes = (is_v ? p.v : p.k) + blk * (KV_BLOCK * D) + E * l;
         float *scale = (is_v ? p.vs : p.ks) + blk;
 
-        float *keep = s_x + warp * KV_BLOCK * D + E * lane;  // each lane reads back its own
+        // the block's new rows, RB at a time with their loads in flight together, wait in shared memory
+        // until the scale is known; each lane reads back its own
+        constexpr int ROW = D * H::HPW;
+        float *keep = s_x + warp * KV_BLOCK * ROW + E * lane;
+        const float d0 = ok && tok0 > 0 ? *scale : 0.0f;
         float top = 0.0f;
         for (int j0 = 0; j0 < m; j0 += RB) {
-            float x[RB][E];
+            float x[RB][E] = {};
             Angles<E> ang[RB];
 #pragma unroll
             for (int j = 0; j < RB; ++j)
                 if (j0 + j < m) {
-                    load_f32(x[j], src + (j0 + j) * stride);
+                    if (ok)
+                        load_f32(x[j], src + (j0 + j) * stride);
                     if (turn)
-                        load_angles(ang[j], a.rope, r.pos + j0 + j, lane);
+                        load_angles(ang[j], a.rope, r.pos + j0 + j, l);
                 }
 #pragma unroll
             for (int j = 0; j < RB; ++j)
-                if (j0 + j < m) {
-                    if (turn)
-                        rotate(x[j], a.rope, ang[j], lane);
-                    store_f32(keep + (j0 + j) * D, x[j]);
+                if (j0 + j < m) {  // (the same for every lane)
+                    if (turn) {
+                        float o[E];
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            o[e] = __shfl_sync(0xffffffffu, x[j][e], other);
+                        rotate(x[j], o, a.rope, ang[j], l);
+                    }
+                    store_f32(keep + (j0 + j) * ROW, x[j]);
 #pragma unroll
                     for (int e = 0; e < E; ++e)
                         top = fmaxf(top, fabsf(x[j][e]));
                 }
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
+        for (int o = H::LPH / 2; o > 0; o >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float d0 = tok0 > 0 ? *scale : 0.0f;
         const float d = fmaxf(d0, top < 1e-30f ? 0.0f : __fdiv_rn(top, 127.0f));
         const float inv = d > 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
-        if (d > d0) {
-            // the block's earlier tokens in steps of the larger scale
+        if (ok) {
+            if (d > d0) {
+                // the block's earlier tokens in steps of the larger scale
 #pragma unroll 2
-            for (int j = 0; j < tok0; ++j) {
-                float y[E];
-                load_codes(y, codes + j * D);
+                for (int j = 0; j < tok0; ++j) {
+                    float y[E];
+                    load_codes(y, codes + j * D);
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    y[e] = __fmul_rn(y[e], d0);
-                store_codes(codes + j * D, y, inv);
+                    for (int e = 0; e < E; ++e)
+                        y[e] = __fmul_rn(y[e], d0);
+                    store_codes<true>(codes + j * D, y, inv);
+                }
+            }
+#pragma unroll 4
+            for (int j = 0; j < m; ++j) {
+                float x[E];
+                load_f32(x, keep + j * ROW);
+                store_codes<false>(codes + (tok0 + j) * D, x, inv);
             }
         }
-#pragma unroll 4
-        for (int j = 0; j < m; ++j) {
-            float x[E];
-            load_f32(x, keep + j * D);
-            store_codes(codes + (tok0 + j) * D, x, inv);
-        }
         __syncwarp();  // every lane has read the old scale
-        if (lane == 0)
+        if (ok && l == 0)
             *scale = d;
     }
 }
-
-constexpr int READ_HEADS = 4;
 
 struct ReadArgs {
     KvParams kv;
@@ -295,7 +333,8 @@ struct ReadArgs {
 template <int D>
 __global__ void __launch_bounds__(APP_WARPS * 32) kv_read_kernel(const ReadArgs a)
 {
-    constexpr int E = D / 32;
+    using H = HeadLanes<D>;
+    constexpr int E = H::E;
     __shared__ KvRow s_row[APP_CHUNK];
     __shared__ int s_order[APP_CHUNK], s_count;
     pdl_launch_dependents();
@@ -304,34 +343,35 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv_read_kernel(const ReadArgs 
     const int64_t t0 = (int64_t)blockIdx.x * APP_CHUNK;
     chunk_rows(p, t0, s_row, s_order, &s_count);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // a warp takes READ_HEADS neighbouring heads of a row, keys or values: their loads in flight together
-    const int groups = (p.heads + READ_HEADS - 1) / READ_HEADS;
+    const int hl = lane / H::LPH, l = lane % H::LPH;
+    // a warp takes some neighbouring heads of a row, keys or values: their loads in flight together
+    const int groups = (p.heads + H::RN * H::HPW - 1) / (H::RN * H::HPW);
     const int tasks = APP_CHUNK * groups * 2;
     for (int task = blockIdx.y * APP_WARPS + warp; task < tasks; task += gridDim.y * APP_WARPS) {
-        const int i = task / (2 * groups), h = task / 2 % groups * READ_HEADS;
+        const int i = task / (2 * groups), h = task / 2 % groups * (H::RN * H::HPW) + hl;
         const bool is_v = task & 1;
         const KvRow r = s_row[i];
         float *out = is_v ? a.v : a.k;
         if (r.seq < 0 || r.page < 0 || !out)
             continue;
         const int64_t blk = kv_block_offset(p, r.page, h, r.pos / KV_BLOCK);
-        const int8_t *codes = (is_v ? p.v : p.k) + (blk * KV_BLOCK + r.pos % KV_BLOCK) * D + E * lane;
+        const int8_t *codes = (is_v ? p.v : p.k) + (blk * KV_BLOCK + r.pos % KV_BLOCK) * D + E * l;
         const float *scale = (is_v ? p.vs : p.ks) + blk;
-        float x[READ_HEADS][E], d[READ_HEADS];
+        float x[H::RN][E], d[H::RN];
 #pragma unroll
-        for (int j = 0; j < READ_HEADS; ++j)
-            if (h + j < p.heads) {
-                load_codes(x[j], codes + (int64_t)j * p.page_blocks * (KV_BLOCK * D));
-                d[j] = scale[j * p.page_blocks];
+        for (int j = 0; j < H::RN; ++j)
+            if (h + j * H::HPW < p.heads) {
+                load_codes(x[j], codes + (int64_t)j * H::HPW * p.page_blocks * (KV_BLOCK * D));
+                d[j] = scale[j * H::HPW * p.page_blocks];
             }
-        float *dst = out + (t0 + i) * (is_v ? a.v_stride : a.k_stride) + h * D + E * lane;
+        float *dst = out + (t0 + i) * (is_v ? a.v_stride : a.k_stride) + h * D + E * l;
 #pragma unroll
-        for (int j = 0; j < READ_HEADS; ++j)
-            if (h + j < p.heads) {
+        for (int j = 0; j < H::RN; ++j)
+            if (h + j * H::HPW < p.heads) {
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     x[j][e] = __fmul_rn(x[j][e], d[j]);
-                store_f32(dst + j * D, x[j]);
+                store_f32(dst + j * H::HPW * D, x[j]);
             }
     }
 }
@@ -389,8 +429,8 @@ qmd_status launch_kv_append(const KvParams &kv, int head_dim, const float *k, in
     const AppendArgs a = {kv, {rope, rope_rows, rot, pairs}, k, v, q, q_out, k_stride, v_stride, q_stride,
                           q_out_stride, q_heads};
     const int64_t rows = kv.rows < APP_CHUNK ? kv.rows : APP_CHUNK;
-    const int64_t tasks = rows * (2 * kv.heads + (q_heads + APP_HEADS - 1) / APP_HEADS);
-    const size_t smem = (size_t)APP_WARPS * KV_BLOCK * head_dim * 4;
+    const int64_t tasks = rows * (2 * kv.heads + (q_heads * head_dim + 1023) / 1024);
+    const size_t smem = (size_t)APP_WARPS * KV_BLOCK * (head_dim < 128 ? 128 : head_dim) * 4;
     return head_dim == 64    ? launch_chunks(kv_append_kernel<64>, a, tasks, sms, smem, "kv_append launch", s)
            : head_dim == 128 ? launch_chunks(kv_append_kernel<128>, a, tasks, sms, smem, "kv_append launch", s)
                              : launch_chunks(kv_append_kernel<256>, a, tasks, sms, smem, "kv_append launch", s);
@@ -401,7 +441,7 @@ qmd_status launch_kv_read(const KvParams &kv, int head_dim, float *k, int64_t k_
 {
     const ReadArgs a = {kv, k, v, k_stride, v_stride};
     const int64_t rows = kv.rows < APP_CHUNK ? kv.rows : APP_CHUNK;
-    const int64_t tasks = rows * 2 * ((kv.heads + READ_HEADS - 1) / READ_HEADS);
+    const int64_t tasks = rows * 2 * ((kv.heads * head_dim + 511) / 512);
     return head_dim == 64    ? launch_chunks(kv_read_kernel<64>, a, tasks, sms, 0, "kv_read launch", s)
            : head_dim == 128 ? launch_chunks(kv_read_kernel<128>, a, tasks, sms, 0, "kv_read launch", s)
                              : launch_chunks(kv_read_kernel<256>, a, tasks, sms, 0, "kv_read launch", s);
