@@ -42,8 +42,8 @@
 //
 // Measured: 48 sequences of 2500-12301 tokens (32 heads over 8 of 128) 125 us, 6.24 TB/s, 0.93 of the
 // copy rate; per-lane cp.async instead of tensor copies 166 us, with or without the arithmetic.  One
-// sequence of 32768 23 us, of 17 8.8 us: lookups that wait for each other, and the joins.  16 rows to a
-// head (16 x 8100 tokens, 4 rows each) 77 us against 40 for the bytes: 8 warps to an SM are few for it.
+// sequence of 32768 22.4 us, of 17 8.6 us: lookups that wait for each other, and the joins.  16 rows to a
+// head (16 x 8100 tokens, 4 rows each) 78 us against 40 for the bytes: 8 warps to an SM are few for it.
 #include <climits>
 #include <cstring>
 #include <mutex>
