@@ -506,14 +506,22 @@ def lora_add(x, base, A, B, adapter, scale, out=None, stream=None):
     if A.dim() != 3 or x.dim() != 2 or base.dim() != 2:
         raise QmdError(6, "x [batch, K], base [batch, rows] and A [adapters, rank, K] are wanted")
     (n, rank, K), (batch, rows) = A.shape, base.shape
-    y = _array(base, _F32, (batch, rows), dev, "base")
     if out is None:
         out = _empty((batch, rows), x.device, stream)
-    o = y if out is base else _array(out, _F32, (batch, rows), dev, "out")
-    st = lib().qmd_lora_add(F16 if half is torch.float16 else BF16, _array(x, _F32, (batch, K), dev, "x"), y,
-                            _array(A, half, (n, rank, K), dev, "A"), _array(B, half, (n, rows, rank), dev, "B"),
-                            _array(scale, _F32, (n,), dev, "scale"), _array(adapter, _I32, (batch,), dev, "adapter"), o,
-                            K, rows, rank, n, batch, st)
+    # all of it in one condition (seven tensors: a call of _array for each costs 1 us more); what is
+    # wrong is found out below
+    if not (x.dtype is base.dtype is scale.dtype is out.dtype is _F32 and B.dtype is half and adapter.dtype is _I32
+            and x.shape == (batch, K) and B.shape == (n, rows, rank) and scale.shape == (n,) and adapter.shape == (batch,)
+            and out.shape == (batch, rows) and x.is_contiguous() and base.is_contiguous() and A.is_contiguous()
+            and B.is_contiguous() and scale.is_contiguous() and adapter.is_contiguous() and out.is_contiguous()
+            and dev == base.get_device() == A.get_device() == B.get_device() == scale.get_device()
+            == adapter.get_device() == out.get_device()):
+        for t, dtype, shape, what in ((x, _F32, (batch, K), "x"), (base, _F32, (batch, rows), "base"), (A, half, A.shape, "A"),
+                                      (B, half, (n, rows, rank), "B"), (scale, _F32, (n,), "scale"),
+                                      (adapter, _I32, (batch,), "adapter"), (out, _F32, (batch, rows), "out")):
+            _array(t, dtype, shape, dev, what)
+    st = lib().qmd_lora_add(F16 if half is torch.float16 else BF16, x.data_ptr(), base.data_ptr(), A.data_ptr(), B.data_ptr(),
+                            scale.data_ptr(), adapter.data_ptr(), out.data_ptr(), K, rows, rank, n, batch, st)
     if st:
         _check(st)
     return out

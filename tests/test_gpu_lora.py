@@ -129,3 +129,19 @@ def test_two_streams_and_large_and_small_values():
     torch.cuda.synchronize()
     for (t, _, _), o in zip(jobs, outs):
         check(t, o)
+
+
+def test_refusals_of_the_binding():
+    x, base, A, B, idx, scale = [a.to(DEV) for a in make(2, 3, 8, 512, 40, torch.float16)]
+    wide = torch.zeros((2, 80), device=DEV)
+    for bad in ((x.double(), base, A, B, idx, scale), (x[:1], base, A, B, idx, scale), (x, base[:, :39], A, B, idx, scale),
+                (x, wide[:, :40], A, B, idx, scale), (x, base, A.bfloat16(), B, idx, scale), (x, base, A.float(), B, idx, scale),
+                (x, base, A, B[:2], idx, scale), (x, base, A, B.transpose(1, 2), idx, scale), (x, base, A, B, idx.long(), scale),
+                (x, base, A, B, idx[:1], scale), (x, base, A, B, idx, scale[:2]), (x, base, A, B, idx, scale.cpu()),
+                (x, base, A[0], B, idx, scale), (x, base.cpu(), A, B, idx, scale)):
+        with pytest.raises(q.QmdError):
+            q.lora_add(*bad)
+    for out in (torch.empty((2, 41), device=DEV), torch.empty((2, 40), dtype=torch.float64, device=DEV), wide[:, 40:], x[:, :40]):
+        with pytest.raises(q.QmdError):
+            q.lora_add(x, base, A, B, idx, scale, out=out)
+    q.get_device_error()
