@@ -9,7 +9,7 @@
 // Codes are decided by rounding, so every f32 operation is rounded on its own (explicit _rn
 // intrinsics): the same inputs give the same codes as any other program that does these steps.
 //
-// Layout: a CTA looks up a chunk of 16 rows -- the sequence, position and page of each, once --
+// Layout: a CTA looks up a chunk of 32 rows -- the sequence, position and page of each, once --
 // and its warps take tasks: a block of one head's K or V (two heads of 64), or 1024 query values of a
 // row.  A row is the
 // leader of a block if it is the first of the call's rows in it; the block's task is done by the
@@ -19,9 +19,10 @@
 //
 // Bound: memory for prompts (11739 rows of 32 + 2 x 8 heads of 128: 95 us for 511 MB, 5.4 TB/s; with
 // their blocks read back 131, 121 and 160 us at 4, 8 and 16 query heads a task; the rows by cp.async, all
-// in flight, 122; a read back of 32000 rows 60 us, 5.5 TB/s, with streaming stores 72), launch latency
-// for single tokens (8 rows 3.5 us).  64-wide heads two to a warp: 40 us against 47 with one (8 bytes a
-// lane); 256-wide ones with 2 rows in flight 143 against 153 with 4 (registers).
+// in flight, 122; a read back of 32000 rows 56 us, 5.9 TB/s; streaming stores cost a fifth of that),
+// launch latency for single tokens (8 rows 3.5 us).  Chunks of 16 rows: 1 to 8 % more for appends.
+// 64-wide heads two to a warp: 40 us against 47 with one (8 bytes a lane); 256-wide ones with 2 rows in
+// flight 143 against 153 with 4 (registers).
 #include <mutex>
 #include <set>
 #include <utility>
@@ -35,7 +36,7 @@
 namespace qmd {
 
 constexpr int APP_WARPS = 4;
-constexpr int APP_CHUNK = 16;  // rows a CTA looks up
+constexpr int APP_CHUNK = 32;  // rows a CTA looks up, a lane each
 
 // How a warp holds heads: E neighbouring values to a lane (16 bytes at least), so one head, or two of 64.
 template <int D>
@@ -55,7 +56,7 @@ struct KvRow {
     int lead;  // the first of the call's rows in its block
 };
 
-// Fill rows[0..16) for the chunk and order[] with the chunk's leaders; all threads call it.
+// Fill rows[] for the chunk and order[] with the chunk's leaders; all threads call it.
 __device__ __forceinline__ void chunk_rows(const KvParams &p, int64_t t0, KvRow *rows, int *order, int *count)
 {
     if (threadIdx.x < 32) {
@@ -376,18 +377,20 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv_read_kernel(const ReadArgs 
     }
 }
 
-// CTAs per chunk: enough that every task has a warp while the launch has no more than a few waves.
-static unsigned chunk_ctas(int64_t chunks, int64_t tasks, int sms)
+// CTAs per chunk: enough that every task has a warp, while the launch has no more than `per_sm` CTAs an
+// SM.  Appends 16: 5400 rows of 16 + 2 x 16 heads of 128 take 64 us, 69 with 10 or 24.  Reads 32: 16000
+// rows of 8 heads of 256 take 59 us, 69 with 16, 63 with 24, 60 with 48.
+static unsigned chunk_ctas(int64_t chunks, int64_t tasks, int sms, int per_sm)
 {
     int64_t y = (tasks + APP_WARPS - 1) / APP_WARPS;
-    const int64_t most = (int64_t)sms * 16 / chunks;
+    const int64_t most = (int64_t)sms * per_sm / chunks;
     if (y > most)
         y = most;
     return (unsigned)(y < 1 ? 1 : y > 65535 ? 65535 : y);
 }
 
 template <class Args>
-static qmd_status launch_chunks(void (*kernel)(const Args), const Args &a, int64_t tasks, int sms, size_t smem,
+static qmd_status launch_chunks(void (*kernel)(const Args), const Args &a, int64_t tasks, int sms, int per_sm, size_t smem,
                                 const char *what, cudaStream_t s)
 {
     if (smem > 48 * 1024) {
@@ -408,7 +411,7 @@ static qmd_status launch_chunks(void (*kernel)(const Args), const Args &a, int64
     }
     const int64_t chunks = (a.kv.rows + APP_CHUNK - 1) / APP_CHUNK;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)chunks, chunk_ctas(chunks, tasks, sms));
+    cfg.gridDim = dim3((unsigned)chunks, chunk_ctas(chunks, tasks, sms, per_sm));
     cfg.blockDim = dim3(APP_WARPS * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
@@ -431,9 +434,9 @@ qmd_status launch_kv_append(const KvParams &kv, int head_dim, const float *k, in
     const int64_t rows = kv.rows < APP_CHUNK ? kv.rows : APP_CHUNK;
     const int64_t tasks = rows * (2 * kv.heads + (q_heads * head_dim + 1023) / 1024);
     const size_t smem = (size_t)APP_WARPS * KV_BLOCK * (head_dim < 128 ? 128 : head_dim) * 4;
-    return head_dim == 64    ? launch_chunks(kv_append_kernel<64>, a, tasks, sms, smem, "kv_append launch", s)
-           : head_dim == 128 ? launch_chunks(kv_append_kernel<128>, a, tasks, sms, smem, "kv_append launch", s)
-                             : launch_chunks(kv_append_kernel<256>, a, tasks, sms, smem, "kv_append launch", s);
+    return head_dim == 64    ? launch_chunks(kv_append_kernel<64>, a, tasks, sms, 16, smem, "kv_append launch", s)
+           : head_dim == 128 ? launch_chunks(kv_append_kernel<128>, a, tasks, sms, 16, smem, "kv_append launch", s)
+                             : launch_chunks(kv_append_kernel<256>, a, tasks, sms, 16, smem, "kv_append launch", s);
 }
 
 qmd_status launch_kv_read(const KvParams &kv, int head_dim, float *k, int64_t k_stride, float *v, int64_t v_stride,
@@ -442,9 +445,9 @@ qmd_status launch_kv_read(const KvParams &kv, int head_dim, float *k, int64_t k_
     const ReadArgs a = {kv, k, v, k_stride, v_stride};
     const int64_t rows = kv.rows < APP_CHUNK ? kv.rows : APP_CHUNK;
     const int64_t tasks = rows * 2 * ((kv.heads * head_dim + 511) / 512);
-    return head_dim == 64    ? launch_chunks(kv_read_kernel<64>, a, tasks, sms, 0, "kv_read launch", s)
-           : head_dim == 128 ? launch_chunks(kv_read_kernel<128>, a, tasks, sms, 0, "kv_read launch", s)
-                             : launch_chunks(kv_read_kernel<256>, a, tasks, sms, 0, "kv_read launch", s);
+    return head_dim == 64    ? launch_chunks(kv_read_kernel<64>, a, tasks, sms, 32, 0, "kv_read launch", s)
+           : head_dim == 128 ? launch_chunks(kv_read_kernel<128>, a, tasks, sms, 32, 0, "kv_read launch", s)
+                             : launch_chunks(kv_read_kernel<256>, a, tasks, sms, 32, 0, "kv_read launch", s);
 }
 
 }  // namespace qmd
