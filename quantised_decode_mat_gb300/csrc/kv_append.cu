@@ -378,8 +378,8 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv_read_kernel(const ReadArgs 
 }
 
 // CTAs per chunk: enough that every task has a warp, while the launch has no more than `per_sm` CTAs an
-// SM.  Appends 16: 5400 rows of 16 + 2 x 16 heads of 128 take 64 us, 69 with 10 or 24.  Reads 32: 16000
-// rows of 8 heads of 256 take 59 us, 69 with 16, 63 with 24, 60 with 48.
+// SM.  Appends 16: 5400 rows of 16 + 2 x 16 heads of 128 and their read back take 64 us, 69 with 10 or 24.
+// Reads 32: 16000 rows of 8 heads of 256 take 59 us, 69 with 16, 63 with 24, 60 with 48.
 static unsigned chunk_ctas(int64_t chunks, int64_t tasks, int sms, int per_sm)
 {
     int64_t y = (tasks + APP_WARPS - 1) / APP_WARPS;
