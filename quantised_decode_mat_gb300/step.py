@@ -24,10 +24,9 @@ from dataclasses import dataclass, field
 
 import numpy as np
 
-from . import (Q4_K, Q6_K_SPLIT, QMD_QK, ROPE_HALVES, KVBatch, KVCache, Q8K, bind_q6k, kv_append, kv_attention,
-               kv_workspace, lora_add, q6k_prefix_stride, q8k_pack, qmatvec, qmatvec_x, rope_table)
+from . import (Q4_K, Q6_K_SPLIT, QMD_QK, ROPE_HALVES, KVBatch, KVCache, Q8K, QmdError, bind_q6k, kv_append,
+               kv_attention, kv_workspace, lora_add, q6k_prefix_stride, q8k_pack, qmatvec, qmatvec_x, rope_table)
 from . import synth
-
 
 @dataclass
 class Projection:
@@ -345,6 +344,17 @@ class AttentionBlock:
         import torch
         dev, D = self.cache.device, self.cache.head_dim
         self.q_width, self.kv_width = self.heads * D, self.cache.kv_heads * D
+        # the mat-vecs take addresses: what they would read and write is checked here and in run
+        for W, rows, K, what in ((self.W_qkv, self.q_width + 2 * self.kv_width, self.hidden, "W_qkv"),
+                                 (self.W_o, self.hidden, self.q_width, "W_o")):
+            if K % QMD_QK:
+                raise QmdError(3, f"{what}: rows of {K} values")
+            if W.dtype is not torch.uint8:
+                raise QmdError(2, f"{what}: uint8 blocks are wanted, got {W.dtype}")
+            if W.shape[0] != rows or W.numel() != rows * (K // QMD_QK) * synth.Q4K_BLOCK_BYTES or not W.is_contiguous():
+                raise QmdError(6, f"{what}: {rows} rows of {K // QMD_QK} Q4_K blocks are wanted, got {tuple(W.shape)}")
+            if W.device != dev:
+                raise QmdError(9, f"{what} is on {W.device}, not on the cache's device")
         f32 = dict(dtype=torch.float32, device=dev)
         self.qkv = torch.empty((self.rows, self.q_width + 2 * self.kv_width), **f32)
         self.attended = torch.empty((self.rows, self.q_width), **f32)
@@ -356,7 +366,23 @@ class AttentionBlock:
     def run(self, x, batch: KVBatch, adapter=None, stream=None):
         """One call's rows through the block: x f32 [rows, hidden]; batch says which sequences they
         belong to (kv_len counts them in); adapter int32 [rows] picks each row's adapter (below 0:
-        none) where the block has adapters.  Returns y."""
+        none) where the block has adapters.  Returns y.  A call whose arguments are refused has
+        launched nothing."""
+        if x.dtype is not self.qkv.dtype:
+            raise QmdError(2, f"x: float32 is wanted, got {x.dtype}")
+        adapted = self.qkv_adapters is not None or self.o_adapters is not None
+        if (x.dim() != 2 or x.shape[1] != self.hidden or not x.is_contiguous() or not batch.rows <= x.shape[0] <= self.rows
+                or adapted and x.shape[0] != self.rows):
+            raise QmdError(6, f"x: contiguous [{self.rows}, {self.hidden}] is wanted, got {tuple(x.shape)} for a batch of "
+                              f"{batch.rows} rows")
+        if x.device != self.qkv.device:
+            raise QmdError(9, f"x is on {x.device}, not on the cache's device")
+        if batch.index != self.cache.index:
+            raise QmdError(9, f"the batch is on {batch.page_table.device}, the cache on {self.cache.device}")
+        if adapted and adapter is None:
+            raise QmdError(1, "adapter: the block has adapters, each row's choice is wanted")
+        if adapted and adapter.shape != (self.rows,):
+            raise QmdError(6, f"adapter: shape ({self.rows},) is wanted, got {tuple(adapter.shape)}")
         qmatvec_x(Q4_K, self.W_qkv, None, x, self.qkv, stream=stream)
         if self.qkv_adapters is not None:
             a = self.qkv_adapters
