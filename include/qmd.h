@@ -384,6 +384,7 @@ typedef enum qmd_rope_pairs { QMD_ROPE_HALVES = 0, QMD_ROPE_ADJACENT = 1 } qmd_r
  *   k, v    f32 rows of kv_heads * head_dim values, row r at k + r * k_stride
  *   q       f32 rows of q_heads * head_dim values, rotated into q_out; or NULL (then q_out NULL
  *           and q_heads 0).  q_out may be q itself with the same stride; no other overlap.
+ *           Row tensors may be parts of one wider buffer (equal strides, apart in a row).
  *   rope    f32 [rope_rows][rot]: rot / 2 cosines, then rot / 2 sines, of position p; or NULL
  *           (then rot 0): nothing is rotated and q is copied.  A position at or past rope_rows is
  *           an index error: that row is not stored.
@@ -407,6 +408,7 @@ qmd_status qmd_kv_append(const qmd_kv_cache *cache, const qmd_kv_batch *batch, c
  * reads any last part of each sequence.  A sequence shorter than its rows is an index error, but for
  * one without tokens (as in qmd_kv_append); the rows of neither are written.
  * Pointers 16-byte aligned, strides (in f32 values) multiples of 4 and at least kv_heads * head_dim.
+ * k_out and v_out may be parts of one wider buffer (equal strides, apart in a row).
  * Errors: NULL, SHAPE, MISALIGNED, VALUE (k_out and v_out overlap), DEVICE, LAUNCH.
  */
 qmd_status qmd_kv_read(const qmd_kv_cache *cache, const qmd_kv_batch *batch, float *k_out, int64_t k_stride,
@@ -423,7 +425,7 @@ qmd_status qmd_kv_read(const qmd_kv_cache *cache, const qmd_kv_batch *batch, flo
  * affect their own row and head only.
  *
  *   q         f32 rows of q_heads * head_dim values (rotated already), row r at q + r * q_stride
- *   out       f32 rows likewise; must not overlap q
+ *   out       f32 rows likewise; must not overlap q's rows (parts of one wider buffer do not)
  *   scale     finite (1 / sqrt(head_dim) as a rule)
  *   window    0: no window; else >= 1
  *   workspace device, qmd_kv_workspace_bytes() bytes, 16-byte aligned, owned by the caller.  Zero

@@ -1,6 +1,7 @@
 // api_kv.cu -- the C ABI of the key/value cache calls and of the adapters: argument validation on
 // the host, before anything is launched, with the same named statuses as api.cu.
 #include <cmath>
+#include <numeric>
 
 #include <cuda_runtime.h>
 
@@ -19,8 +20,30 @@ inline bool overlaps(const void *a, size_t na, const void *b, size_t nb)
     return a && b && pa < pb + nb && pb < pa + na;
 }
 
+// `rows` rows of `width` f32 values, a stride apart.
+struct Rows {
+    const void *p;
+    int64_t stride, width;
+};
+
 // Bytes from the first value of `rows` rows of `width` f32 values to the end of the last.
 inline size_t extent(int64_t rows, int64_t stride, int64_t width) { return ((size_t)(rows - 1) * stride + width) * 4; }
+
+// Do a's and b's rows overlap?  Parts of one wider buffer lie between each other's rows: every byte of
+// a's rows is 0 .. its width past a's first value, counted modulo the greatest common divisor of the
+// strides, so b's rows are apart from them if they fall behind that and end before the next one begins.
+// With equal strides that decides it; with others rows that interleave some other way count as overlapping.
+bool rows_overlap(const Rows &a, const Rows &b, int64_t rows)
+{
+    if (!a.p || !b.p || !overlaps(a.p, extent(rows, a.stride, a.width), b.p, extent(rows, b.stride, b.width)))
+        return false;
+    if (rows == 1)
+        return true;
+    const int64_t period = std::gcd(a.stride, b.stride) * 4;
+    const intptr_t apart = (intptr_t)reinterpret_cast<uintptr_t>(b.p) - (intptr_t)reinterpret_cast<uintptr_t>(a.p);
+    const int64_t at = (apart % period + period) % period;
+    return at < a.width * 4 || at + b.width * 4 > period;
+}
 
 // A row stride that keeps 16-byte alignment, holds a row, and cannot overflow an offset.
 inline bool stride_ok(int64_t stride, int64_t width) { return stride >= width && stride % 4 == 0 && stride < ((int64_t)1 << 36); }
@@ -95,9 +118,9 @@ qmd_status qmd_kv_append(const qmd_kv_cache *cache, const qmd_kv_batch *batch, c
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) || !aligned(rope, 16))
         return QMD_ERR_MISALIGNED;
     if (q && !(q_out == q && q_out_stride == q_stride)) {
-        const size_t n = extent(T, q_out_stride, qw);
-        if (overlaps(q_out, n, q, extent(T, q_stride, qw)) || overlaps(q_out, n, k, extent(T, k_stride, kw)) ||
-            overlaps(q_out, n, v, extent(T, v_stride, kw)))
+        const Rows out = {q_out, q_out_stride, qw};
+        if (rows_overlap(out, {q, q_stride, qw}, T) || rows_overlap(out, {k, k_stride, kw}, T) ||
+            rows_overlap(out, {v, v_stride, kw}, T))
             return QMD_ERR_VALUE;
     }
     DeviceInfo dev;
@@ -123,7 +146,7 @@ qmd_status qmd_kv_read(const qmd_kv_cache *cache, const qmd_kv_batch *batch, flo
         return QMD_ERR_SHAPE;
     if (!aligned(k_out, 16) || !aligned(v_out, 16))
         return QMD_ERR_MISALIGNED;
-    if (k_out && v_out && overlaps(k_out, extent(T, k_stride, kw), v_out, extent(T, v_stride, kw)))
+    if (rows_overlap({k_out, k_stride, kw}, {v_out, v_stride, kw}, T))
         return QMD_ERR_VALUE;
     DeviceInfo dev;
     if ((st = current_device(&dev)) != QMD_OK)
@@ -151,7 +174,7 @@ qmd_status qmd_kv_attention(const qmd_kv_cache *cache, const qmd_kv_batch *batch
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16))
         return QMD_ERR_MISALIGNED;
     if (!std::isfinite(scale) || window < 0 ||
-        overlaps(out, extent(batch->rows, out_stride, qw), q, extent(batch->rows, q_stride, qw)))
+        rows_overlap({out, out_stride, qw}, {q, q_stride, qw}, batch->rows))
         return QMD_ERR_VALUE;
     DeviceInfo dev;
     if ((st = current_device(&dev)) != QMD_OK)
