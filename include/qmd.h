@@ -383,8 +383,8 @@ typedef enum qmd_rope_pairs { QMD_ROPE_HALVES = 0, QMD_ROPE_ADJACENT = 1 } qmd_r
  *
  *   k, v    f32 rows of kv_heads * head_dim values, row r at k + r * k_stride
  *   q       f32 rows of q_heads * head_dim values, rotated into q_out; or NULL (then q_out NULL
- *           and q_heads 0).  q_out may be q itself with the same stride; no other overlap.
- *           Row tensors may be parts of one wider buffer (equal strides, apart in a row).
+ *           and q_heads 0).  q_out may be q itself with the same stride; its rows overlap no other
+ *           input.  Row tensors may be parts of one wider buffer (equal strides, apart in a row).
  *   rope    f32 [rope_rows][rot]: rot / 2 cosines, then rot / 2 sines, of position p; or NULL
  *           (then rot 0): nothing is rotated and q is copied.  A position at or past rope_rows is
  *           an index error: that row is not stored.

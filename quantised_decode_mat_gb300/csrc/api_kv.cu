@@ -117,10 +117,12 @@ qmd_status qmd_kv_append(const qmd_kv_cache *cache, const qmd_kv_batch *batch, c
         return QMD_ERR_VALUE;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16) || !aligned(rope, 16))
         return QMD_ERR_MISALIGNED;
-    if (q && !(q_out == q && q_out_stride == q_stride)) {
+    if (q) {  // q_out may be q itself; in place or not, it is written while k, v and the table are read
         const Rows out = {q_out, q_out_stride, qw};
-        if (rows_overlap(out, {q, q_stride, qw}, T) || rows_overlap(out, {k, k_stride, kw}, T) ||
-            rows_overlap(out, {v, v_stride, kw}, T))
+        const bool in_place = q_out == q && q_out_stride == q_stride;
+        if ((!in_place && rows_overlap(out, {q, q_stride, qw}, T)) || rows_overlap(out, {k, k_stride, kw}, T) ||
+            rows_overlap(out, {v, v_stride, kw}, T) ||
+            (rope && overlaps(q_out, extent(T, q_out_stride, qw), rope, extent(rope_rows, rot, rot))))
             return QMD_ERR_VALUE;
     }
     DeviceInfo dev;

@@ -1,5 +1,6 @@
-"""Which row buffers overlap: parts of one wider buffer do not, whatever their extents (no GPU needed:
-refused before the device is touched, and what is accepted ends at the device check)."""
+"""Which row buffers overlap: parts of one wider buffer do not, whatever their extents; q_out in place of
+q is still checked against k, v and the table (no GPU needed: refused before the device is touched, and
+what is accepted ends at the device check)."""
 import pytest
 
 import quantised_decode_mat_gb300 as q
@@ -62,6 +63,21 @@ def test_rows_that_meet_are_refused(L):
     assert read(L, at(0), at(KW + 4), 512, 512) == VALUE              # runs into the next row's keys
     assert attention(L, at(0), at(QW + 4)) == VALUE and attention(L, at(0), at(QW - 4)) == VALUE
     assert attention(L, at(0), at(0)) == VALUE
+
+
+def test_in_place_queries_that_run_into_keys_or_values(L):
+    assert append(L, at(508), FAR, at(0), at(0)) == VALUE
+    assert append(L, FAR, at(0), at(0), at(0)) == VALUE
+    assert append(L, at(512), at(896), at(0), at(0)) == VALUE         # values run into the next row's queries
+    assert append(L, at(0), at(0), at(0), at(0), rows=1) == VALUE
+    assert append(L, at(512), at(1024 - 256), at(0), at(0), rows=1) == 9
+
+
+def test_rotated_queries_over_the_table(L):
+    assert append(L, FAR, 2 * FAR, at(0), at(0), rope=at(1024 * 4 + 508)) == VALUE
+    assert append(L, FAR, 2 * FAR, at(0), at(0), rope=at(1024 * 4 + 512)) == 9
+    assert append(L, FAR, 2 * FAR, at(12800), at(12800), rope=at(0)) == 9
+    assert append(L, FAR, 2 * FAR, at(12796), at(12796), rope=at(0)) == VALUE
 
 
 def test_every_offset_and_stride_against_the_bytes(L):
