@@ -369,12 +369,14 @@ typedef enum qmd_rope_pairs { QMD_ROPE_HALVES = 0, QMD_ROPE_ADJACENT = 1 } qmd_r
  * first `rot` are left as they are.
  * Quantisation, per block of 16 positions and head, each f32 operation rounded on its own:
  *   d_row  = amax / 127, amax = max |x| over a row's head; 0 where amax < 1e-30
- *   d      = the largest d_row of the call's rows in the block -- and the block's scale, if the
- *            block also holds earlier positions of the sequence
- *   code   = clamp(round_to_nearest_even(x * (1 / d)), -127, 127), 0 where d = 0
- *   and if d grew past the scale d0 that the block had, its earlier codes become
+ *   d      = the largest d_row of the call's rows in the block -- and |d0|, d0 the block's scale, if
+ *            the block also holds earlier positions of the sequence
+ *   code   = clamp(round_to_nearest_even(x * (1 / d)), -127, 127), 0 where d = 0 (1 / d at most the
+ *            largest f32)
+ *   and if d differs from d0 (it grew, or d0 was negative), the earlier codes become
  *   clamp(round_to_nearest_even((code * d0) * (1 / d)), -127, 127).
- * A block's scale thus never shrinks while positions are added, and a position's error is at most
+ * A block's scale thus never shrinks while positions are added (one that the caller wrote may be
+ * anything finite: its sign moves into the codes), and a position's error is at most
  * half a step of the final scale for each time that it grew (the first rounding included).  Rows
  * may overwrite positions that were used before (after a draft was rejected, or in a recycled
  * page): whatever the block held at or after the first of them is forgotten.  Codes at positions

@@ -5,7 +5,8 @@
 //
 // Mathematics: per pair (a, b) of a head at position p, a' = a c - b s and b' = b c + a s with the
 // table's c, s of p; per block of 16 positions and head, d = max |x| / 127 over the block's new
-// rows (and the scale that its earlier positions have), code = rne(x / d) taken as x * (1 / d).
+// rows (and the size of the scale that its earlier positions have), code = rne(x / d) taken as
+// x * (1 / d) and held in -127 .. 127.
 // Codes are decided by rounding, so every f32 operation is rounded on its own (explicit _rn
 // intrinsics): the same inputs give the same codes as any other program that does these steps.
 //
@@ -158,10 +159,10 @@ __device__ __forceinline__ int partner(const RopeArgs &r, int l)
     return l < off ? l + off : l < 2 * off ? l - off : l;
 }
 
-// The codes of E values: x * inv rounded to the nearest even integer by adding 1.5 * 2^23 (unit 1),
-// which leaves it in the low byte.  |x * inv| <= 127 (1 + 2^-22), as inv is 1 over a scale of at least
-// max |x| / 127, so nothing needs a clamp but a code of -128 that is stored again (EARLIER).
-template <bool EARLIER, int E>
+// The codes of E values: x * inv held in -127 .. 127 and rounded to the nearest even integer by adding
+// 1.5 * 2^23 (unit 1), which leaves it in the low byte.  Both bounds are needed: a block's scale may be one
+// that the caller wrote, with codes of -128, or so small that a new value is thousands of its steps.
+template <int E>
 __device__ __forceinline__ void store_codes(int8_t *p, const float (&x)[E], float inv)
 {
 #pragma unroll
@@ -169,10 +170,7 @@ __device__ __forceinline__ void store_codes(int8_t *p, const float (&x)[E], floa
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-        {
-            const float q = __fmul_rn(x[i + e], inv);
-            w[e] = __float_as_uint(__fadd_rn(EARLIER ? fmaxf(q, -127.0f) : q, 12582912.0f));
-        }
+            w[e] = __float_as_uint(__fadd_rn(fminf(fmaxf(__fmul_rn(x[i + e], inv), -127.0f), 127.0f), 12582912.0f));
         *reinterpret_cast<uint32_t *>(p + i) =
             __byte_perm(__byte_perm(w[0], w[1], 0x5140u), __byte_perm(w[2], w[3], 0x5140u), 0x5410u);
     }
@@ -297,11 +295,13 @@ __global__ void __launch_bounds__(APP_WARPS * 32, D == 256 ? 3 : 4) kv_append_ke
 #pragma unroll
         for (int o = H::LPH / 2; o > 0; o >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float d = fmaxf(d0, top < 1e-30f ? 0.0f : __fdiv_rn(top, 127.0f));
-        const float inv = d > 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+        // the scale's size counts, so that earlier values are kept whatever its sign; under 2^-128 its
+        // reciprocal is held at the largest f32
+        const float d = fmaxf(fabsf(d0), top < 1e-30f ? 0.0f : __fdiv_rn(top, 127.0f));
+        const float inv = d > 0.0f ? fminf(__fdiv_rn(1.0f, d), 3.402823466e38f) : 0.0f;
         if (ok) {
-            if (d > d0) {
-                // the block's earlier tokens in steps of the larger scale
+            if (d != d0) {
+                // the block's earlier tokens in steps of the new scale
 #pragma unroll 2
                 for (int j = 0; j < tok0; ++j) {
                     float y[E];
@@ -309,14 +309,14 @@ __global__ void __launch_bounds__(APP_WARPS * 32, D == 256 ? 3 : 4) kv_append_ke
 #pragma unroll
                     for (int e = 0; e < E; ++e)
                         y[e] = __fmul_rn(y[e], d0);
-                    store_codes<true>(codes + j * D, y, inv);
+                    store_codes(codes + j * D, y, inv);
                 }
             }
 #pragma unroll 4
             for (int j = 0; j < m; ++j) {
                 float x[E];
                 load_f32(x, keep + j * ROW);
-                store_codes<false>(codes + (tok0 + j) * D, x, inv);
+                store_codes(codes + (tok0 + j) * D, x, inv);
             }
         }
         __syncwarp();  // every lane has read the old scale
