@@ -29,10 +29,13 @@
 // outputs.  A code c becomes an f16 by bytes: c + 128 under the exponent byte 0x64 is 1024 + c + 128,
 // less 1152.
 //
-// The running maximum moves only when a score passes it by more than 2^8 (then every sum is
-// rescaled); until then weights are at most 2^8, which costs f32 nothing.  A value block's scale
-// enters the weights relative to a running power of two at or above every scale so far, so the f16
-// parts neither overflow nor lose bits that the sum keeps.
+// Each query row has two references.  The sum of weights is kept over 2^m, m a running maximum of the
+// scores s (log2 units, rounded up to an integer).  The sums of values are kept over 2^(m + e): with d < 2^k
+// a block's scale, 2^(m + e) is at or above the largest 2^(s + k) met so far.  What f16 holds is thus small
+// only against what the row has already summed: a large scale without weight takes no bits from a small
+// one that has it (one reference for all scales lost 1.5e-2 of the result at scales 2^24 apart).  The
+// references move only when a weight passes one of them by more than 2^8 (then every sum is rescaled);
+// until then weights are at most 2^8, which f32 and the f16 parts have room for.
 //
 // Loads: a lane asks for each block's keys and values by tiled tensor copies (TMA) into a ring of
 // STAGES blocks per warp in shared memory, 4 KB a block (head_dim 128), an mbarrier to a stage.  The
@@ -119,7 +122,12 @@ struct AttnCfg {
 
 constexpr int ATT_MAX_ROWS_FLOATS = 16 * 128;  // the largest R x D of an instance (8 x 256 is the same)
 constexpr float ATT_NONE = -3.0e38f;           // the maximum before any score
-constexpr float ATT_SLACK = 8.0f;              // how far (log2) a score may pass the running maximum
+constexpr float ATT_SLACK = 8.0f;              // how far (log2) a weight may pass its reference
+// e before any value, and the least: an output under 2^-113 may have fewer bits
+constexpr float ATT_LOW = -120.0f;
+// How far a block's k may pass e: what e^x loses under 2^-126 is 2^-46 of the reference then.  Scales up to
+// twice as far apart lower m.
+constexpr float ATT_APART = 80.0f;
 
 // tma_load_3d with the default L2 policy: the cache is read again in the next step.
 __device__ __forceinline__ void load_tile(uint32_t dst, const void *tmap, int x, int block, uint32_t bar)
@@ -136,6 +144,13 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// 2^n for an integer n, exactly: 0 under 2^-126, infinity from 2^128 on.  (n's lowest byte comes to stand in
+// the low bits of 1.5 * 2^23 + 127 + n.)
+__device__ __forceinline__ float pow2(float n)
+{
+    return __uint_as_float(__float_as_uint(fminf(fmaxf(n, -127.0f), 128.0f) + 12583039.0f) << 23);
 }
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -185,6 +200,13 @@ __device__ __forceinline__ void split_pairs(float x, float y, uint32_t &hi, uint
 }
 
 constexpr float LOW_PART = 1.0f / 2048.0f;
+
+// The least k (at most 127) with |d| < 2^k, for a value scale d down to 2^-126; 256 where d is not finite.
+__device__ __forceinline__ float scale_log2(float d)
+{
+    const int ex = (int)(__float_as_uint(d) >> 23 & 255u);
+    return ex == 255 ? 256.0f : (float)min(ex - 126, 127);
+}
 
 struct Group {  // the rows of a row group and what they see
     int lo, hi;  // blocks [lo, hi) that any of them sees
@@ -454,7 +476,10 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             put = put + 1 == S ? 0 : put + 1;
         }
         float ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
-        meta[lane] = make_int4(bi_n, __float_as_int(ks_n), __float_as_int(vs_n), 0);
+        auto put_meta = [&](int at) {
+            meta[at] = make_int4(bi_n, __float_as_int(ks_n), __float_as_int(vs_n), __float_as_int(scale_log2(vs_n)));
+        };
+        put_meta(lane);
         __syncwarp();
 
         // ---- the queries as two f16 parts ------------------------------------------------------
@@ -516,14 +541,13 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
         const int all_from = row_begin(a, row_end(sq, (cg * R + gr.rows - 1) / a.by_group));
 
         float o[OT][4];
-        float m[QR], l[QR];
-        // value scales are taken over vref; wide rows' weights times 2^6 besides, so that what f16 loses
-        // below its smallest value is 2^-31 of the largest weight
+        float m[QR], ve8[QR], vinv[QR], l[QR];  // the references: m, e + ATT_SLACK, 2^-e; the weights' sum
+        // wide rows' weights times 2^6 besides, so that what f16 loses below its smallest value is 2^-31 of
+        // the reference
         constexpr float LIFT = WIDE ? 64.0f : 1.0f;
-        float vref = 7.52316385e-37f, vinv = 1.32922800e36f * LIFT;  // 2^-120, 2^120
 #pragma unroll
         for (int i = 0; i < QR; ++i)
-            m[i] = ATT_NONE, l[i] = 0.0f;
+            m[i] = ATT_NONE, ve8[i] = ATT_LOW + ATT_SLACK, vinv[i] = 0.0f, l[i] = 0.0f;
 #pragma unroll
         for (int i = 0; i < OT; ++i)
             o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
@@ -591,7 +615,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
                     ks_n = bi_n >= 0 ? p.ks[bi_n] : 0.0f, vs_n = bi_n >= 0 ? p.vs[bi_n] : 0.0f;
                 } else if ((idx & 24) == 16) {
                     __syncwarp();
-                    meta[i & 63] = make_int4(bi_n, __float_as_int(ks_n), __float_as_int(vs_n), 0);
+                    put_meta(i & 63);
                     __syncwarp();
                 }
             }
@@ -605,7 +629,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             scores(c, ring + use * C::BLOCK_BYTES);
             const int4 md = meta[idx & 63];
             const int bi = md.x;
-            const float ks = __int_as_float(md.y), vs = __int_as_float(md.z);
+            const float ks = __int_as_float(md.y), vs = __int_as_float(md.z), vk = __int_as_float(md.w);
             const unsigned char *st = ring + use * C::BLOCK_BYTES;
 
             // The scores in log2 units.  sc[i][e] is of query row t at position pos + rho + 8 e; or of row
@@ -615,6 +639,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             const bool whole = pos >= all_from && pos + KV_BLOCK <= all_to && bi >= 0;
             float sc[QR][SN];
             bool up = false;
+            float vr[QR];  // the block's scale over 2^e
 #pragma unroll
             for (int i = 0; i < QR; ++i) {
                 const float f = qscale[i] * ks;
@@ -637,19 +662,14 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
                             sc[i][e] = -INFINITY;
                     }
                 }
+                vr[i] = vs * vinv[i];
+                const float room = ve8[i] - vk, most = m[i] + fminf(ATT_SLACK, room);
+                up |= room < ATT_SLACK - ATT_APART;
 #pragma unroll
                 for (int e = 0; e < SN; ++e)
-                    up |= sc[i][e] > m[i] + ATT_SLACK;
+                    up |= sc[i][e] > most;
             }
-            const float va = fabsf(vs);
-            if (__any_sync(0xffffffffu, up) || va > vref) {
-                float fv = 1.0f;
-                if (va > vref) {
-                    const float r = __uint_as_float((__float_as_uint(va) + 0x7fffffu) & 0x7f800000u);
-                    fv = vref / r;
-                    vref = r;
-                    vinv = LIFT / r;
-                }
+            if (__any_sync(0xffffffffu, up)) {
                 float fo[QR];
 #pragma unroll
                 for (int i = 0; i < QR; ++i) {
@@ -661,11 +681,18 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
 #pragma unroll
                     for (int x = WIDE ? 1 : 4; x < (WIDE ? 4 : 32); x <<= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-                    const float mn = top > m[i] ? top : m[i];
-                    const float f = ex2(m[i] - mn);
-                    m[i] = mn;
-                    l[i] *= f;
-                    fo[i] = f * fv;
+                    // integers, so that e moves by what m moves and 2^(m + e) stays where it is
+                    const float mn = top > m[i] ? ceilf(top) : m[i], ve = ve8[i] - ATT_SLACK;
+                    const float k = top > -INFINITY ? vk : ATT_LOW;  // (a row that does not see the block keeps its references)
+                    const float en = fmaxf(fmaxf(ve + (m[i] - mn), ceilf(top - mn + k)), fmaxf(ATT_LOW, k - 2.0f * ATT_APART));
+                    // a scale further above 2^e than e^x reaches: m that much lower, and e higher
+                    const float low = fmaxf(k - en - ATT_APART, 0.0f);
+                    l[i] *= pow2(m[i] - mn + low);
+                    fo[i] = pow2(m[i] - mn + (ve - en));
+                    m[i] = mn - low;
+                    ve8[i] = en + low + ATT_SLACK;
+                    vinv[i] = pow2(1.0f - (en + low)) * (0.5f * LIFT);
+                    vr[i] = vs * vinv[i];
                 }
 #pragma unroll
                 for (int i = 0; i < OT; ++i)
@@ -673,7 +700,6 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
                     for (int e = 0; e < 4; ++e)
                         o[i][e] *= fo[R == 16 ? e >> 1 : 0];
             }
-            const float vr = vs * vinv;
             // the weights, as the second product's operand: columns, or rows
             uint32_t pb[WIDE ? R / 8 : 1][4];
 #pragma unroll
@@ -683,7 +709,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
                 for (int e = 0; e < SN; ++e) {
                     w[e] = ex2(sc[i][e] - m[i]);
                     l[i] += w[e];
-                    w[e] *= vr;
+                    w[e] *= vr[i];
                 }
                 if constexpr (!WIDE) {
                     uint32_t a0, a1;
@@ -778,7 +804,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             for (int x = WIDE ? 1 : 4; x < (WIDE ? 4 : 32); x <<= 1)
                 l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
             const int r = WIDE ? g + 8 * i : t;
-            const float f = (done ? (l[i] == 0.0f ? 0.0f : vref / l[i]) : vref) * (1.0f / LIFT);
+            const float f = (done ? (l[i] == 0.0f ? 0.0f : 1.0f / l[i]) : 1.0f) * (1.0f / LIFT), fe = pow2(ve8[i] - ATT_SLACK);
             if (!done && (WIDE ? t : g) == 0)
                 s_ml[(warp * 2 + part) * R + r] = make_float2(m[i], l[i]);
             if (done && r >= gr.rows)
@@ -797,7 +823,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
                     for (int e = 0; e < 4; ++e)
                         y[e] = (!WIDE ? fmaf(o[(d + e) / 2 % OT][((d + e) & 1) * 2 + 1], LOW_PART, o[(d + e) / 2 % OT][((d + e) & 1) * 2])
                                 : R == 8 ? o[(d + e) % OT][n] + o[(d + e) % OT][2 + n]
-                                         : o[(d + e) % OT][2 * i + n]) * f;
+                                         : o[(d + e) % OT][2 * i + n]) * f * fe;
                     *reinterpret_cast<float4 *>(to + d / RUN * 128 + piece * RUN + d % RUN) = make_float4(y[0], y[1], y[2], y[3]);
                 }
             }
