@@ -424,7 +424,7 @@ qmd_status qmd_kv_read(const qmd_kv_cache *cache, const qmd_kv_batch *batch, flo
  * with m the largest s_j.  A row that sees no position (a sequence with fewer tokens than rows)
  * gets zeros.  f32 throughout to about 1e-6: the 8-bit codes enter the tensor cores exactly, the
  * query and the weights as two f16 parts each (22 bits), sums are f32.  NaN or infinite queries
- * affect their own row and head only.
+ * affect their own row and head only, a scale that is not finite only rows that see its block.
  *
  *   q         f32 rows of q_heads * head_dim values (rotated already), row r at q + r * q_stride
  *   out       f32 rows likewise; must not overlap q's rows (parts of one wider buffer do not)

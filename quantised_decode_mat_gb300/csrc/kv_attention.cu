@@ -692,7 +692,8 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
                     m[i] = mn - low;
                     ve8[i] = en + low + ATT_SLACK;
                     vinv[i] = pow2(1.0f - (en + low)) * (0.5f * LIFT);
-                    vr[i] = vs * vinv[i];
+                    // 0 for a row that does not see the block, whose scale may not be finite
+                    vr[i] = k == vk ? vs * vinv[i] : 0.0f;
                 }
 #pragma unroll
                 for (int i = 0; i < OT; ++i)

@@ -1,4 +1,5 @@
-"""How exact attention is where value blocks' scales and weights lie far apart.  Errors are measured
+"""How exact attention is where it is hard: value blocks whose scales and weights lie far apart, scales
+that are not finite in blocks that some rows of a group do not see, long sequences.  Errors are measured
 against the weighted mean of |V| (what the sum itself keeps), not against the largest value around."""
 import numpy as np
 import pytest
@@ -127,3 +128,22 @@ def test_scales_that_rise_and_fall(ws, heads, kv, rows, dim):
     s.place()
     x = (sign.repeat(heads // kv, 0) * s.rng.uniform(0.9, 1.1, (s.T, heads, dim))).astype(np.float32)
     close(s, x, ws, 30 * np.log(2) / (100 / 64 * dim), copies=300)
+
+
+@pytest.mark.parametrize("heads", [2, 4, 8])  # of 2 key/value heads and 4 rows: 4, 8 and 16 rows to one
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+@pytest.mark.parametrize("which", ["ks", "vs"])
+def test_scales_that_are_not_finite_stay_with_the_rows_that_see_them(ws, heads, dim, bad, which):
+    # sequence 0: the last row alone sees block 4; sequence 1, window 20: rows see 14 + i .. 33 + i, so
+    # the first two alone see block 0
+    s = Scene([65, 37], [4, 4], heads, 2, dim, 16, seed=dim + heads)
+    x = s.queries()
+    ref, bound, _ = attend(s, x, 0.1, 20)
+    getattr(s.c, which)[s.table[0, 4]] = bad
+    getattr(s.c, which)[s.table[1, 0]] = bad
+    s.place()
+    got = q.kv_attention(s.cache, s.batch, dev(x), 0.1, ws, window=20).view(x.shape).cpu().numpy()
+    q.get_device_error()
+    clear = [0, 1, 2, 6, 7]
+    assert (np.abs(got - ref) <= bound)[clear].all()
