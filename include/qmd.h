@@ -422,8 +422,11 @@ qmd_status qmd_kv_read(const qmd_kv_cache *cache, const qmd_kv_batch *batch, flo
  * j > p - window:
  *     s_j = scale * sum_d q[r][h][d] * K[j][g][d],   out[r][h] = sum_j e^(s_j - m) V[j][g] / sum_j e^(s_j - m)
  * with m the largest s_j.  A row that sees no position (a sequence with fewer tokens than rows)
- * gets zeros.  f32 throughout to about 1e-6: the 8-bit codes enter the tensor cores exactly, the
- * query and the weights as two f16 parts each (22 bits), sums are f32.  NaN or infinite queries
+ * gets zeros.  The 8-bit codes enter the tensor cores exactly, the query and the weights as two f16
+ * parts each (22 bits, counted from a row's largest |q|, and from its largest weight times block scale),
+ * sums are f32.  An output's error is at most 2^-20 (1e-6, root mean square) of sum e^(s_j - m) |V[j]| /
+ * sum e^(s_j - m) while |scale| * sum_d |q| |K| is up to 32, whatever the lengths; above that it grows
+ * with that sum.  Value scales of a sequence may lie 2^160 apart.  NaN or infinite queries
  * affect their own row and head only, a scale that is not finite only rows that see its block.
  *
  *   q         f32 rows of q_heads * head_dim values (rotated already), row r at q + r * q_stride

@@ -147,3 +147,15 @@ def test_scales_that_are_not_finite_stay_with_the_rows_that_see_them(ws, heads, 
     q.get_device_error()
     clear = [0, 1, 2, 6, 7]
     assert (np.abs(got - ref) <= bound)[clear].all()
+
+
+@pytest.mark.parametrize("heads,kv,rows,dim", [(4, 1, 1, 64), (8, 1, 1, 64), (8, 2, 4, 64), (32, 8, 1, 128), (16, 2, 1, 128),
+                                               (16, 2, 2, 128), (4, 2, 2, 256), (8, 1, 1, 256), (4, 2, 4, 256)])
+def test_long_sequences_to_f32(ws, heads, kv, rows, dim):
+    """20011 tokens.  No chain of sums is longer than a warp's range and its joins: at most 13 blocks (with
+    132 SMs or more of 6 warps or more), 16 parts in a CTA and 152 in all, which round once (U), so the
+    bound counts 100 steps of 2 U.  The root mean square is what the header says, with sums |q| |K| of 15
+    to 28."""
+    s = Scene([20011], [rows], heads, kv, dim, 64, seed=dim + heads, uniform=True)
+    err, mean = close(s, s.queries(), ws, dim ** -0.5, chain=100)
+    assert np.sqrt(((err / mean) ** 2).mean()) <= 2.0 ** -20
