@@ -460,7 +460,8 @@ typedef enum qmd_half { QMD_F16 = 1, QMD_BF16 = 2 } qmd_half;
 /*
  * qmd_lora_add -- adds each vector's own low-rank adapter to a projection that all share:
  *     out[v] = base[v] + scale[a] * (B[a] (A[a] x[v])),   a = adapter[v];  out[v] = base[v] where a < 0
- * for v < batch, in f32 (A and B are widened exactly; x is not quantised).  base is the shared
+ * for v < batch, in f32 (A and B are widened exactly; x is not quantised; A x enters the product with B as
+ * 22 bits for f16, down to 2^-36 of its largest value, and as 24 for bf16).  base is the shared
  * projection's output (qmd_qmatvec's y) and out may be base itself.
  *   type     QMD_F16 or QMD_BF16: how A and B are held
  *   A        [adapters][rank][K], B [adapters][rows][rank], 16-byte aligned.  A smaller adapter in

@@ -219,23 +219,22 @@ __global__ void __launch_bounds__(LORA_WARPS * 32, 1) lora_add_kernel(const Lora
     __syncthreads();
 
     // ---- this CTA's rows of B --------------------------------------------------------------------
-    float s = a.scale[id];
+    const float s = a.scale[id];
     // Lane (g, t) holds column g of the products' second operand: the parts of ranks 8 (t + 4 i) + 0..7
     // of group i, zeros past the rank and in the columns without a part.
     constexpr bool F16 = sizeof(T) == 2 && __is_same(T, __half);
     constexpr int NI = (NR * LORA_WARPS + 31) / 32;  // groups of 32 ranks
     const int g = lane >> 2, q = lane & 3, pieces_b = a.rank / 8;
-    float up = 1.0f;  // f16: t is taken over a power of two, its largest value in [0.5, 1)
+    // f16: t is taken over a power of two, its largest value in [0.5, 1).  Sums go back by a product of their
+    // own: that power times the adapter's scale may leave f32 where the result does not.
+    float up = 1.0f, back = 1.0f;
     if constexpr (F16) {
-        float top = 0.0f;
+        unsigned top = 0;  // |t|'s order is that of its bits
         for (int i = lane; i < a.rank; i += 32)
-            top = fmaxf(top, fabsf(s_t[i]));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int ex = min(252, (int)(__float_as_uint(top) >> 23));
+            top = max(top, __float_as_uint(s_t[i]) & 0x7fffffffu);
+        const int ex = min(252, (int)(__reduce_max_sync(0xffffffffu, top) >> 23));
         up = __uint_as_float((uint32_t)(253 - ex) << 23);
-        s *= __uint_as_float((uint32_t)max(1, ex + 1) << 23);
+        back = __uint_as_float((uint32_t)max(1, ex + 1) << 23);
     }
     uint32_t tb[NI][4];
 #pragma unroll
@@ -281,8 +280,8 @@ __global__ void __launch_bounds__(LORA_WARPS * 32, 1) lora_add_kernel(const Lora
             }
             float ya, yb;
             if constexpr (F16) {
-                ya = fmaf(c[1], LORA_LOW, c[0]);
-                yb = fmaf(c[3], LORA_LOW, c[2]);
+                ya = fmaf(c[1], LORA_LOW, c[0]) * back;
+                yb = fmaf(c[3], LORA_LOW, c[2]) * back;
             } else {
                 ya = c[0] + (c[1] + __shfl_down_sync(0xffffffffu, c[0], 1));
                 yb = c[2] + (c[3] + __shfl_down_sync(0xffffffffu, c[2], 1));

@@ -1,0 +1,96 @@
+"""Adapters whose sums lie far from 1: finite results through large and small A x and scales, ranks far
+apart; one-hot A and x, so that A x is exact and what B does with it shows."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import quantised_decode_mat_gb300 as q  # noqa: E402
+
+pytestmark = [
+    pytest.mark.gpu,
+    pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA GPU"),
+]
+DEV = "cuda"
+U = 2.0 ** -24
+HALVES = [torch.float16, torch.bfloat16]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from quantised_decode_mat_gb300 import build as qbuild
+    qbuild.build()
+    q.lib()
+    q.get_device_error()
+    yield
+
+
+def run(t, B, base, s, dtype, K=512):
+    """t f64 [batch, rank] as A x exactly (A picks values of x), B [rows, rank], base [batch, rows]:
+    the result, its 64-bit value and a bound."""
+    batch, rank = t.shape
+    A = torch.zeros((1, rank, K))
+    A[0, torch.arange(rank), torch.arange(rank) * (K // rank)] = 1
+    x = torch.zeros((batch, K))
+    x[:, torch.arange(rank) * (K // rank)] = torch.from_numpy(t).float()
+    t = x[:, torch.arange(rank) * (K // rank)].double().numpy()
+    Bh, base = torch.from_numpy(B).to(dtype), torch.from_numpy(base).float()
+    Bv, basev = Bh.double().numpy(), base.double().numpy()
+    got = q.lora_add(x.to(DEV), base.to(DEV), A.to(dtype).to(DEV), Bh[None].contiguous().to(DEV),
+                     torch.zeros(batch, dtype=torch.int32, device=DEV), torch.tensor([s], device=DEV))
+    q.get_device_error()
+    add = np.float32(s).astype(np.float64) * (t @ Bv.T)
+    most = abs(s) * (np.abs(t) @ np.abs(Bv).T)
+    # t's parts: 2 U each value (two f16 parts: 4 U, and multiples of 2^-36 of twice the largest; the tensor
+    # cores align products to the largest, a zero of B counting as 2^-14 of its value of t: 2^-38 a rank);
+    # rank + 8 steps of sums at 2 U (they may truncate); scale and base: 4 roundings of the result
+    floor = abs(s) * np.abs(t).max(1, keepdims=True) * (2.0 ** -35 * np.abs(Bv).sum(1) + rank * 2.0 ** -38)
+    if dtype is torch.bfloat16:
+        floor = abs(s) * np.abs(t).max(1, keepdims=True) * rank * 2.0 ** -126 * np.ones(len(Bv))
+    return got.double().cpu().numpy(), basev + add, (rank + 12) * 2 * U * most + 4 * U * np.abs(basev + add) + floor + 1e-44
+
+
+def check(*a, **k):
+    got, ref, bound = run(*a, **k)
+    err = np.abs(got - ref)
+    assert np.isfinite(ref.astype(np.float32)).all()
+    assert (err <= bound).all(), f"{np.nanmax(err / bound)} times the bound, {np.isnan(got).sum()} NaN"
+    return got
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("rank", [8, 24, 64, 128])
+@pytest.mark.parametrize("ex,s,small", [(120, 1000.0, 2.0 ** -10), (126, 30000.0, 2.0 ** -14), (110, 2.0 ** 30, 2.0 ** -14),
+                                        (-100, 2.0 ** 90, 1.0), (100, 2.0 ** -90, 1.0), (0, 1.0, 1.0)])
+def test_large_and_small_sums_with_finite_results(dtype, rank, ex, s, small):
+    rng = np.random.default_rng(rank + ex + 200)
+    t = rng.uniform(0.5, 1, (3, rank)) * rng.choice([-1, 1], (3, rank)) * 2.0 ** ex / rank
+    B = rng.uniform(0.5, 1, (70, rank)) * rng.choice([-1, 1], (70, rank)) * small
+    B[::7] = 0
+    got = check(t, B, np.zeros((3, 70)), s, dtype)
+    assert not got[:, ::7].any()
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("rank", [8, 40, 128])
+@pytest.mark.parametrize("ratio", [10, 20, 24])
+def test_ranks_far_apart(dtype, rank, ratio):
+    """The largest value of A x meets zeros of B: the others, 2^ratio smaller, are what counts."""
+    # (f16 has two parts, so its floor shows from 2^12 on; bf16's exponents reach as far as f32's)
+    rng = np.random.default_rng(rank)
+    t = rng.standard_normal((2, rank)) * 2.0 ** -ratio
+    B = rng.standard_normal((300, rank))
+    big = rank // 2
+    t[:, big], B[:, big] = 1.0, 0.0
+    check(t, B, np.zeros((2, 300)), 1.5, dtype)
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+def test_each_rank_and_row_alone(dtype):
+    """One-hot B: row r holds a 1 at rank r % rank, so an output is one value of A x and the base."""
+    rng = np.random.default_rng(1)
+    for rank in (8, 64, 120):
+        rows = 4099
+        B = np.zeros((rows, rank))
+        B[np.arange(rows), np.arange(rows) % rank] = 1
+        check(rng.standard_normal((5, rank)), B, rng.standard_normal((5, rows)), -2.0, dtype, K=1024)
