@@ -79,8 +79,9 @@ __device__ __forceinline__ float dot8(const uint4 &u, const float4 &a, const flo
     return fmaf(f.y, b.w, fmaf(f.x, b.z, acc));
 }
 
-// The parts of a value of t that columns 0, 1 (and 2) hold.
-constexpr float LORA_LOW = 1.0f / 2048.0f;
+// The parts of a value of t that columns 0, 1 (and 2) hold.  The second is 2^11 (bf16: 2^8) times larger than
+// it counts, the third 2^16: as large as the first, so that none runs out of exponents before it.
+constexpr float LORA_LOW = 1.0f / 2048.0f, LORA_LOW_BF16 = 1.0f / 256.0f;
 __device__ __forceinline__ uint32_t part_bits(float x, int col, __half)
 {
     const __half h = __float2half_rn(x), l = __float2half_rn((x - __half2float(h)) * 2048.0f);
@@ -89,8 +90,8 @@ __device__ __forceinline__ uint32_t part_bits(float x, int col, __half)
 __device__ __forceinline__ uint32_t part_bits(float x, int col, __nv_bfloat16)
 {
     const __nv_bfloat16 h = __float2bfloat16_rn(x);
-    const float r = x - __bfloat162float(h);
-    const __nv_bfloat16 m = __float2bfloat16_rn(r), l = __float2bfloat16_rn(r - __bfloat162float(m));
+    const float r = (x - __bfloat162float(h)) * 256.0f;
+    const __nv_bfloat16 m = __float2bfloat16_rn(r), l = __float2bfloat16_rn((r - __bfloat162float(m)) * 256.0f);
     return __bfloat16_as_ushort(col == 0 ? h : col == 1 ? m : col == 2 ? l : __nv_bfloat16(0.0f));
 }
 
@@ -283,8 +284,8 @@ __global__ void __launch_bounds__(LORA_WARPS * 32, 1) lora_add_kernel(const Lora
                 ya = fmaf(c[1], LORA_LOW, c[0]) * back;
                 yb = fmaf(c[3], LORA_LOW, c[2]) * back;
             } else {
-                ya = c[0] + (c[1] + __shfl_down_sync(0xffffffffu, c[0], 1));
-                yb = c[2] + (c[3] + __shfl_down_sync(0xffffffffu, c[2], 1));
+                ya = fmaf(fmaf(__shfl_down_sync(0xffffffffu, c[0], 1), LORA_LOW_BF16, c[1]), LORA_LOW_BF16, c[0]);
+                yb = fmaf(fmaf(__shfl_down_sync(0xffffffffu, c[2], 1), LORA_LOW_BF16, c[3]), LORA_LOW_BF16, c[2]);
             }
             if (q == 0 && r + g < n)
                 out[row + r + g] = fmaf(s, ya, bs[r + g]);

@@ -61,7 +61,7 @@ def check(*a, **k):
 @pytest.mark.parametrize("dtype", HALVES)
 @pytest.mark.parametrize("rank", [8, 24, 64, 128])
 @pytest.mark.parametrize("ex,s,small", [(120, 1000.0, 2.0 ** -10), (126, 30000.0, 2.0 ** -14), (110, 2.0 ** 30, 2.0 ** -14),
-                                        (-100, 2.0 ** 90, 1.0), (100, 2.0 ** -90, 1.0), (0, 1.0, 1.0)])
+                                        (-100, 2.0 ** 90, 1.0), (-120, 2.0 ** 120, 1.0), (100, 2.0 ** -90, 1.0), (0, 1.0, 1.0)])
 def test_large_and_small_sums_with_finite_results(dtype, rank, ex, s, small):
     rng = np.random.default_rng(rank + ex + 200)
     t = rng.uniform(0.5, 1, (3, rank)) * rng.choice([-1, 1], (3, rank)) * 2.0 ** ex / rank
