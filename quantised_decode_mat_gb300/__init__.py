@@ -442,18 +442,25 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, rope=None, q=None, q_out=Non
     return q_out
 
 
-def kv_read(cache: KVCache, batch: KVBatch, k_out=None, v_out=None, stream=None):
+def kv_read(cache: KVCache, batch: KVBatch, k_out=None, v_out=None, stream=None, keys: bool = True, values: bool = True):
     """qmd_kv_read: the rows' keys and values as the cache holds them, code * scale, f32
-    [rows, kv_heads, head_dim] each (new tensors by default)."""
+    [rows, kv_heads, head_dim] each (new tensors by default).  keys=False or values=False leaves one of
+    them out (None in its place)."""
     st = _kv_stream(cache, batch, stream)
     H, D, dev, T = cache.kv_heads, cache.head_dim, cache.index, batch.rows
-    if k_out is None:
-        k_out = _empty((T, H, D), cache.device, stream)
-    if v_out is None:
-        v_out = _empty((T, H, D), cache.device, stream)
-    _, ks = _rows_of(k_out, T, H, D, dev, "k_out")
-    _, vs = _rows_of(v_out, T, H, D, dev, "v_out")
-    st = lib().qmd_kv_read(cache.ptrs, batch.ptrs, k_out.data_ptr(), ks, v_out.data_ptr(), vs, st)
+    if not (keys and values):
+        _need(keys or values, 1, "neither keys nor values are wanted")
+        _need((keys or k_out is None) and (values or v_out is None), 10, "an output is given for what is left out")
+    ks = vs = 0
+    if keys:
+        if k_out is None:
+            k_out = _empty((T, H, D), cache.device, stream)
+        _, ks = _rows_of(k_out, T, H, D, dev, "k_out")
+    if values:
+        if v_out is None:
+            v_out = _empty((T, H, D), cache.device, stream)
+        _, vs = _rows_of(v_out, T, H, D, dev, "v_out")
+    st = lib().qmd_kv_read(cache.ptrs, batch.ptrs, _ptr(k_out), ks, _ptr(v_out), vs, st)
     if st:
         _check(st)
     return k_out, v_out

@@ -1,5 +1,5 @@
 """Row tensors that are parts of one wider buffer give what separate tensors give, and what lies between
-and behind them stays as it was."""
+and behind them stays as it was; keys or values read alone."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -69,3 +69,20 @@ def test_queries_rotated_into_the_buffer_of_keys_and_values():
         q.get_device_error()
         results.append([o.clone(), qkv[:, 1024:].clone(), s.cache.k, s.cache.v])
     assert all(torch.equal(a, b) for a, b in zip(*results)) and (results[0][0][-1] == 5).all()
+
+
+def test_keys_or_values_read_alone():
+    s = scene(4)
+    k, v = q.kv_read(s.cache, s.batch)
+    own = s.T - 1  # the last row is no sequence's
+    a, none = q.kv_read(s.cache, s.batch, values=False)
+    assert none is None and torch.equal(a[:own], k[:own])
+    none, b = q.kv_read(s.cache, s.batch, keys=False)
+    assert none is None and torch.equal(b[:own], v[:own])
+    out = torch.full_like(v, 5.0)
+    assert q.kv_read(s.cache, s.batch, v_out=out, keys=False)[1] is out
+    q.get_device_error()
+    assert torch.equal(out[:own], v[:own]) and (out[own] == 5).all()
+    for bad in (dict(keys=False, values=False), dict(keys=False, k_out=out), dict(values=False, v_out=out)):
+        with pytest.raises(q.QmdError):
+            q.kv_read(s.cache, s.batch, **bad)
