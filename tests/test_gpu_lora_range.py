@@ -94,3 +94,24 @@ def test_each_rank_and_row_alone(dtype):
         B = np.zeros((rows, rank))
         B[np.arange(rows), np.arange(rows) % rank] = 1
         check(rng.standard_normal((5, rank)), B, rng.standard_normal((5, rows)), -2.0, dtype, K=1024)
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("batch,rank,K,rows", [(1, 8, 65536, 300), (8, 24, 14336, 1001), (5, 128, 2304, 4100), (8, 64, 256, 29)])
+def test_whole_numbers_are_exact(dtype, batch, rank, K, rows):
+    """x, A, B and base of small whole numbers: A x is below 2^17 and the outputs below 2^24, so every product,
+    part and sum is a whole number that f32 holds, in whatever order; a lost or doubled term is off by 1."""
+    g = torch.Generator().manual_seed(K + rank)
+    whole = lambda lo, hi, *shape: torch.randint(lo, hi, shape, generator=g)  # noqa: E731
+    x, A = whole(-1, 2, batch, K), whole(-1, 2, 3, rank, K)
+    B, base = torch.zeros((3, rows, rank), dtype=torch.int64), whole(-99, 100, batch, rows)
+    for a in range(3):  # up to 8 ranks to a row
+        B[a].scatter_(1, whole(0, rank, rows, 8), whole(-8, 9, rows, 8))
+    idx = whole(0, 3, batch).int()
+    want = torch.stack([base[v] + 2 * (B[i] @ (A[i] @ x[v])) for v, i in enumerate(idx.tolist())])
+    assert want.abs().max() < 1 << 24
+    d = lambda t, ty: t.to(ty).to(DEV)  # noqa: E731
+    got = q.lora_add(d(x, torch.float32), d(base, torch.float32), d(A, dtype), d(B, dtype), idx.to(DEV),
+                     torch.full((3,), 2.0, device=DEV))
+    q.get_device_error()
+    assert torch.equal(got.cpu().long(), want)
