@@ -408,7 +408,7 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, inv_freq=None, d
     import torch
     if inv_freq is None:
         inv_freq = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
-    inv_freq = torch.as_tensor(inv_freq, dtype=torch.float64)
+    inv_freq = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").detach()
     _need(inv_freq.shape == (rot // 2,), 6, f"inv_freq: {rot // 2} values are wanted")
     angle = torch.arange(positions, dtype=torch.float64)[:, None] * inv_freq
     return torch.cat((angle.cos(), angle.sin()), 1).float().to(device)
