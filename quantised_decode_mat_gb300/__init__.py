@@ -393,6 +393,8 @@ class KVBatch:
             _need(rows is not None, 6, "rows: the rows of the call's tensors are wanted with q_start")
         self.page_table, self.kv_len, self.q_start = page_table, kv_len, q_start
         self.max_q, self.rows = max_q, seqs * max_q if rows is None else rows
+        # (ctypes would take them modulo 2^32 and 2^64; the library checks what fits)
+        _need(abs(max_q) < 1 << 31 and abs(self.rows) < 1 << 63, 6, f"max_q {max_q}, rows {self.rows}")
         self.ptrs = KVBatchPtrs(_ptr(page_table), _ptr(kv_len), _ptr(q_start), page_table.shape[1], self.rows, seqs, max_q)
 
 
@@ -424,6 +426,7 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, rope=None, q=None, q_out=Non
     D, dev, T = cache.head_dim, cache.index, batch.rows
     _, ks = _rows_of(k, T, cache.kv_heads, D, dev, "k")
     _, vs = _rows_of(v, T, cache.kv_heads, D, dev, "v")
+    _need(pairs == ROPE_HALVES or pairs == ROPE_ADJACENT, 10, "pairs: ROPE_HALVES or ROPE_ADJACENT")
     heads = qs = os_ = 0
     if q is not None:
         heads, qs = _rows_of(q, T, None, D, dev, "q")
@@ -485,6 +488,8 @@ def kv_attention(cache: KVCache, batch: KVBatch, q, scale: float, workspace, win
     st = _kv_stream(cache, batch, stream)
     D, dev, T = cache.head_dim, cache.index, batch.rows
     heads, qs = _rows_of(q, T, None, D, dev, "q")
+    if window >> 63:
+        raise QmdError(10, f"window: {window}")
     if out is None:
         out = _empty((T, heads * D), cache.device, stream)
     _, os_ = _rows_of(out, T, heads, D, dev, "out")
