@@ -394,8 +394,9 @@ typedef enum qmd_rope_pairs { QMD_ROPE_HALVES = 0, QMD_ROPE_ADJACENT = 1 } qmd_r
  * A sequence shorter than its rows is an index error (none of its rows is stored); one without
  * tokens (kv_len 0) pads the batch: its rows are neither read nor written, and nothing is reported.
  * Row pointers 16-byte aligned, strides (in f32 values) multiples of 4 and at least a row long.
- * A block that is appended to must belong to one sequence: the same block under two sequences of
- * one call, or of calls that overlap on the GPU, is a race.
+ * A block that is appended to must belong to one sequence, at one place of its table: the same block
+ * under two sequences of one call or at two places that its rows reach, or of calls that overlap on the
+ * GPU, is a race.
  * Errors: NULL, SHAPE, MISALIGNED, VALUE (pairs, overlap, q without q_out), DEVICE, LAUNCH.
  */
 qmd_status qmd_kv_append(const qmd_kv_cache *cache, const qmd_kv_batch *batch, const float *k, int64_t k_stride,
