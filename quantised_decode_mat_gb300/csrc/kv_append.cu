@@ -161,7 +161,8 @@ __device__ __forceinline__ int partner(const RopeArgs &r, int l)
 
 // The codes of E values: x * inv held in -127 .. 127 and rounded to the nearest even integer by adding
 // 1.5 * 2^23 (unit 1), which leaves it in the low byte.  Both bounds are needed: a block's scale may be one
-// that the caller wrote, with codes of -128, or so small that a new value is thousands of its steps.
+// that the caller wrote, with codes of -128, or so small that a new value is thousands of its steps.  (0.7 % of a
+// prompt's append; new rows held only under 1e-30, by a branch, cost 1.3 %.)
 template <int E>
 __device__ __forceinline__ void store_codes(int8_t *p, const float (&x)[E], float inv)
 {

@@ -43,10 +43,10 @@
 // read shared memory together meet eight different pieces: no bank conflicts.  Page numbers and
 // scales are looked up 32 blocks at a time, a lane each, a chunk ahead.
 //
-// Measured: 48 sequences of 2500-12301 tokens (32 heads over 8 of 128) 125 us, 6.24 TB/s, 0.93 of the
+// Measured: 48 sequences of 2500-12301 tokens (32 heads over 8 of 128) 123-125 us, 6.3 TB/s, 0.94 of the
 // copy rate; per-lane cp.async instead of tensor copies 166 us, with or without the arithmetic.  One
-// sequence of 32768 22.4 us, of 17 8.6 us: lookups that wait for each other, and the joins.  16 rows to a
-// head (16 x 8100 tokens, 4 rows each) 78 us against 40 for the bytes: 8 warps to an SM are few for it.
+// sequence of 32768 22.2 us, of 17 8.5 us: lookups that wait for each other, and the joins.  16 rows to a
+// head (16 x 8100 tokens, 4 rows each) 75.5 us against 40 for the bytes: 8 warps to an SM are few for it.
 #include <climits>
 #include <cstring>
 #include <mutex>
