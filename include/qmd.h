@@ -23,8 +23,8 @@
  *    launch refusals; "Kernel SPI and the selection algorithm", "Why a kernel declines").
  *  - Layouts are batch-major and row-major; K is the reduction length (columns of W), a
  *    multiple of 256; nb = K / 256.
- *  - Launch order: qmd_q8k_pack, qmd_rmsnorm_q8k_pack, qmd_qmatvec, the qmd_kv_* calls and
- *    qmd_lora_add are launched as programmatic dependents of the preceding kernel in the
+ *  - Launch order: qmd_q8k_pack, qmd_rmsnorm_q8k_pack, qmd_qmatvec, the qmd_kv_* and qmd_kv4_* calls
+ *    and qmd_lora_add are launched as programmatic dependents of the preceding kernel in the
  *    stream.  Before waiting for that kernel to finish they read only weight buffers (W, W_aux;
  *    the norm gain g; an adapter's A, B and scale); everything else is read and written after it has finished.  Weights therefore must not be written
  *    by the kernel launched immediately before them in the same stream unless that kernel
@@ -50,6 +50,7 @@ extern "C" {
 #define QMD_WORKSPACE_BYTES 4096 /* scheduling workspace of qmd_qmatvec_ws / qmd_qmatvec_x_ws */
 #define QMD_KV_BLOCK 16          /* tokens of one head that share a scale in the key/value cache */
 #define QMD_KV_MAX_SEQS 2048     /* sequences per key/value call */
+#define QMD_KV4_GROUP 32         /* values of a head that share a scale in the 4-bit cache */
 #define QMD_LORA_MAX_RANK 128
 
 typedef enum qmd_status {
@@ -453,6 +454,111 @@ qmd_status qmd_kv_attention(const qmd_kv_cache *cache, const qmd_kv_batch *batch
 
 /* Bytes of qmd_kv_attention's workspace on the current device (0 if there is none). */
 size_t qmd_kv_workspace_bytes(void);
+
+/* ---- the same cache in 4 bits, and its eviction --------------------------------------------
+ *
+ * For requests whose keys and values take more memory, or more of a step's time, than they are worth: the
+ * cache holds 4.5 bits a value, and positions that attention hardly looks at can be taken out
+ * ("Language models on the device: the cajeta-llm kernels", §2.5: the cache that attention reads; the pages
+ * have no counterpart of the 4-bit form or of eviction).
+ *
+ * qmd_kv4_cache: pages of `page_tokens` tokens.  A cached value is d * (c - 8), with a 4-bit code c and one
+ * f16 scale d (of either sign) for each group of QMD_KV4_GROUP neighbouring values of a token's head.
+ *   k, v              [pages][kv_heads][page_tokens][head_dim / 2] bytes, dimension 2 i in the low four bits
+ *                     of byte i and 2 i + 1 in the high; 16-byte aligned
+ *   k_scale, v_scale  f16 [pages][kv_heads][page_tokens][head_dim / 32], 16-byte aligned
+ *   limits as qmd_kv_cache's.  The batch descriptor, its checks and its errors are qmd_kv_batch's; the slot that
+ *   page_table and kv_len speak of is called the position of a row where nothing was evicted.
+ */
+typedef struct qmd_kv4_cache {
+    uint8_t *k, *v;
+    uint16_t *k_scale, *v_scale;
+    int64_t pages;
+    int kv_heads, page_tokens, head_dim;
+} qmd_kv4_cache;
+
+/*
+ * qmd_kv4_append -- qmd_kv_append for the 4-bit cache: rotates the rows' keys (and queries), quantises keys
+ * and values and stores them at their slots.  Per group of 32 values, each f32 operation rounded on its own:
+ *   top  = the value of the largest size (of several the first)
+ *   d    = f16(top / -8), held in -65504 .. 65504
+ *   code = clamp(round_to_nearest_even(x * (1 / d)), -8, 7) + 8, 8 where d = 0
+ * A value is off by at most half a step |d|, but where it comes within half a step of -top, which has no code:
+ * there, and where d was held or is under 2^-14, by up to a step.  Rows do not touch what the cache
+ * holds of other tokens.
+ *   positions  int32 [rows], device: the position that row r is rotated by; or NULL: its slot.  (A request's
+ *              positions run ahead of its slots once something was evicted.)  Not read without rope.  One
+ *              outside [0, rope_rows) is an index error: that row is not stored, its query not written.
+ * Other arguments, limits and errors as qmd_kv_append; a slot belongs to one sequence, at one place of its
+ * table.  Non-finite inputs are outside the contract (no fault, their groups are unspecified).
+ * Errors: NULL, SHAPE, MISALIGNED, VALUE (pairs, overlap, q without q_out), DEVICE, LAUNCH.
+ */
+qmd_status qmd_kv4_append(const qmd_kv4_cache *cache, const qmd_kv_batch *batch, const float *k, int64_t k_stride,
+                          const float *v, int64_t v_stride, const float *q, int64_t q_stride, int q_heads,
+                          float *q_out, int64_t q_out_stride, const float *rope, int64_t rope_rows, int rot,
+                          qmd_rope_pairs pairs, const int32_t *positions, void *stream);
+
+/*
+ * qmd_kv4_read -- qmd_kv_read for the 4-bit cache: d * (c - 8) of every row's slot, exact in f32.
+ * Arguments, limits and errors as qmd_kv_read.
+ */
+qmd_status qmd_kv4_read(const qmd_kv4_cache *cache, const qmd_kv_batch *batch, float *k_out, int64_t k_stride,
+                        float *v_out, int64_t v_stride, void *stream);
+
+/*
+ * qmd_kv4_attention -- qmd_kv_attention over the 4-bit cache, and optionally each row's log-sum-exp:
+ *     lse[r][h] = m + ln sum_j e^(s_j - m)       (-infinity for a row that sees no position)
+ * Window and causal order count slots.
+ *   lse  f32 [rows][q_heads], 4-byte aligned, or NULL; must not overlap out or q
+ * Accuracy as qmd_kv_attention's, with one more limit: what a group of 32 values adds to an output is kept down
+ * to 2^-36 of the largest weight times scale among all the groups that the row has met.
+ * NaN or infinite queries affect their own row and head only, a scale that is not finite only rows that see
+ * its slot.  Other arguments (workspace among them, of qmd_kv_workspace_bytes()), limits and errors as
+ * qmd_kv_attention.
+ */
+qmd_status qmd_kv4_attention(const qmd_kv4_cache *cache, const qmd_kv_batch *batch, const float *q, int64_t q_stride,
+                             int q_heads, float scale, int64_t window, float *out, int64_t out_stride, float *lse,
+                             void *workspace, void *stream);
+
+/*
+ * qmd_kv4_weigh -- adds up how much attention each cached token got: for each slot j of a sequence and
+ * key/value head g,
+ *     weight[j][g] = (weight[j][g], or 0 where j is one of the call's own rows)
+ *                    + sum over the rows that see j and the query heads h of g of e^(s_j - lse[r][h])
+ * with s_j as qmd_kv4_attention's, of the same q, scale and window, whose lse it takes.  Called once after
+ * each attention call it keeps the sum of a token's weights since it was appended; called after a
+ * prompt's last rows only, over weights that are zero, it keeps what those rows looked at.  Weights of slots
+ * behind a sequence's last are left as they were.  The rows are added in one order: the same inputs on the
+ * same device give the same bits.
+ *   lse     f32 [rows][q_heads], 4-byte aligned
+ *   weight  f32 [pages][kv_heads][page_tokens], 16-byte aligned (read and written)
+ * Values are not read (cache->v and v_scale may be NULL).  A weight is off by at most 2^-20 of itself while
+ * |scale| * sum_d |q| |K| and |lse| are up to 32, and grows with them.  Rows that see no position (their lse is
+ * -infinity) add nothing.  A slot must belong to one sequence, at one place of its table (no shared pages).
+ * Other arguments, limits and errors as qmd_kv4_attention (there is no workspace).
+ */
+qmd_status qmd_kv4_weigh(const qmd_kv4_cache *cache, const qmd_kv_batch *batch, const float *q, int64_t q_stride,
+                         int q_heads, float scale, int64_t window, const float *lse, float *weight, void *stream);
+
+/*
+ * qmd_kv4_evict -- takes the tokens with the least weight out of every sequence that has more than `keep`.
+ * Each key/value head chooses for itself: the first `sinks` and the last `recent` slots stay, and of the
+ * others those with the largest weight, of equal weights the earlier, until `keep` are left.  They move, codes,
+ * scales and weights, to slots 0 .. keep - 1 in their order; what lies behind those is left as it was, and the
+ * pages behind them may be used otherwise.  (-0 counts as 0, a NaN as less than everything.)
+ *   batch     page_table, table_stride, kv_len and seqs; its rows and q_start are not read.  A slot must belong
+ *             to one sequence, at one place of its table (no shared pages).
+ *   weight    f32 [pages][kv_heads][page_tokens], 16-byte aligned (read, moved)
+ *   len_out   int32 [seqs], 4-byte aligned: min(kv_len, keep), the next call's kv_len (before its rows are
+ *             counted in).  Must not overlap kv_len.
+ *   kept      int32 [seqs][kv_heads][keep], 4-byte aligned, or NULL: the slots that the tokens came from, then -1
+ *   keep 1 .. 2^24, sinks and recent >= 0, together at most keep
+ * A length out of range gives len_out 0, a page out of range leaves the whole sequence as it was (len_out its
+ * length); kept is -1 for both, and both are index errors.
+ * Errors: NULL, SHAPE, MISALIGNED, VALUE (keep, sinks, recent, overlap), DEVICE, LAUNCH.
+ */
+qmd_status qmd_kv4_evict(const qmd_kv4_cache *cache, const qmd_kv_batch *batch, float *weight, int64_t keep,
+                         int64_t sinks, int64_t recent, int32_t *len_out, int32_t *kept, void *stream);
 
 /* ---- low-rank adapters beside a shared projection ------------------------------------------ */
 

@@ -1,5 +1,6 @@
 """Thin Python binding of libqmd (ctypes): decode-time Q4_K / Q6_K x q8_K mat-vec on GB300, and
-the operators of a decode step around it (the 8-bit key/value cache, low-rank adapters).
+the operators of a decode step around it (the 8-bit and the 4-bit key/value cache, eviction, low-rank
+adapters).
 
 Argument marshalling only.  Every step of the computation runs in the library's CUDA kernels;
 torch supplies device memory and streams.  The functions here carry the C ABI's names
@@ -22,6 +23,7 @@ Q4_K = 12
 Q5_K = 13
 Q6_K_SPLIT = 14
 QMD_KV_BLOCK = 16
+QMD_KV4_GROUP = 32
 ROPE_HALVES, ROPE_ADJACENT = 0, 1
 F16, BF16 = 1, 2
 
@@ -58,6 +60,10 @@ class KVCachePtrs(ctypes.Structure):
                 ("page_tokens", ctypes.c_int), ("head_dim", ctypes.c_int)]
 
 
+class KV4CachePtrs(ctypes.Structure):
+    _fields_ = KVCachePtrs._fields_
+
+
 class KVBatchPtrs(ctypes.Structure):
     _fields_ = [("page_table", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
                 ("table_stride", ctypes.c_int64), ("rows", ctypes.c_int64), ("seqs", ctypes.c_int),
@@ -84,6 +90,7 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         ip = ctypes.POINTER(ctypes.c_int)
         sizep = ctypes.POINTER(ctypes.c_size_t)
         cp, bp = ctypes.POINTER(KVCachePtrs), ctypes.POINTER(KVBatchPtrs)
+        c4 = ctypes.POINTER(KV4CachePtrs)
         sigs = {
             "qmd_q8k_pack": ([vp, Q8KPtrs, i64, i32, vp], i32),
             "qmd_rmsnorm_q8k_pack": ([vp, vp, vp, ctypes.c_float, vp, Q8KPtrs, i64, i32, vp], i32),
@@ -118,6 +125,11 @@ def lib(path: str | None = None) -> ctypes.CDLL:
             "qmd_kv_read": ([cp, bp, vp, i64, vp, i64, vp], i32),
             "qmd_kv_attention": ([cp, bp, vp, i64, i32, ctypes.c_float, i64, vp, i64, vp, vp], i32),
             "qmd_kv_workspace_bytes": ([], ctypes.c_size_t),
+            "qmd_kv4_append": ([c4, bp, vp, i64, vp, i64, vp, i64, i32, vp, i64, vp, i64, i32, i32, vp, vp], i32),
+            "qmd_kv4_read": ([c4, bp, vp, i64, vp, i64, vp], i32),
+            "qmd_kv4_attention": ([c4, bp, vp, i64, i32, ctypes.c_float, i64, vp, i64, vp, vp, vp], i32),
+            "qmd_kv4_weigh": ([c4, bp, vp, i64, i32, ctypes.c_float, i64, vp, vp, vp], i32),
+            "qmd_kv4_evict": ([c4, bp, vp, i64, i64, i64, vp, vp, vp], i32),
             "qmd_lora_add": ([i32, vp, vp, vp, vp, vp, vp, vp, i64, i64, i32, i32, i32, vp], i32),
         }
         if hasattr(L, "qmd_debug_trace"):  # the traced build (include/qmd_trace.h)
@@ -298,15 +310,16 @@ def _stream_on(stream, index: int, what: str) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _empty(shape, device, stream):
-    """A new f32 tensor for a call on `stream`: its memory belongs to that stream."""
+def _empty(shape, device, stream, dtype=None):
+    """A new f32 tensor (or of dtype) for a call on `stream`: its memory belongs to that stream."""
     import torch
+    dtype = dtype or torch.float32
     if stream is None:
-        return torch.empty(shape, dtype=torch.float32, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=torch.float32, device=device)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 # The checks below run on every call of a decode step's small operators: messages are made only for
@@ -416,13 +429,8 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, inv_freq=None, d
     return torch.cat((angle.cos(), angle.sin()), 1).float().to(device)
 
 
-def kv_append(cache: KVCache, batch: KVBatch, k, v, rope=None, q=None, q_out=None, pairs: int = ROPE_HALVES,
-              stream=None):
-    """qmd_kv_append: rotates the rows' keys and queries by the table's positions, quantises keys and
-    values into the cache and returns the rotated queries (q_out, by default a new tensor; None
-    without q).  k, v f32 [rows, kv_heads, head_dim], q f32 [rows, heads, head_dim], strided by rows
-    only (parts of one fused projection's output); q_out may be q."""
-    st = _kv_stream(cache, batch, stream)
+def _append_args(cache, batch: KVBatch, k, v, rope, q, q_out, pairs, stream):
+    """What qmd_kv_append and qmd_kv4_append take alike, and the rotated queries."""
     D, dev, T = cache.head_dim, cache.index, batch.rows
     _, ks = _rows_of(k, T, cache.kv_heads, D, dev, "k")
     _, vs = _rows_of(v, T, cache.kv_heads, D, dev, "v")
@@ -438,18 +446,26 @@ def kv_append(cache: KVCache, batch: KVBatch, k, v, rope=None, q=None, q_out=Non
         _need(rope.dim() == 2, 6, "rope: [positions, rot] is wanted")
         n, rot = rope.shape
         _array(rope, _F32, (n, rot), dev, "rope")
-    st = lib().qmd_kv_append(cache.ptrs, batch.ptrs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, heads,
-                             _ptr(q_out), os_, _ptr(rope), n, rot, pairs, st)
+    return (cache.ptrs, batch.ptrs, k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, heads, _ptr(q_out), os_, _ptr(rope), n,
+            rot, pairs), q_out
+
+
+def kv_append(cache: KVCache, batch: KVBatch, k, v, rope=None, q=None, q_out=None, pairs: int = ROPE_HALVES,
+              stream=None):
+    """qmd_kv_append: rotates the rows' keys and queries by the table's positions, quantises keys and
+    values into the cache and returns the rotated queries (q_out, by default a new tensor; None
+    without q).  k, v f32 [rows, kv_heads, head_dim], q f32 [rows, heads, head_dim], strided by rows
+    only (parts of one fused projection's output); q_out may be q."""
+    st = _kv_stream(cache, batch, stream)
+    args, q_out = _append_args(cache, batch, k, v, rope, q, q_out, pairs, stream)
+    st = lib().qmd_kv_append(*args, st)
     if st:
         _check(st)
     return q_out
 
 
-def kv_read(cache: KVCache, batch: KVBatch, k_out=None, v_out=None, stream=None, keys: bool = True, values: bool = True):
-    """qmd_kv_read: the rows' keys and values as the cache holds them, code * scale, f32
-    [rows, kv_heads, head_dim] each (new tensors by default).  keys=False or values=False leaves one of
-    them out (None in its place)."""
-    st = _kv_stream(cache, batch, stream)
+def _read_args(cache, batch: KVBatch, k_out, v_out, stream, keys, values):
+    """The outputs of qmd_kv_read and qmd_kv4_read, with their strides."""
     H, D, dev, T = cache.kv_heads, cache.head_dim, cache.index, batch.rows
     if not (keys and values):
         _need(keys or values, 1, "neither keys nor values are wanted")
@@ -463,6 +479,15 @@ def kv_read(cache: KVCache, batch: KVBatch, k_out=None, v_out=None, stream=None,
         if v_out is None:
             v_out = _empty((T, H, D), cache.device, stream)
         _, vs = _rows_of(v_out, T, H, D, dev, "v_out")
+    return k_out, ks, v_out, vs
+
+
+def kv_read(cache: KVCache, batch: KVBatch, k_out=None, v_out=None, stream=None, keys: bool = True, values: bool = True):
+    """qmd_kv_read: the rows' keys and values as the cache holds them, code * scale, f32
+    [rows, kv_heads, head_dim] each (new tensors by default).  keys=False or values=False leaves one of
+    them out (None in its place)."""
+    st = _kv_stream(cache, batch, stream)
+    k_out, ks, v_out, vs = _read_args(cache, batch, k_out, v_out, stream, keys, values)
     st = lib().qmd_kv_read(cache.ptrs, batch.ptrs, _ptr(k_out), ks, _ptr(v_out), vs, st)
     if st:
         _check(st)
@@ -501,6 +526,131 @@ def kv_attention(cache: KVCache, batch: KVBatch, q, scale: float, workspace, win
     if st:
         _check(st)
     return out
+
+
+class KV4Cache:
+    """A paged 4-bit key/value cache: codes uint8 [pages, kv_heads, page_tokens, head_dim / 2] of keys and of
+    values (dimension 2 i in the low four bits of byte i), and f16 scales [pages, kv_heads, page_tokens,
+    head_dim / 32].  A cached value is scale * (code - 8)."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        _torch_names()
+        _need(k.dim() == 4, 6, "k: [pages, kv_heads, page_tokens, head_dim / 2] is wanted")
+        pages, heads, tokens, half = k.shape
+        self.index = k.get_device()
+        for t, what in ((k, "k"), (v, "v")):
+            _array(t, torch.uint8, k.shape, self.index, what)
+        for t, what in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _array(t, torch.float16, (pages, heads, tokens, 2 * half // QMD_KV4_GROUP), self.index, what)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.kv_heads, self.head_dim, self.device = heads, 2 * half, k.device
+        self.page_tokens, self.pages = tokens, pages
+        self.ptrs = KV4CachePtrs(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), pages, heads, tokens, 2 * half)
+
+    @staticmethod
+    def empty(pages: int, kv_heads: int, page_tokens: int, head_dim: int, device="cuda") -> "KV4Cache":
+        import torch
+        codes = [torch.zeros((pages, kv_heads, page_tokens, head_dim // 2), dtype=torch.uint8, device=device) for _ in "kv"]
+        scales = [torch.zeros((pages, kv_heads, page_tokens, head_dim // QMD_KV4_GROUP), dtype=torch.float16, device=device)
+                  for _ in "kv"]
+        return KV4Cache(*codes, *scales)
+
+    def new_weights(self):
+        """f32 zeros [pages, kv_heads, page_tokens]: what kv4_weigh adds up and kv4_evict chooses by."""
+        import torch
+        return torch.zeros((self.pages, self.kv_heads, self.page_tokens), dtype=torch.float32, device=self.device)
+
+
+def _kv4_stream(cache: KV4Cache, batch: KVBatch, stream) -> int:
+    if not isinstance(cache, KV4Cache):
+        raise QmdError(2, f"a KV4Cache is wanted, got {type(cache).__name__}")
+    return _kv_stream(cache, batch, stream)
+
+
+def kv4_append(cache: KV4Cache, batch: KVBatch, k, v, rope=None, q=None, q_out=None, pairs: int = ROPE_HALVES,
+               positions=None, stream=None):
+    """qmd_kv4_append: kv_append into the 4-bit cache.  positions int32 [rows] says by which position each row
+    is rotated (its slot by default; the two differ once something was evicted)."""
+    st = _kv4_stream(cache, batch, stream)
+    args, q_out = _append_args(cache, batch, k, v, rope, q, q_out, pairs, stream)
+    at = None if positions is None else _array(positions, _I32, (batch.rows,), cache.index, "positions")
+    st = lib().qmd_kv4_append(*args, at, st)
+    if st:
+        _check(st)
+    return q_out
+
+
+def kv4_read(cache: KV4Cache, batch: KVBatch, k_out=None, v_out=None, stream=None, keys: bool = True, values: bool = True):
+    """qmd_kv4_read: kv_read of the 4-bit cache."""
+    st = _kv4_stream(cache, batch, stream)
+    k_out, ks, v_out, vs = _read_args(cache, batch, k_out, v_out, stream, keys, values)
+    st = lib().qmd_kv4_read(cache.ptrs, batch.ptrs, _ptr(k_out), ks, _ptr(v_out), vs, st)
+    if st:
+        _check(st)
+    return k_out, v_out
+
+
+def kv4_attention(cache: KV4Cache, batch: KVBatch, q, scale: float, workspace, window: int = 0, out=None, lse=None,
+                  stream=None):
+    """qmd_kv4_attention: kv_attention over the 4-bit cache.  lse, if given, f32 [rows, heads], receives each
+    row's log-sum-exp of its scores, which kv4_weigh takes."""
+    st = _kv4_stream(cache, batch, stream)
+    D, dev, T = cache.head_dim, cache.index, batch.rows
+    heads, qs = _rows_of(q, T, None, D, dev, "q")
+    if window >> 63:
+        raise QmdError(10, f"window: {window}")
+    if out is None:
+        out = _empty((T, heads * D), cache.device, stream)
+    _, os_ = _rows_of(out, T, heads, D, dev, "out")
+    at = None if lse is None else _array(lse, _F32, (T, heads), dev, "lse")
+    L = lib()
+    if dev not in _workspace_words:
+        _workspace_words[dev] = (int(L.qmd_kv_workspace_bytes()) // 4,)
+    ws = _array(workspace, _I32, _workspace_words[dev], dev, "workspace")
+    st = L.qmd_kv4_attention(cache.ptrs, batch.ptrs, q.data_ptr(), qs, heads, scale, window, out.data_ptr(), os_, at, ws, st)
+    if st:
+        _check(st)
+    return out
+
+
+def kv4_weigh(cache: KV4Cache, batch: KVBatch, q, scale: float, lse, weight, window: int = 0, stream=None):
+    """qmd_kv4_weigh: adds to weight (f32 [pages, kv_heads, page_tokens]) what the attention of these rows gave
+    to each cached token: q, scale and window as kv4_attention had them, lse as it left it.  The call's own
+    rows' tokens begin at nothing.  Returns weight."""
+    st = _kv4_stream(cache, batch, stream)
+    D, dev, T = cache.head_dim, cache.index, batch.rows
+    heads, qs = _rows_of(q, T, None, D, dev, "q")
+    if window >> 63:
+        raise QmdError(10, f"window: {window}")
+    st = lib().qmd_kv4_weigh(cache.ptrs, batch.ptrs, q.data_ptr(), qs, heads, scale, window,
+                             _array(lse, _F32, (T, heads), dev, "lse"),
+                             _array(weight, _F32, (cache.pages, cache.kv_heads, cache.page_tokens), dev, "weight"), st)
+    if st:
+        _check(st)
+    return weight
+
+
+def kv4_evict(cache: KV4Cache, batch: KVBatch, weight, keep: int, sinks: int = 0, recent: int = 0, len_out=None, kept=None,
+              stream=None):
+    """qmd_kv4_evict: of sequences longer than `keep` each key/value head keeps the first `sinks` tokens, the
+    last `recent`, and of the others those with the largest weight, moved to slots 0 .. keep - 1 in their order.
+    Returns len_out, int32 [seqs] (a new tensor by default): the lengths after it, min(kv_len, keep).  kept, if
+    given, int32 [seqs, kv_heads, keep], receives the slots that the tokens came from, then -1."""
+    st = _kv4_stream(cache, batch, stream)
+    dev, seqs = cache.index, batch.kv_len.shape[0]
+    for n, what in ((keep, "keep"), (sinks, "sinks"), (recent, "recent")):
+        if n >> 62:
+            raise QmdError(10, f"{what}: {n}")
+    if len_out is None:
+        len_out = _empty((seqs,), cache.device, stream, _I32)
+    at = None if kept is None else _array(kept, _I32, (seqs, cache.kv_heads, keep), dev, "kept")
+    st = lib().qmd_kv4_evict(cache.ptrs, batch.ptrs,
+                             _array(weight, _F32, (cache.pages, cache.kv_heads, cache.page_tokens), dev, "weight"), keep,
+                             sinks, recent, _array(len_out, _I32, (seqs,), dev, "len_out"), at, st)
+    if st:
+        _check(st)
+    return len_out
 
 
 def lora_add(x, base, A, B, adapter, scale, out=None, stream=None):

@@ -7,6 +7,7 @@
 
 #include "internal.h"
 #include "kv.cuh"
+#include "kv4.cuh"
 
 namespace qmd {
 namespace {
@@ -84,26 +85,55 @@ qmd_status check_kv(const qmd_kv_cache *c, const qmd_kv_batch *b, bool want_k, b
     return QMD_OK;
 }
 
-}  // namespace
-}  // namespace qmd
-
-using namespace qmd;
-
-extern "C" {
-
-qmd_status qmd_kv_append(const qmd_kv_cache *cache, const qmd_kv_batch *batch, const float *k, int64_t k_stride,
-                         const float *v, int64_t v_stride, const float *q, int64_t q_stride, int q_heads,
-                         float *q_out, int64_t q_out_stride, const float *rope, int64_t rope_rows, int rot,
-                         qmd_rope_pairs pairs, void *stream)
+// The 4-bit cache differs in what its bytes mean and in where its scales lie; its limits are the same.
+qmd_status check_kv4(const qmd_kv4_cache *c, const qmd_kv_batch *b, bool want_k, bool want_v, Kv4Params *kv)
 {
-    KvParams kv;
-    qmd_status st = check_kv(cache, batch, true, true, &kv);
+    if (!c)
+        return QMD_ERR_NULL;
+    const qmd_kv_cache c8 = {reinterpret_cast<int8_t *>(c->k), reinterpret_cast<int8_t *>(c->v),
+                             reinterpret_cast<float *>(c->k_scale), reinterpret_cast<float *>(c->v_scale),
+                             c->pages, c->kv_heads, c->page_tokens, c->head_dim};
+    const qmd_status st = check_kv(&c8, b, want_k, want_v, kv);
     if (st != QMD_OK)
         return st;
+    if (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))
+        return QMD_ERR_MISALIGNED;
+    kv->ks = kv->vs = nullptr;
+    kv->ks4 = reinterpret_cast<__half *>(c->k_scale);
+    kv->vs4 = reinterpret_cast<__half *>(c->v_scale);
+    return QMD_OK;
+}
+
+// What attention and its weights ask of queries.
+qmd_status check_queries(const KvParams &kv, int head_dim, const float *q, int64_t q_stride, int q_heads, float scale,
+                         int64_t window)
+{
+    if (!q)
+        return QMD_ERR_NULL;
+    if (q_heads < 1 || q_heads % kv.heads != 0 || q_heads / kv.heads > 64 || !stride_ok(q_stride, (int64_t)q_heads * head_dim))
+        return QMD_ERR_SHAPE;
+    if (!aligned(q, 16))
+        return QMD_ERR_MISALIGNED;
+    return std::isfinite(scale) && window >= 0 ? QMD_OK : QMD_ERR_VALUE;
+}
+
+// The current device and its error word.
+qmd_status find_device(DeviceInfo *dev, KvParams *kv)
+{
+    const qmd_status st = current_device(dev);
+    if (st != QMD_OK)
+        return st;
+    return (kv->err = device_error_word()) ? QMD_OK : QMD_ERR_DEVICE;
+}
+
+// Rows, strides, rotation, alignment and overlaps of an append.
+qmd_status check_append(const KvParams &kv, int D, int64_t T, const float *k, int64_t k_stride, const float *v,
+                        int64_t v_stride, const float *q, int64_t q_stride, int q_heads, const float *q_out,
+                        int64_t q_out_stride, const float *rope, int64_t rope_rows, int rot, qmd_rope_pairs pairs)
+{
     if (!k || !v)
         return QMD_ERR_NULL;
-    const int D = cache->head_dim;
-    const int64_t T = batch->rows, kw = (int64_t)kv.heads * D;
+    const int64_t kw = (int64_t)kv.heads * D;
     if (!stride_ok(k_stride, kw) || !stride_ok(v_stride, kw))
         return QMD_ERR_SHAPE;
     if ((q != nullptr) != (q_out != nullptr) || (q == nullptr) != (q_heads == 0))
@@ -125,6 +155,40 @@ qmd_status qmd_kv_append(const qmd_kv_cache *cache, const qmd_kv_batch *batch, c
             (rope && overlaps(q_out, extent(T, q_out_stride, qw), rope, extent(rope_rows, rot, rot))))
             return QMD_ERR_VALUE;
     }
+    return QMD_OK;
+}
+
+qmd_status check_read(const KvParams &kv, int D, int64_t T, const float *k_out, int64_t k_stride, const float *v_out,
+                      int64_t v_stride)
+{
+    const int64_t kw = (int64_t)kv.heads * D;
+    if ((k_out && !stride_ok(k_stride, kw)) || (v_out && !stride_ok(v_stride, kw)))
+        return QMD_ERR_SHAPE;
+    if (!aligned(k_out, 16) || !aligned(v_out, 16))
+        return QMD_ERR_MISALIGNED;
+    return rows_overlap({k_out, k_stride, kw}, {v_out, v_stride, kw}, T) ? QMD_ERR_VALUE : QMD_OK;
+}
+
+}  // namespace
+}  // namespace qmd
+
+using namespace qmd;
+
+extern "C" {
+
+qmd_status qmd_kv_append(const qmd_kv_cache *cache, const qmd_kv_batch *batch, const float *k, int64_t k_stride,
+                         const float *v, int64_t v_stride, const float *q, int64_t q_stride, int q_heads,
+                         float *q_out, int64_t q_out_stride, const float *rope, int64_t rope_rows, int rot,
+                         qmd_rope_pairs pairs, void *stream)
+{
+    KvParams kv;
+    qmd_status st = check_kv(cache, batch, true, true, &kv);
+    if (st != QMD_OK)
+        return st;
+    const int D = cache->head_dim;
+    if ((st = check_append(kv, D, batch->rows, k, k_stride, v, v_stride, q, q_stride, q_heads, q_out, q_out_stride, rope,
+                           rope_rows, rot, pairs)) != QMD_OK)
+        return st;
     DeviceInfo dev;
     if ((st = current_device(&dev)) != QMD_OK)
         return st;
@@ -143,13 +207,8 @@ qmd_status qmd_kv_read(const qmd_kv_cache *cache, const qmd_kv_batch *batch, flo
     qmd_status st = check_kv(cache, batch, k_out != nullptr, v_out != nullptr, &kv);
     if (st != QMD_OK)
         return st;
-    const int64_t T = batch->rows, kw = (int64_t)kv.heads * cache->head_dim;
-    if ((k_out && !stride_ok(k_stride, kw)) || (v_out && !stride_ok(v_stride, kw)))
-        return QMD_ERR_SHAPE;
-    if (!aligned(k_out, 16) || !aligned(v_out, 16))
-        return QMD_ERR_MISALIGNED;
-    if (rows_overlap({k_out, k_stride, kw}, {v_out, v_stride, kw}, T))
-        return QMD_ERR_VALUE;
+    if ((st = check_read(kv, cache->head_dim, batch->rows, k_out, k_stride, v_out, v_stride)) != QMD_OK)
+        return st;
     DeviceInfo dev;
     if ((st = current_device(&dev)) != QMD_OK)
         return st;
@@ -185,6 +244,130 @@ qmd_status qmd_kv_attention(const qmd_kv_cache *cache, const qmd_kv_batch *batch
         return QMD_ERR_DEVICE;
     return launch_kv_attention(kv, cache->head_dim, q, q_stride, q_heads, scale, window, out, out_stride, workspace,
                                dev, static_cast<cudaStream_t>(stream));
+}
+
+qmd_status qmd_kv4_append(const qmd_kv4_cache *cache, const qmd_kv_batch *batch, const float *k, int64_t k_stride,
+                          const float *v, int64_t v_stride, const float *q, int64_t q_stride, int q_heads,
+                          float *q_out, int64_t q_out_stride, const float *rope, int64_t rope_rows, int rot,
+                          qmd_rope_pairs pairs, const int32_t *positions, void *stream)
+{
+    Kv4Params kv;
+    qmd_status st = check_kv4(cache, batch, true, true, &kv);
+    if (st != QMD_OK)
+        return st;
+    const int D = cache->head_dim;
+    if ((st = check_append(kv, D, batch->rows, k, k_stride, v, v_stride, q, q_stride, q_heads, q_out, q_out_stride, rope,
+                           rope_rows, rot, pairs)) != QMD_OK)
+        return st;
+    if (!aligned(positions, 4))
+        return QMD_ERR_MISALIGNED;
+    if (overlaps(q_out, q ? extent(batch->rows, q_out_stride, (int64_t)q_heads * D) : 0, positions, (size_t)batch->rows * 4))
+        return QMD_ERR_VALUE;
+    DeviceInfo dev;
+    if ((st = find_device(&dev, &kv)) != QMD_OK)
+        return st;
+    return launch_kv4_append(kv, D, k, k_stride, v, v_stride, q, q_stride, q_heads, q_out, q_out_stride, rope, rope_rows,
+                             rot, pairs, positions, dev.sm_count, static_cast<cudaStream_t>(stream));
+}
+
+qmd_status qmd_kv4_read(const qmd_kv4_cache *cache, const qmd_kv_batch *batch, float *k_out, int64_t k_stride,
+                        float *v_out, int64_t v_stride, void *stream)
+{
+    Kv4Params kv;
+    if (!k_out && !v_out)
+        return QMD_ERR_NULL;
+    qmd_status st = check_kv4(cache, batch, k_out != nullptr, v_out != nullptr, &kv);
+    if (st != QMD_OK)
+        return st;
+    if ((st = check_read(kv, cache->head_dim, batch->rows, k_out, k_stride, v_out, v_stride)) != QMD_OK)
+        return st;
+    DeviceInfo dev;
+    if ((st = find_device(&dev, &kv)) != QMD_OK)
+        return st;
+    return launch_kv4_read(kv, cache->head_dim, k_out, k_stride, v_out, v_stride, dev.sm_count,
+                           static_cast<cudaStream_t>(stream));
+}
+
+qmd_status qmd_kv4_attention(const qmd_kv4_cache *cache, const qmd_kv_batch *batch, const float *q, int64_t q_stride,
+                             int q_heads, float scale, int64_t window, float *out, int64_t out_stride, float *lse,
+                             void *workspace, void *stream)
+{
+    Kv4Params kv;
+    qmd_status st = check_kv4(cache, batch, true, true, &kv);
+    if (st != QMD_OK)
+        return st;
+    if (!out || !workspace)
+        return QMD_ERR_NULL;
+    if ((st = check_queries(kv, cache->head_dim, q, q_stride, q_heads, scale, window)) != QMD_OK)
+        return st;
+    const int64_t qw = (int64_t)q_heads * cache->head_dim, T = batch->rows;
+    if (!stride_ok(out_stride, qw))
+        return QMD_ERR_SHAPE;
+    if (!aligned(out, 16) || !aligned(workspace, 16) || !aligned(lse, 4))
+        return QMD_ERR_MISALIGNED;
+    const Rows l = {lse, q_heads, q_heads};
+    if (rows_overlap({out, out_stride, qw}, {q, q_stride, qw}, T) || rows_overlap(l, {q, q_stride, qw}, T) ||
+        rows_overlap(l, {out, out_stride, qw}, T))
+        return QMD_ERR_VALUE;
+    DeviceInfo dev;
+    if ((st = find_device(&dev, &kv)) != QMD_OK)
+        return st;
+    return launch_kv4_attention(kv, cache->head_dim, q, q_stride, q_heads, scale, window, out, out_stride, lse, workspace,
+                                dev, static_cast<cudaStream_t>(stream));
+}
+
+qmd_status qmd_kv4_weigh(const qmd_kv4_cache *cache, const qmd_kv_batch *batch, const float *q, int64_t q_stride,
+                         int q_heads, float scale, int64_t window, const float *lse, float *weight, void *stream)
+{
+    Kv4Params kv;
+    qmd_status st = check_kv4(cache, batch, true, false, &kv);
+    if (st != QMD_OK)
+        return st;
+    if (!lse || !weight)
+        return QMD_ERR_NULL;
+    if ((st = check_queries(kv, cache->head_dim, q, q_stride, q_heads, scale, window)) != QMD_OK)
+        return st;
+    if (!aligned(lse, 4) || !aligned(weight, 16))
+        return QMD_ERR_MISALIGNED;
+    const size_t wb = (size_t)cache->pages * cache->kv_heads * cache->page_tokens * 4;
+    if (overlaps(weight, wb, q, extent(batch->rows, q_stride, (int64_t)q_heads * cache->head_dim)) ||
+        overlaps(weight, wb, lse, (size_t)batch->rows * q_heads * 4))
+        return QMD_ERR_VALUE;
+    DeviceInfo dev;
+    if ((st = find_device(&dev, &kv)) != QMD_OK)
+        return st;
+    return launch_kv4_weigh(kv, cache->head_dim, q, q_stride, q_heads, scale, window, lse, weight, dev,
+                            static_cast<cudaStream_t>(stream));
+}
+
+qmd_status qmd_kv4_evict(const qmd_kv4_cache *cache, const qmd_kv_batch *batch, float *weight, int64_t keep,
+                         int64_t sinks, int64_t recent, int32_t *len_out, int32_t *kept, void *stream)
+{
+    Kv4Params kv;
+    if (!batch)
+        return QMD_ERR_NULL;
+    // rows are not read: whatever the descriptor says of them is not looked at
+    qmd_kv_batch b = *batch;
+    b.q_start = nullptr;
+    b.max_q = 1;
+    b.rows = b.seqs > 0 ? b.seqs : 1;
+    qmd_status st = check_kv4(cache, &b, true, true, &kv);
+    if (st != QMD_OK)
+        return st;
+    if (!weight || !len_out)
+        return QMD_ERR_NULL;
+    if (!aligned(weight, 16) || !aligned(len_out, 4) || !aligned(kept, 4))
+        return QMD_ERR_MISALIGNED;
+    if (keep < 1 || keep > (1 << 24) || sinks < 0 || recent < 0 || sinks > keep || recent > keep - sinks)
+        return QMD_ERR_VALUE;
+    const size_t lb = (size_t)b.seqs * 4, kb = lb * cache->kv_heads * keep;
+    if (overlaps(len_out, lb, b.kv_len, lb) || overlaps(kept, kb, b.kv_len, lb) || overlaps(kept, kb, len_out, lb))
+        return QMD_ERR_VALUE;
+    DeviceInfo dev;
+    if ((st = find_device(&dev, &kv)) != QMD_OK)
+        return st;
+    return launch_kv4_evict(kv, cache->head_dim, weight, (int)keep, (int)sinks, (int)recent, len_out, kept, dev,
+                            static_cast<cudaStream_t>(stream));
 }
 
 size_t qmd_kv_workspace_bytes(void)

@@ -129,6 +129,21 @@ qmd_status launch_kv_attention(const KvParams &kv, int head_dim, const float *q,
                                float scale, int64_t window, float *out, int64_t out_stride, void *ws,
                                const DeviceInfo &dev, cudaStream_t s);
 size_t kv_attention_workspace(const DeviceInfo &dev);
+struct Kv4Params;  // kv4.cuh
+qmd_status launch_kv4_append(const Kv4Params &kv, int head_dim, const float *k, int64_t k_stride, const float *v,
+                             int64_t v_stride, const float *q, int64_t q_stride, int q_heads, float *q_out,
+                             int64_t q_out_stride, const float *rope, int64_t rope_rows, int rot, int pairs,
+                             const int32_t *positions, int sms, cudaStream_t s);
+qmd_status launch_kv4_read(const Kv4Params &kv, int head_dim, float *k, int64_t k_stride, float *v, int64_t v_stride,
+                           int sms, cudaStream_t s);
+qmd_status launch_kv4_attention(const Kv4Params &kv, int head_dim, const float *q, int64_t q_stride, int q_heads,
+                                float scale, int64_t window, float *out, int64_t out_stride, float *lse, void *ws,
+                                const DeviceInfo &dev, cudaStream_t s);
+qmd_status launch_kv4_weigh(const Kv4Params &kv, int head_dim, const float *q, int64_t q_stride, int q_heads,
+                            float scale, int64_t window, const float *lse, float *weight, const DeviceInfo &dev,
+                            cudaStream_t s);
+qmd_status launch_kv4_evict(const Kv4Params &kv, int head_dim, float *weight, int keep, int sinks, int recent,
+                            int32_t *len_out, int32_t *kept, const DeviceInfo &dev, cudaStream_t s);
 qmd_status launch_lora_add(qmd_half type, const float *x, const float *base, const void *A, const void *B,
                            const float *scale, const int32_t *adapter, float *out, int64_t K, int64_t rows, int rank,
                            int adapters, int batch, const DeviceInfo &dev, unsigned *err, cudaStream_t s);
