@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libqmd.so")
 BUILD_TRACE = os.path.join(HERE, "_build_trace")
 LIB_TRACE = os.path.join(HERE, "libqmd_trace.so")
 UNITS = ("api", "api_kv", "pack", "rmsnorm", "qmv_q4k", "qmv_q5k", "qmv_q6k", "bind", "alu", "kv_append",
-         "kv_attention", "kv4_append", "kv4_attention", "kv4_evict", "lora")
+         "kv_attention", "kv4_append", "kv4_attention", "kv4_weigh", "kv4_evict", "lora")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v"] + ARCH
 

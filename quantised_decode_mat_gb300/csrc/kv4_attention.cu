@@ -1,180 +1,604 @@
-// kv4_attention.cu -- attention of a decode step's rows over the 4-bit key/value cache, and the attention
-// weight that each cached token gets.
+// kv4_attention.cu -- attention of a decode step's rows over the paged 4-bit key/value cache.
 //
-// out = sum_j e^(s_j - m) V_j / sum_j e^(s_j - m) with s_j = scale q . K_j, over the slots j that a row sees; its
-// log-sum-exp m + ln sum_j e^(s_j - m); and weight_j += sum of e^(s_j - lse) over rows and heads.
+// Per row and query head, over the slots j that it sees:  out = sum_j e^(s_j - m) V_j / sum_j e^(s_j - m),
+// s_j = scale q . K_j, lse = m + ln sum_j e^(s_j - m).  One pass over the cache.
 //
-// A warp to a row and query head, 32 slots at a time: a lane takes a slot's score, then some dimensions of the
-// sums.  Weights: a warp to 32 slots of a key/value head, a lane a slot.
+// Work as in kv_attention.cu: an item is up to R = 4, 8 or 16 query rows of one sequence and key/value head, a
+// unit 32 slots of an item; the line of all units is cut into equal ranges for one CTA per SM and its warps, and
+// items that were cut are joined in the CTA and, through the workspace, between CTAs.
+//
+// A unit.  S = K Q^T as kv4_mma.cuh has it.  Then O^T += V^T P^T, the head's dimensions the 16 rows: the weights
+// move from the first product's layout to the second's by 8 x 8 transposes between lanes (movmatrix).  A value
+// scale belongs to a slot and a group of 32 dimensions, so the weights are multiplied by it, for each group
+// its own operand, as two f16 parts of 11 bits.
+//
+// Reference.  Weights are taken over 2^ref, an integer for each query row, such that weight times |scale| stays
+// under 2^16 (what f16 holds) and weights under 2^46; it moves up only when one of these is passed, to leave
+// the largest product in (2^12, 2^14] (then every sum is rescaled, exactly).  What two f16 parts lose is then
+// at most 2^-22 of a product, or 2^-37 of the largest that the row has met.  (A scale without weight does not count.)
+//
+// Loads: per unit a warp asks for the keys' and the values' codes by tiled tensor copies (swizzled, so that
+// ldmatrix meets no bank conflicts) and for their scales by plain bulk copies, into a ring of STAGES units.
+// A page of an even number of 16-token blocks holds whole units: one copy of 32 rows instead of two of 16.
+#include <climits>
+#include <mutex>
+
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "internal.h"
-#include "kv4.cuh"
-#include "ptx.cuh"
+#include "kv4_mma.cuh"
+#include "tensor_map.h"
 
 namespace qmd {
 
-struct Attn4Args {
-    Kv4Params kv;
-    const float *q;
-    float *out, *lse;
-    float *weight;
-    int64_t q_stride, out_stride, window;
-    int q_heads;
-    float scale;
+struct Attn4Args : AttnArgs {
+    const __half *ks4, *vs4;
+    int pairs;  // pages hold whole units
 };
 
-template <int D>
-__device__ float dot4(const float *q, const uint8_t *codes, const __half *scales)
+struct Attn4Maps {  // the pools as [block][16][head_dim / 2] bytes
+    CUtensorMap k, v;
+};
+
+template <int D, int R>
+struct Attn4Cfg {
+    using T = Tile4<D>;
+    static constexpr int W = D == 256 ? (R == 4 ? 8 : 6) : R == 4 ? (D == 64 ? 16 : 12) : R == 8 ? 12 : D == 64 ? 12 : 8;
+    static constexpr int STAGES = D == 64 ? 4 : D == 256 || R == 16 ? 2 : 3;
+    static constexpr int RING = STAGES * 2 * T::CODES, SRING = STAGES * 2 * T::SCALES;
+    static constexpr int SLOT = R * D * 4;
+    static constexpr bool QS = D == 256 || (D == 128 && R == 16);  // query fragments in shared memory
+    static constexpr int QN = Query4<D, R>::N;
+    static constexpr int QBYTES = QS ? QN * 128 : 0;
+    static_assert(RING >= SLOT, "a warp's last part lies in its ring");
+    static_assert(RING % 1024 == 0, "rings begin where the swizzle does");
+    static constexpr int BAR = 8 * STAGES;
+    static constexpr int FIXED = W * (RING + SRING + SLOT + QBYTES) + 2 * W * R * 8 + (W + 1) * 32 + W * (BAR + 8) + 8;
+    static_assert(FIXED + 256 + (QMD_KV_MAX_SEQS + 1) * 4 <= 227 * 1024, "fits beside the sums of the most sequences");
+};
+
+constexpr float A4_TOP = 60000.0f;  // how large a weight times scale may get
+constexpr float A4_LOG = 14.0f;     // and (log2) may be where the reference moves
+constexpr float A4_WEIGHT = 44.0f;  // likewise a weight alone, whose limit is 2^2 above
+
+// The least k with |d| < 2^k, for an f16 scale; 16 where it is not finite.
+__device__ __forceinline__ float scale4_log2(float d)
 {
-    float s = 0.0f;
-    for (int g = 0; g < D / KV4_GROUP; ++g) {
-        float part = 0.0f;
-        for (int w = 0; w < 4; ++w) {
-            float x[8];
-            unpack4(x, reinterpret_cast<const uint32_t *>(codes)[4 * g + w]);
-            for (int e = 0; e < 8; ++e)
-                part = fmaf(x[e], q[32 * g + 8 * w + e], part);
-        }
-        s = fmaf(part, __half2float(scales[g]), s);
-    }
-    return s;
+    return (float)min((int)(__float_as_uint(d) >> 23 & 255u) - 126, 16);
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) kv4_attention_kernel(const Attn4Args a)
+template <int D, int R>
+__global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
+    kv4_attention_kernel(const Attn4Args a, const __grid_constant__ Attn4Maps maps)
 {
+    using C = Attn4Cfg<D, R>;
+    using T = Tile4<D>;
+    using Q = Cols4<R>;
+    constexpr int W = C::W, S = C::STAGES, G = T::G, LR = Q::LR, NT = Q::NT;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    constexpr int SLOTS = W * C::RING, SRINGS = SLOTS + W * C::SLOT, QS0 = SRINGS + W * C::SRING;
+    float2 *s_ml = reinterpret_cast<float2 *>(smem + QS0 + W * C::QBYTES);  // [W][2][R] maximum, weight sum
+    Job *s_job = reinterpret_cast<Job *>(s_ml + 2 * W * R);                 // [1 + W]
+    uint64_t *s_bar = reinterpret_cast<uint64_t *>(s_job + W + 1);          // [W][STAGES]
+    int64_t *s_warp = reinterpret_cast<int64_t *>(s_bar + W * S);           // [W]
+    int *s_last = reinterpret_cast<int *>(s_warp + W);                      // [2]
+    int *s_pre = s_last + 2;                                                // [seqs + 1] units before a sequence
+
+    const KvParams &p = a.kv;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const uint32_t bar0 = smem_addr(s_bar + warp * S);
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+            mbar_init(bar0 + 8 * i, 1);
+        fence_barrier_init();
+        fence_proxy_async_smem();
+        s_job[1 + warp].rows = 0;
+        if (warp == 0)
+            s_job[0].rows = 0;
+    }
     pdl_launch_dependents();
     pdl_wait();
-    const Kv4Params &p = a.kv;
-    const int lane = threadIdx.x & 31;
-    const int64_t task = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int r = (int)(task / a.q_heads), h = (int)(task % a.q_heads);
-    if (r >= p.rows)
+    if ((smem_addr(smem) & 1023u) != 0) {  // the copies' swizzle counts from 1024-byte boundaries
+        atomicOr(p.err, (unsigned)ERRBIT_PLAN);
         return;
-    const int s = kv_row_seq(p, r);
-    const KvSeq sq = kv_seq(p, s);
-    if (r < sq.row0 || r >= sq.row0 + sq.n)
+    }
+    __syncwarp();
+
+    // ---- the line of units, this CTA's range, this warp's range ---------------------------------
+    auto units_in = [](const Group &gr) { return max(1, ((gr.hi + 1) >> 1) - (gr.lo >> 1)); };
+    auto units_of = [&](const KvSeq &q) {
+        int64_t u = 0;
+        for (int cg = 0; cg * R < q.n * a.group; ++cg)
+            u += units_in(group_of<R>(a, q, cg));
+        return u * p.heads;
+    };
+    const UnitLine line = unit_line<W>(p, units_of, s_warp, s_pre);
+    const int units = line.units;
+    if (line.too_many) {  // more units than a launch counts
+        kv_index_error(p);
         return;
-    const int end = max(0, sq.len - sq.n + 1 + (r - sq.row0));
-    const int begin = a.window > 0 && end > a.window ? (int)(end - a.window) : 0;
-    const int head = h / (a.q_heads / p.heads);
-    const float *q = a.q + r * a.q_stride + h * D;
-    float m = -INFINITY, sum = 0.0f, o[D / 32] = {};
-    for (int j0 = begin / 32 * 32; j0 < end; j0 += 32) {
-        const int j = j0 + lane;
-        int64_t tok = -1;
-        if (j >= begin && j < end) {
-            const int page = kv_page(p, s, j / KV_BLOCK);
-            if (page >= 0)
-                tok = kv4_token(p, page, head, j);
+    }
+    // at least a unit for every warp, so that short items are cut inside a CTA, not between CTAs
+    const int per = max(W, (units - 1) / a.by_grid + 1);
+    if ((int64_t)blockIdx.x * per >= units)
+        return;
+    const int u0 = blockIdx.x * per;
+    const int span = min(units - u0, per), pw = (span + W - 1) / W;
+    int u = warp * pw;  // from here on counted from u0
+    const int w1 = min(span, u + pw);
+
+    unsigned char *ring = smem + warp * C::RING, *sring = smem + SRINGS + warp * C::SRING;
+    const uint32_t ring_a = smem_addr(ring), sring_a = smem_addr(sring);
+    uint32_t lane_at[T::LOADS];
+#pragma unroll
+    for (int x = 0; x < T::LOADS; ++x)
+        lane_at[x] = T::at(lane, x);
+    uint32_t use = 0, use_phase = 0;  // the ring stage of the next unit to read, and its barrier's phase
+    bool dead = false;                // a copy did not land in time
+
+    int s = 0, cg = 0, head = 0, b0 = 0;  // the item of unit u, and the unit's place in it
+    if (u < w1) {
+        int pre, count;
+        s = line_find(line, p, u0 + u, s_pre, &pre, &count);
+        int rem = u0 + u - pre;
+        const KvSeq sq = kv_seq(p, s);
+        // the row groups of a head lie together: they read the same keys and values
+        const int of_head = count / a.by_heads;
+        head = rem / of_head;
+        rem -= head * of_head;
+        for (;; ++cg) {
+            const int nb = units_in(group_of<R>(a, sq, cg));
+            if (rem < nb)
+                break;
+            rem -= nb;
         }
-        const float sc = tok < 0 ? -INFINITY
-                                 : a.scale * dot4<D>(q, reinterpret_cast<const uint8_t *>(p.k) + tok * (D / 2),
-                                                     p.ks4 + tok * (D / KV4_GROUP));
-        float top = sc;
-        for (int x = 16; x > 0; x >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        const float mn = fmaxf(m, top);
-        if (mn == -INFINITY && __all_sync(0xffffffffu, tok < 0))
-            continue;
-        const float w = tok < 0 ? 0.0f : expf(sc - mn), f = expf(m - mn);
-        m = mn;
-        sum = sum * f + w;
-        for (int e = 0; e < D / 32; ++e)
-            o[e] *= f;
-        for (int x = 0; x < 32; ++x) {
-            const float wx = __shfl_sync(0xffffffffu, w, x);
-            const int64_t tx = __shfl_sync(0xffffffffu, tok, x);
-            if (tx < 0)
+        b0 = rem;
+    }
+    while (u < w1) {
+        const KvSeq sq = kv_seq(p, s);
+        const Group gr = group_of<R>(a, sq, cg);
+        const int lo2 = gr.lo >> 1, hi2 = (gr.hi + 1) >> 1;
+        const int nb = max(1, hi2 - lo2);
+        const int cnt = min(nb - b0, w1 - u);          // units of this item in the range
+        const int real = min(cnt, hi2 - lo2 - b0);     // those that hold slots
+
+        // pages, 32 units at a time, a lane each: a unit's two blocks in the pool, or -1
+        const int first_blk = 2 * (lo2 + b0);
+        auto block_of = [&](int blk) -> int {
+            if (blk < gr.lo || blk >= gr.hi)
+                return -1;
+            const int col = blk / a.by_blocks;
+            const int page = p.table[(int64_t)s * p.table_stride + col];
+            if (page < 0 || page >= p.pages) {
+                kv_index_error(p);
+                return -1;
+            }
+            return (page * p.heads + head - col) * p.page_blocks + blk;
+        };
+        int2 bi = make_int2(-1, -1), bi_n = bi;  // of this chunk of 32 units, and of the next
+        auto look_up = [&](int i) -> int2 {      // the item's i-th unit here
+            int2 b = make_int2(-1, -1);
+            if (i < real) {
+                const int blk = first_blk + 2 * i;
+                if (a.pairs) {  // both blocks lie in one page, whichever of them is seen
+                    b.x = block_of(max(blk, gr.lo));
+                    if (b.x >= 0)
+                        b.x -= max(blk, gr.lo) - blk;
+                    b.y = b.x >= 0 ? b.x + 1 : -1;
+                } else {
+                    b.x = block_of(blk);
+                    b.y = block_of(blk + 1);
+                }
+            }
+            return b;
+        };
+        bi = look_up(lane);
+        fence_proxy_async_smem();
+        __syncwarp();  // every lane has read the last item's ring
+
+        auto issue = [&](int j, int x, int y, uint32_t stage) {  // copy the item's j-th unit, blocks x and y, into a stage
+            if (j < real && lane == 0) {
+                const uint32_t dst = ring_a + stage * 2 * T::CODES, sdst = sring_a + stage * 2 * T::SCALES;
+                const uint32_t bar = bar0 + 8 * stage;
+                constexpr int HC = T::CODES / 2, HS = T::SCALES / 2;
+                mbar_arrive_expect_tx(bar, (x >= 0 ? 2 * (HC + HS) : 0) + (y >= 0 ? 2 * (HC + HS) : 0));
+                if (a.pairs) {
+                    if (x >= 0) {
+                        load_tile(dst, &maps.k, 0, x, bar);
+                        load_bytes(sdst, a.ks4 + (int64_t)x * (HS / 2), 2 * HS, bar);
+                        load_tile(dst + T::CODES, &maps.v, 0, x, bar);
+                        load_bytes(sdst + T::SCALES, a.vs4 + (int64_t)x * (HS / 2), 2 * HS, bar);
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int b = h ? y : x;
+                        if (b >= 0) {
+                            load_tile(dst + h * HC, &maps.k, 0, b, bar);
+                            load_bytes(sdst + h * HS, a.ks4 + (int64_t)b * (HS / 2), HS, bar);
+                            load_tile(dst + T::CODES + h * HC, &maps.v, 0, b, bar);
+                            load_bytes(sdst + T::SCALES + h * HS, a.vs4 + (int64_t)b * (HS / 2), HS, bar);
+                        }
+                    }
+                }
+            }
+        };
+        uint32_t put = use;  // the ring stage of the next unit to ask for
+#pragma unroll
+        for (int j = 0; j < S - 1; ++j) {
+            issue(j, __shfl_sync(0xffffffffu, bi.x, j), __shfl_sync(0xffffffffu, bi.y, j), put);
+            put = put + 1 == S ? 0 : put + 1;
+        }
+
+        Query4<D, R> qf;
+        qf.load(a.q, [&](int r) { return row_offset(a, sq.row0, head, cg * R + r, a.q_stride, D); }, gr.rows, a.scale_log2e);
+        uint4 *q_keep = reinterpret_cast<uint4 *>(smem + QS0 + warp * C::QBYTES) + lane;
+        if constexpr (C::QS) {
+#pragma unroll
+            for (int i = 0; i < C::QN / 4; ++i)
+                q_keep[i * 32] = make_uint4(qf.f[4 * i], qf.f[4 * i + 1], qf.f[4 * i + 2], qf.f[4 * i + 3]);
+        }
+        auto query = [&](int i) {
+            if constexpr (C::QS)
+                return q_keep[i * 32];
+            else
+                return make_uint4(qf.f[4 * i], qf.f[4 * i + 1], qf.f[4 * i + 2], qf.f[4 * i + 3]);
+        };
+        // slots in [all_from, all_to) are seen by every row of the group
+        const int all_to = row_end(sq, cg * R / a.by_group);
+        const int all_from = row_begin(a, row_end(sq, (cg * R + gr.rows - 1) / a.by_group));
+
+        float o[NT][D / 16][4];
+        float ref[LR], l[LR];
+#pragma unroll
+        for (int i = 0; i < LR; ++i)
+            ref[i] = ATT_NONE, l[i] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+                o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
+
+        for (int idx = 0; idx < real; ++idx) {
+            if ((idx & 31) == 16 && (idx | 31) + 1 < real)
+                bi_n = look_up((idx | 31) + 1 + lane);
+            const int bx = __shfl_sync(0xffffffffu, bi.x, idx & 31), by = __shfl_sync(0xffffffffu, bi.y, idx & 31);
+            const uint32_t next = use + 1 == S ? 0 : use + 1, next_phase = next == 0 ? use_phase ^ 1u : use_phase;
+            fence_proxy_async_smem();
+            __syncwarp();  // every lane has read the stage that is asked for again
+            {
+                const int j = idx + S - 1;
+                const bool later = (j ^ idx) & 32;
+                issue(j, __shfl_sync(0xffffffffu, later ? bi_n.x : bi.x, j & 31),
+                      __shfl_sync(0xffffffffu, later ? bi_n.y : bi.y, j & 31), put);
+                put = put + 1 == S ? 0 : put + 1;
+            }
+            if ((idx & 31) == 31)
+                bi = bi_n;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar0 + 8 * use, use_phase, a.wait_ns))) {
+                dead = true;
+                break;
+            }
+            const uint32_t codes = ring_a + use * 2 * T::CODES;
+            const unsigned char *scales = sring + use * 2 * T::SCALES;
+            float sc[2][LR][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                scores4<D, R>(sc[h], codes + h * 16 * T::ROW, scales + h * 16 * G * 2, lane_at, query, qf.scale);
+            uint32_t dv[2][2][G / 2];  // the values' scales, of slots 16 h + g + 8 e
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                load_scales<D>(dv[h], scales + T::SCALES + h * 16 * G * 2, g);
+
+            const int pos = (first_blk + 2 * idx) * KV_BLOCK;
+            unsigned poison = 0;
+            if (pos < all_from || pos + KV4_UNIT > all_to || bx < 0 || by < 0) {
+                // some slot is not there, or not seen by some row
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = pos + 16 * h + 8 * e + g;
+                        bool any = false, all = true, bad = false;
+                        bool sees[LR];
+#pragma unroll
+                        for (int i = 0; i < LR; ++i) {
+                            const int end = row_end(sq, (cg * R + min(Q::row(i, t), gr.rows - 1)) / a.by_group);
+                            sees[i] = (h ? by : bx) >= 0 && j >= row_begin(a, end) && j < end;
+                            any |= sees[i];
+                            all &= sees[i];
+                            if (!sees[i])
+                                sc[h][i][e] = -INFINITY;
+                        }
+                        // a scale that is not finite must not reach rows that do not see its slot: where some of the
+                        // lane's do not, it is 0 and the others' values are made NaN below
+#pragma unroll
+                        for (int i = 0; i < G / 2; ++i) {
+                            const float2 d = halves(dv[h][e][i]);
+                            bad |= !(fabsf(d.x) <= 65504.0f && fabsf(d.y) <= 65504.0f);
+                        }
+                        if (!any || (bad && !all)) {
+#pragma unroll
+                            for (int i = 0; i < G / 2; ++i)
+                                dv[h][e][i] = 0;
+#pragma unroll
+                            for (int i = 0; i < LR; ++i)
+                                if (sees[i])
+                                    poison |= 1u << (4 * i + 2 * h + e);
+                        }
+                    }
+            }
+            // the slots' largest |scale|
+            float dm[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    __half2 m = __habs2(*reinterpret_cast<const __half2 *>(&dv[h][e][0]));
+#pragma unroll
+                    for (int i = 1; i < G / 2; ++i)
+                        m = __hmax2(m, __habs2(*reinterpret_cast<const __half2 *>(&dv[h][e][i])));
+                    const float2 f = __half22float2(m);
+                    dm[h][e] = fmaxf(f.x, f.y);
+                }
+            float w[2][LR][2];
+            bool up = false;
+#pragma unroll
+            for (int i = 0; i < LR; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float x = sc[h][i][e] - ref[i];
+                        w[h][i][e] = ex2(x);
+                        up |= x > A4_WEIGHT + 2.0f || w[h][i][e] * dm[h][e] > A4_TOP;
+                    }
+            if (__any_sync(0xffffffffu, up)) {
+                float f[LR];
+#pragma unroll
+                for (int i = 0; i < LR; ++i) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            top = fmaxf(top, sc[h][i][e] + fmaxf(dm[h][e] > 0.0f ? scale4_log2(dm[h][e]) - A4_LOG : -A4_WEIGHT,
+                                                                 -A4_WEIGHT));
+#pragma unroll
+                    for (int x = 4; x < 32; x <<= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    const float now = top > ref[i] ? ceilf(top) : ref[i];
+                    f[i] = pow2(ref[i] - now);
+                    ref[i] = now;
+                    l[i] *= f[i];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            w[h][i][e] = ex2(sc[h][i][e] - now);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[n][i][e] *= f[R == 4 ? 0 : 2 * n + (e & 1)];
+            }
+#pragma unroll
+            for (int i = 0; i < LR; ++i)
+                l[i] += (w[0][i][0] + w[0][i][1]) + (w[1][i][0] + w[1][i][1]);
+            if (poison) {
+#pragma unroll
+                for (int i = 0; i < LR; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (poison >> (4 * i + 2 * h + e) & 1)
+                                w[h][i][e] = NAN;
+            }
+
+            // the second product: V^T P^T, 16 slots at a time, for each group its own weights
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[2][G];
+                load_words<D, true>(v, codes + T::CODES + h * 16 * T::ROW, lane_at);
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    uint32_t x[4], y[4];
+                    unpack4_f16(x, v[0][i]);
+                    unpack4_f16(y, v[1][i]);
+                    const uint32_t first[4] = {x[0], x[1], y[0], y[1]}, second[4] = {x[2], x[3], y[2], y[3]};
+                    float d[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 two = halves(dv[h][e][i / 2]);
+                        d[e] = i & 1 ? two.y : two.x;
+                    }
+                    if constexpr (R == 4) {
+                        uint32_t b[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float q = w[h][0][e] * d[e], hi = first_bits(q);
+                            b[e] = transpose_8x8(pack_f16(hi, q - hi));
+                        }
+                        mma_16816(o[0][2 * i], first, b[0], b[1]);
+                        mma_16816(o[0][2 * i + 1], second, b[0], b[1]);
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            uint32_t bh[2], bl[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float q0 = w[h][(2 * n) % LR][e] * d[e], q1 = w[h][(2 * n + 1) % LR][e] * d[e];
+                                const float h0 = first_bits(q0), h1 = first_bits(q1);
+                                bh[e] = transpose_8x8(pack_f16(h0, h1));
+                                bl[e] = transpose_8x8(pack_f16(q0 - h0, q1 - h1));
+                            }
+                            mma_16816(o[n][2 * i], first, bl[0], bl[1]);
+                            mma_16816(o[n][2 * i + 1], second, bl[0], bl[1]);
+                            mma_16816(o[n][2 * i], first, bh[0], bh[1]);
+                            mma_16816(o[n][2 * i + 1], second, bh[0], bh[1]);
+                        }
+                    }
+                }
+            }
+            use = next;
+            use_phase = next_phase;
+        }
+        if (dead) {
+            // flag it, wait (bounded) for this warp's copies that may be in flight, leave the rest out
+            if (lane == 0) {
+                atomicOr(p.err, (unsigned)ERRBIT_QMV_WAIT);
+                for (int i = 0; i < S; ++i) {
+                    if (!mbar_wait_bounded(bar0 + 8 * use, use_phase, a.wait_ns)) {
+                        atomicOr(p.err, (unsigned)ERRBIT_DRAIN_WAIT);
+                        break;
+                    }
+                    use = use + 1 == S ? 0 : use + 1;
+                    use_phase = use == 0 ? use_phase ^ 1u : use_phase;
+                }
+            }
+            __syncwarp();
+            break;
+        }
+
+        // ---- the item's part: finished, or laid down for the join --------------------------------
+        const bool done = b0 == 0 && cnt == nb;
+        const int part = b0 > 0 ? 0 : 1;
+        float *dst = reinterpret_cast<float *>(part == 0 ? smem + SLOTS + warp * C::SLOT : ring);
+        if (part == 1 && !done)
+            __syncwarp();  // every lane has read the ring
+#pragma unroll
+        for (int i = 0; i < LR; ++i) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1)
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+            const int r = Q::row(i, t);
+            if (!done && g == 0)
+                s_ml[(warp * 2 + part) * R + r] = make_float2(ref[i], l[i]);
+            if (done && r >= gr.rows)
                 continue;
-            for (int e = 0; e < D / 32; ++e) {
-                const int d = 32 * e + lane;
-                const int c = reinterpret_cast<const uint8_t *>(p.v)[tx * (D / 2) + d / 2] >> 4 * (d & 1) & 15;
-                o[e] = fmaf(wx, __half2float(p.vs4[tx * (D / KV4_GROUP) + e]) * (float)(c - 8), o[e]);
+            if (done && a.lse && g == 0)
+                store_lse(a, sq.row0, head, cg * R + r, ref[i], l[i]);
+            const float f = done ? (l[i] == 0.0f ? 0.0f : 1.0f / l[i]) : 1.0f;
+            float *to = (done ? a.out + row_offset(a, sq.row0, head, cg * R + r, a.out_stride, D) : dst + r * D) + 4 * g;
+#pragma unroll
+            for (int j = 0; j < G; ++j) {
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float(&c)[4] = o[R == 4 ? 0 : i / 2][2 * j + (e >> 1)];
+                    y[e] = (R == 4 ? c[2 * (e & 1)] + c[2 * (e & 1) + 1] : c[2 * (e & 1) + (i & 1)]) * f;
+                }
+                store_f32(to + 32 * j, y);
+            }
+        }
+        // the item's first cut in this CTA makes the job of joining it
+        if (!done && lane == 0 && (part == 1 || warp == 0)) {
+            Job &j = s_job[part == 1 ? 1 + warp : 0];
+            j.start = u - b0;
+            j.end = u - b0 + nb;
+            j.row0 = sq.row0;
+            j.first = cg * R;
+            j.head = head;
+            j.rows = gr.rows;
+        }
+        u += cnt;
+        b0 = 0;
+        if (u < w1 && ++cg * R >= sq.n * a.group) {  // on to the next head, or the next sequence with rows
+            cg = 0;
+            if (++head == p.heads) {
+                head = 0;
+                s = line_next(line, s, s_pre);
             }
         }
     }
-    for (int x = 16; x > 0; x >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, x);
-    for (int e = 0; e < D / 32; ++e)
-        a.out[r * a.out_stride + h * D + 32 * e + lane] = sum == 0.0f ? 0.0f : o[e] / sum;
-    if (a.lse && lane == 0)
-        a.lse[(int64_t)r * a.q_heads + h] = sum == 0.0f ? -INFINITY : m + logf(sum);
+    __syncthreads();
+    join_parts<D, R, W, true>(a, s_job, s_ml, s_last, smem, C::RING, SLOTS, C::SLOT, u0, span, pw, per);
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) kv4_weigh_kernel(const Attn4Args a)
+// The two pools as tensors of 16-row blocks; a copy takes `blocks` of them, swizzled as their rows are long.
+qmd_status kv4_map(CUtensorMap *map, const void *base, const KvParams &kv, int head_dim, int blocks)
 {
-    pdl_launch_dependents();
-    pdl_wait();
-    const Kv4Params &p = a.kv;
-    const int lane = threadIdx.x & 31, G = a.q_heads / p.heads;
-    const int s = blockIdx.y / p.heads, head = blockIdx.y % p.heads;
-    const KvSeq sq = kv_seq(p, s);
-    if (sq.n == 0)
-        return;
-    const int first = a.window > 0 ? (int)max((int64_t)0, sq.len - sq.n + 1 - a.window) : 0;
-    for (int j = (blockIdx.x * 4 + (threadIdx.x >> 5)) * 32 + lane; j < sq.len; j += gridDim.x * 128) {
-        const bool is_new = j >= sq.len - sq.n;
-        if (j < first && !is_new)
-            continue;
-        const int page = kv_page(p, s, j / KV_BLOCK);
-        if (page < 0)
-            continue;
-        const int64_t tok = kv4_token(p, page, head, j);
-        float w = is_new ? 0.0f : a.weight[tok];
-        for (int i = 0; i < sq.n; ++i) {
-            const int end = sq.len - sq.n + 1 + i;
-            if (j >= end || (a.window > 0 && j < end - a.window))
-                continue;
-            for (int g = 0; g < G; ++g) {
-                const int h = head * G + g;
-                const float sc = a.scale * dot4<D>(a.q + (sq.row0 + i) * a.q_stride + h * D,
-                                                   reinterpret_cast<const uint8_t *>(p.k) + tok * (D / 2),
-                                                   p.ks4 + tok * (D / KV4_GROUP));
-                w += expf(sc - a.lse[(int64_t)(sq.row0 + i) * a.q_heads + h]);
-            }
+    const TensorMapEncodeFn enc = tensor_map_encoder();
+    if (!enc)
+        return fail(QMD_ERR_LAUNCH, "cuTensorMapEncodeTiled entry point", cudaErrorNotSupported);
+    const cuuint64_t row = (cuuint64_t)head_dim / 2;
+    const cuuint64_t dim[3] = {row, KV_BLOCK, (cuuint64_t)kv.pages * kv.heads * kv.page_blocks}, str[2] = {row, row * KV_BLOCK};
+    const cuuint32_t box[3] = {(cuuint32_t)row, KV_BLOCK, (cuuint32_t)blocks}, one[3] = {1, 1, 1};
+    const CUtensorMapSwizzle swizzle = row == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                       : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                   : CU_TENSOR_MAP_SWIZZLE_128B;
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dim, str, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? QMD_OK
+               : fail(QMD_ERR_LAUNCH, "tensor map of the 4-bit cache", cudaErrorInvalidValue);
+}
+
+template <int D, int R>
+static qmd_status launch_att4(const Attn4Args &a, const DeviceInfo &dev, cudaStream_t s)
+{
+    using C = Attn4Cfg<D, R>;
+    const size_t smem = C::FIXED + ((size_t)a.kv.seqs + 1) * sizeof(int);
+    if (smem + 256 > (size_t)dev.smem_optin)
+        return QMD_ERR_SHAPE;
+    {
+        static std::mutex mu;
+        static bool opted[64] = {false};
+        std::lock_guard<std::mutex> lock(mu);
+        if (!opted[dev.device]) {
+            const cudaError_t e = cudaFuncSetAttribute(kv4_attention_kernel<D, R>,
+                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, dev.smem_optin - 256);
+            if (e != cudaSuccess)
+                return fail(QMD_ERR_LAUNCH, "kv4_attention smem attribute", e);
+            opted[dev.device] = true;
         }
-        a.weight[tok] = w;
     }
-}
-
-static qmd_status launch4(void (*kernel)(const Attn4Args), const Attn4Args &a, dim3 grid, const char *what, cudaStream_t s)
-{
+    Attn4Maps maps;
+    qmd_status st = kv4_map(&maps.k, a.kv.k, a.kv, D, a.pairs ? 2 : 1);
+    if (st == QMD_OK)
+        st = kv4_map(&maps.v, a.kv.v, a.kv, D, a.pairs ? 2 : 1);
+    if (st != QMD_OK)
+        return st;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)dev.sm_count);
+    cfg.blockDim = dim3(C::W * 32);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (launch_flags() & LAUNCH_NO_PDL) ? 0 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
-    return e == cudaSuccess ? QMD_OK : fail(QMD_ERR_LAUNCH, what, e);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_attention_kernel<D, R>, a, maps);
+    return e == cudaSuccess ? QMD_OK : fail(QMD_ERR_LAUNCH, "kv4_attention launch", e);
 }
 
 qmd_status launch_kv4_attention(const Kv4Params &kv, int head_dim, const float *q, int64_t q_stride, int q_heads,
                                 float scale, int64_t window, float *out, int64_t out_stride, float *lse, void *ws,
                                 const DeviceInfo &dev, cudaStream_t s)
 {
-    const Attn4Args a = {kv, q, out, lse, nullptr, q_stride, out_stride, window, q_heads, scale};
-    const dim3 grid((unsigned)((kv.rows * q_heads + 3) / 4));
-    return head_dim == 64    ? launch4(kv4_attention_kernel<64>, a, grid, "kv4_attention launch", s)
-           : head_dim == 128 ? launch4(kv4_attention_kernel<128>, a, grid, "kv4_attention launch", s)
-                             : launch4(kv4_attention_kernel<256>, a, grid, "kv4_attention launch", s);
-}
-
-qmd_status launch_kv4_weigh(const Kv4Params &kv, int head_dim, const float *q, int64_t q_stride, int q_heads,
-                            float scale, int64_t window, const float *lse, float *weight, const DeviceInfo &dev,
-                            cudaStream_t s)
-{
-    const Attn4Args a = {kv, q, nullptr, const_cast<float *>(lse), weight, q_stride, 0, window, q_heads, scale};
-    const dim3 grid(64, (unsigned)(kv.seqs * kv.heads));
-    return head_dim == 64    ? launch4(kv4_weigh_kernel<64>, a, grid, "kv4_weigh launch", s)
-           : head_dim == 128 ? launch4(kv4_weigh_kernel<128>, a, grid, "kv4_weigh launch", s)
-                             : launch4(kv4_weigh_kernel<256>, a, grid, "kv4_weigh launch", s);
+    Attn4Args a;
+    static_cast<AttnArgs &>(a) = attn_args(kv, q, q_stride, q_heads, scale, window, out, out_stride, ws, dev);
+    a.lse = lse;
+    a.ks4 = kv.ks4;
+    a.vs4 = kv.vs4;
+    a.pairs = kv.page_blocks % 2 == 0;
+    // rows per item: the least of 4, 8, 16 that holds a sequence's rows of one key/value head
+    const int64_t rows = (int64_t)a.group * kv.max_q;
+    if (head_dim == 64)
+        return rows <= 4 ? launch_att4<64, 4>(a, dev, s) : rows <= 8 ? launch_att4<64, 8>(a, dev, s) : launch_att4<64, 16>(a, dev, s);
+    if (head_dim == 128)
+        return rows <= 4   ? launch_att4<128, 4>(a, dev, s)
+               : rows <= 8 ? launch_att4<128, 8>(a, dev, s)
+                           : launch_att4<128, 16>(a, dev, s);
+    return rows <= 4 ? launch_att4<256, 4>(a, dev, s) : launch_att4<256, 8>(a, dev, s);
 }
 
 }  // namespace qmd
