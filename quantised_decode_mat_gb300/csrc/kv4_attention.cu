@@ -28,17 +28,11 @@
 
 #include "internal.h"
 #include "kv4_mma.cuh"
-#include "tensor_map.h"
 
 namespace qmd {
 
 struct Attn4Args : AttnArgs {
-    const __half *ks4, *vs4;
-    int pairs;  // pages hold whole units
-};
-
-struct Attn4Maps {  // the pools as [block][16][head_dim / 2] bytes
-    CUtensorMap k, v;
+    Units4Args units;
 };
 
 template <int D, int R>
@@ -54,7 +48,7 @@ struct Attn4Cfg {
     static_assert(RING >= SLOT, "a warp's last part lies in its ring");
     static_assert(RING % 1024 == 0, "rings begin where the swizzle does");
     static constexpr int BAR = 8 * STAGES;
-    static constexpr int FIXED = W * (RING + SRING + SLOT + QBYTES) + 2 * W * R * 8 + (W + 1) * 32 + W * (BAR + 8) + 8;
+    static constexpr int FIXED = W * (RING + SRING + SLOT + QBYTES) + 2 * W * R * 8 + (W + 1) * 32 + W * (BAR + 8) + 8 + 16;
     static_assert(FIXED + 256 + (QMD_KV_MAX_SEQS + 1) * 4 <= 227 * 1024, "fits beside the sums of the most sequences");
 };
 
@@ -70,7 +64,7 @@ __device__ __forceinline__ float scale4_log2(float d)
 
 template <int D, int R>
 __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
-    kv4_attention_kernel(const Attn4Args a, const __grid_constant__ Attn4Maps maps)
+    kv4_attention_kernel(const Attn4Args a, const __grid_constant__ Maps4 maps)
 {
     using C = Attn4Cfg<D, R>;
     using T = Tile4<D>;
@@ -83,7 +77,8 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
     uint64_t *s_bar = reinterpret_cast<uint64_t *>(s_job + W + 1);          // [W][STAGES]
     int64_t *s_warp = reinterpret_cast<int64_t *>(s_bar + W * S);           // [W]
     int *s_last = reinterpret_cast<int *>(s_warp + W);                      // [2]
-    int *s_pre = s_last + 2;                                                // [seqs + 1] units before a sequence
+    int *s_range = s_last + 2;                                              // u0, span, pw, per
+    int *s_pre = s_range + 4;                                               // [seqs + 1] units before a sequence
 
     const KvParams &p = a.kv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -127,16 +122,17 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
         return;
     const int u0 = blockIdx.x * per;
     const int span = min(units - u0, per), pw = (span + W - 1) / W;
+    if (tid == 0)
+        s_range[0] = u0, s_range[1] = span, s_range[2] = pw, s_range[3] = per;  // (the joins read them again: registers are few in between)
     int u = warp * pw;  // from here on counted from u0
     const int w1 = min(span, u + pw);
 
     unsigned char *ring = smem + warp * C::RING, *sring = smem + SRINGS + warp * C::SRING;
-    const uint32_t ring_a = smem_addr(ring), sring_a = smem_addr(sring);
+    Units4<D, S, true> kv = {a, a.units, maps, smem_addr(ring), smem_addr(sring), bar0};
     uint32_t lane_at[T::LOADS];
 #pragma unroll
     for (int x = 0; x < T::LOADS; ++x)
         lane_at[x] = T::at(lane, x);
-    uint32_t use = 0, use_phase = 0;  // the ring stage of the next unit to read, and its barrier's phase
     bool dead = false;                // a copy did not land in time
 
     int s = 0, cg = 0, head = 0, b0 = 0;  // the item of unit u, and the unit's place in it
@@ -165,74 +161,8 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
         const int cnt = min(nb - b0, w1 - u);          // units of this item in the range
         const int real = min(cnt, hi2 - lo2 - b0);     // those that hold slots
 
-        // pages, 32 units at a time, a lane each: a unit's two blocks in the pool, or -1
         const int first_blk = 2 * (lo2 + b0);
-        auto block_of = [&](int blk) -> int {
-            if (blk < gr.lo || blk >= gr.hi)
-                return -1;
-            const int col = blk / a.by_blocks;
-            const int page = p.table[(int64_t)s * p.table_stride + col];
-            if (page < 0 || page >= p.pages) {
-                kv_index_error(p);
-                return -1;
-            }
-            return (page * p.heads + head - col) * p.page_blocks + blk;
-        };
-        int2 bi = make_int2(-1, -1), bi_n = bi;  // of this chunk of 32 units, and of the next
-        auto look_up = [&](int i) -> int2 {      // the item's i-th unit here
-            int2 b = make_int2(-1, -1);
-            if (i < real) {
-                const int blk = first_blk + 2 * i;
-                if (a.pairs) {  // both blocks lie in one page, whichever of them is seen
-                    b.x = block_of(max(blk, gr.lo));
-                    if (b.x >= 0)
-                        b.x -= max(blk, gr.lo) - blk;
-                    b.y = b.x >= 0 ? b.x + 1 : -1;
-                } else {
-                    b.x = block_of(blk);
-                    b.y = block_of(blk + 1);
-                }
-            }
-            return b;
-        };
-        bi = look_up(lane);
-        fence_proxy_async_smem();
-        __syncwarp();  // every lane has read the last item's ring
-
-        auto issue = [&](int j, int x, int y, uint32_t stage) {  // copy the item's j-th unit, blocks x and y, into a stage
-            if (j < real && lane == 0) {
-                const uint32_t dst = ring_a + stage * 2 * T::CODES, sdst = sring_a + stage * 2 * T::SCALES;
-                const uint32_t bar = bar0 + 8 * stage;
-                constexpr int HC = T::CODES / 2, HS = T::SCALES / 2;
-                mbar_arrive_expect_tx(bar, (x >= 0 ? 2 * (HC + HS) : 0) + (y >= 0 ? 2 * (HC + HS) : 0));
-                if (a.pairs) {
-                    if (x >= 0) {
-                        load_tile(dst, &maps.k, 0, x, bar);
-                        load_bytes(sdst, a.ks4 + (int64_t)x * (HS / 2), 2 * HS, bar);
-                        load_tile(dst + T::CODES, &maps.v, 0, x, bar);
-                        load_bytes(sdst + T::SCALES, a.vs4 + (int64_t)x * (HS / 2), 2 * HS, bar);
-                    }
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int b = h ? y : x;
-                        if (b >= 0) {
-                            load_tile(dst + h * HC, &maps.k, 0, b, bar);
-                            load_bytes(sdst + h * HS, a.ks4 + (int64_t)b * (HS / 2), HS, bar);
-                            load_tile(dst + T::CODES + h * HC, &maps.v, 0, b, bar);
-                            load_bytes(sdst + T::SCALES + h * HS, a.vs4 + (int64_t)b * (HS / 2), HS, bar);
-                        }
-                    }
-                }
-            }
-        };
-        uint32_t put = use;  // the ring stage of the next unit to ask for
-#pragma unroll
-        for (int j = 0; j < S - 1; ++j) {
-            issue(j, __shfl_sync(0xffffffffu, bi.x, j), __shfl_sync(0xffffffffu, bi.y, j), put);
-            put = put + 1 == S ? 0 : put + 1;
-        }
-
+        kv.begin(s, head, gr.lo, gr.hi, first_blk, real);
         Query4<D, R> qf;
         qf.load(a.q, [&](int r) { return row_offset(a, sq.row0, head, cg * R + r, a.q_stride, D); }, gr.rows, a.scale_log2e);
         uint4 *q_keep = reinterpret_cast<uint4 *>(smem + QS0 + warp * C::QBYTES) + lane;
@@ -263,27 +193,13 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
                 o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
 
         for (int idx = 0; idx < real; ++idx) {
-            if ((idx & 31) == 16 && (idx | 31) + 1 < real)
-                bi_n = look_up((idx | 31) + 1 + lane);
-            const int bx = __shfl_sync(0xffffffffu, bi.x, idx & 31), by = __shfl_sync(0xffffffffu, bi.y, idx & 31);
-            const uint32_t next = use + 1 == S ? 0 : use + 1, next_phase = next == 0 ? use_phase ^ 1u : use_phase;
-            fence_proxy_async_smem();
-            __syncwarp();  // every lane has read the stage that is asked for again
-            {
-                const int j = idx + S - 1;
-                const bool later = (j ^ idx) & 32;
-                issue(j, __shfl_sync(0xffffffffu, later ? bi_n.x : bi.x, j & 31),
-                      __shfl_sync(0xffffffffu, later ? bi_n.y : bi.y, j & 31), put);
-                put = put + 1 == S ? 0 : put + 1;
-            }
-            if ((idx & 31) == 31)
-                bi = bi_n;
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(bar0 + 8 * use, use_phase, a.wait_ns))) {
+            int bx, by;
+            if (!kv.next(idx, bx, by)) {
                 dead = true;
                 break;
             }
-            const uint32_t codes = ring_a + use * 2 * T::CODES;
-            const unsigned char *scales = sring + use * 2 * T::SCALES;
+            const uint32_t codes = kv.ring + kv.use * kv.CODES;
+            const unsigned char *scales = sring + kv.use * kv.SCALES;
             float sc[2][LR][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -447,23 +363,10 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
                     }
                 }
             }
-            use = next;
-            use_phase = next_phase;
+            kv.advance();
         }
         if (dead) {
-            // flag it, wait (bounded) for this warp's copies that may be in flight, leave the rest out
-            if (lane == 0) {
-                atomicOr(p.err, (unsigned)ERRBIT_QMV_WAIT);
-                for (int i = 0; i < S; ++i) {
-                    if (!mbar_wait_bounded(bar0 + 8 * use, use_phase, a.wait_ns)) {
-                        atomicOr(p.err, (unsigned)ERRBIT_DRAIN_WAIT);
-                        break;
-                    }
-                    use = use + 1 == S ? 0 : use + 1;
-                    use_phase = use == 0 ? use_phase ^ 1u : use_phase;
-                }
-            }
-            __syncwarp();
+            kv.drain();  // the rest is left out
             break;
         }
 
@@ -519,26 +422,8 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
         }
     }
     __syncthreads();
-    join_parts<D, R, W, true>(a, s_job, s_ml, s_last, smem, C::RING, SLOTS, C::SLOT, u0, span, pw, per);
-}
-
-// The two pools as tensors of 16-row blocks; a copy takes `blocks` of them, swizzled as their rows are long.
-qmd_status kv4_map(CUtensorMap *map, const void *base, const KvParams &kv, int head_dim, int blocks)
-{
-    const TensorMapEncodeFn enc = tensor_map_encoder();
-    if (!enc)
-        return fail(QMD_ERR_LAUNCH, "cuTensorMapEncodeTiled entry point", cudaErrorNotSupported);
-    const cuuint64_t row = (cuuint64_t)head_dim / 2;
-    const cuuint64_t dim[3] = {row, KV_BLOCK, (cuuint64_t)kv.pages * kv.heads * kv.page_blocks}, str[2] = {row, row * KV_BLOCK};
-    const cuuint32_t box[3] = {(cuuint32_t)row, KV_BLOCK, (cuuint32_t)blocks}, one[3] = {1, 1, 1};
-    const CUtensorMapSwizzle swizzle = row == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
-                                       : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                                   : CU_TENSOR_MAP_SWIZZLE_128B;
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dim, str, box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? QMD_OK
-               : fail(QMD_ERR_LAUNCH, "tensor map of the 4-bit cache", cudaErrorInvalidValue);
+    join_parts<D, R, W, true>(a, s_job, s_ml, s_last, smem, C::RING, SLOTS, C::SLOT, s_range[0], s_range[1], s_range[2],
+                              s_range[3]);
 }
 
 template <int D, int R>
@@ -560,10 +445,10 @@ static qmd_status launch_att4(const Attn4Args &a, const DeviceInfo &dev, cudaStr
             opted[dev.device] = true;
         }
     }
-    Attn4Maps maps;
-    qmd_status st = kv4_map(&maps.k, a.kv.k, a.kv, D, a.pairs ? 2 : 1);
+    Maps4 maps;
+    qmd_status st = kv4_map(&maps.k, a.kv.k, a.kv, D, a.units.pairs);
     if (st == QMD_OK)
-        st = kv4_map(&maps.v, a.kv.v, a.kv, D, a.pairs ? 2 : 1);
+        st = kv4_map(&maps.v, a.kv.v, a.kv, D, a.units.pairs);
     if (st != QMD_OK)
         return st;
     cudaLaunchConfig_t cfg = {};
@@ -587,9 +472,7 @@ qmd_status launch_kv4_attention(const Kv4Params &kv, int head_dim, const float *
     Attn4Args a;
     static_cast<AttnArgs &>(a) = attn_args(kv, q, q_stride, q_heads, scale, window, out, out_stride, ws, dev);
     a.lse = lse;
-    a.ks4 = kv.ks4;
-    a.vs4 = kv.vs4;
-    a.pairs = kv.page_blocks % 2 == 0;
+    a.units = {kv.ks4, kv.vs4, kv.page_blocks % 2 == 0};
     // rows per item: the least of 4, 8, 16 that holds a sequence's rows of one key/value head
     const int64_t rows = (int64_t)a.group * kv.max_q;
     if (head_dim == 64)

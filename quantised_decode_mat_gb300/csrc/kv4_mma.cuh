@@ -20,6 +20,7 @@
 
 #include "kv4.cuh"
 #include "kv_attn.cuh"
+#include "tensor_map.h"
 
 namespace qmd {
 
@@ -250,6 +251,153 @@ __device__ __forceinline__ void load_bytes(uint32_t dst, const void *src, uint32
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                  "l"(src), "r"(bytes), "r"(bar)
                  : "memory");
+}
+
+// What a kernel over the 4-bit cache's units is given.
+struct Units4Args {
+    const __half *ks4, *vs4;
+    int pairs;  // a page holds whole units (an even number of 16-token blocks)
+};
+
+struct Maps4 {  // the pools as [block][16][head_dim / 2] bytes
+    CUtensorMap k, v;
+};
+
+// A warp's way through the units of its items: pages looked up 32 units at a time, a lane each, and copies into a
+// ring of S units of shared memory, S - 1 ahead: codes by tiled tensor copies, scales by plain bulk copies,
+// keys and (VALUES) values.  A whole warp makes every call.
+template <int D, int S, bool VALUES>
+struct Units4 {
+    using T = Tile4<D>;
+    static constexpr int KV = VALUES ? 2 : 1;
+    static constexpr int CODES = KV * T::CODES, SCALES = KV * T::SCALES;  // bytes of a stage
+    const AttnArgs &a;
+    const Units4Args &u;
+    const Maps4 &maps;
+    uint32_t ring, sring, bars;         // this warp's, in shared memory
+    uint32_t use = 0, phase = 0, put = 0;  // the stage to read next, its barrier's phase; the stage to ask for next
+    int seq = 0, head = 0, lo = 0, hi = 0, first = 0, count = 0;
+    int2 now, later;                    // the units' two blocks in the pool, or -1: of this chunk of 32, and of the next
+
+    __device__ __forceinline__ int block_of(int blk) const
+    {
+        if (blk < lo || blk >= hi)
+            return -1;
+        const int col = blk / a.by_blocks, page = a.kv.table[seq * a.kv.table_stride + col];
+        if (page < 0 || page >= a.kv.pages) {
+            kv_index_error(a.kv);
+            return -1;
+        }
+        return (page * a.kv.heads + head - col) * a.kv.page_blocks + blk;
+    }
+    __device__ __forceinline__ int2 look_up(int i) const
+    {
+        int2 b = make_int2(-1, -1);
+        if (i < count) {
+            const int blk = first + 2 * i;
+            if (u.pairs) {  // both blocks lie in one page, whichever of them is seen
+                const int seen = max(blk, lo);
+                b.x = block_of(seen);
+                if (b.x >= 0)
+                    b.x -= seen - blk;
+                b.y = b.x >= 0 ? b.x + 1 : -1;
+            } else {
+                b.x = block_of(blk);
+                b.y = block_of(blk + 1);
+            }
+        }
+        return b;
+    }
+    __device__ __forceinline__ void ask(int i, int x, int y)  // for the item's i-th unit, blocks x and y
+    {
+        if (i < count && (threadIdx.x & 31) == 0) {
+            constexpr int HC = T::CODES / 2, HS = T::SCALES / 2;
+            const uint32_t dst = ring + put * CODES, sdst = sring + put * SCALES, bar = bars + 8 * put;
+            mbar_arrive_expect_tx(bar, (x >= 0 ? KV * (HC + HS) : 0) + (y >= 0 ? KV * (HC + HS) : 0));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int b = h ? y : x;
+                if (b < 0 || (h && u.pairs))
+                    continue;
+                const uint32_t bytes = u.pairs ? 2 * HS : HS;
+                load_tile(dst + h * HC, &maps.k, 0, b, bar);
+                load_bytes(sdst + h * HS, u.ks4 + (int64_t)b * (HS / 2), bytes, bar);
+                if constexpr (VALUES) {
+                    load_tile(dst + T::CODES + h * HC, &maps.v, 0, b, bar);
+                    load_bytes(sdst + T::SCALES + h * HS, u.vs4 + (int64_t)b * (HS / 2), bytes, bar);
+                }
+            }
+        }
+        put = put + 1 == S ? 0 : put + 1;
+    }
+    // An item's units: `count` of them from 16-token block `first` (even) on, of which [lo, hi) are seen.
+    __device__ __forceinline__ void begin(int seq_, int head_, int lo_, int hi_, int first_, int count_)
+    {
+        seq = seq_, head = head_, lo = lo_, hi = hi_, first = first_, count = count_;
+        now = look_up(threadIdx.x & 31);
+        later = make_int2(-1, -1);
+        put = use;
+        fence_proxy_async_smem();
+        __syncwarp();  // every lane has read the last item's stages
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i)
+            ask(i, __shfl_sync(0xffffffffu, now.x, i), __shfl_sync(0xffffffffu, now.y, i));
+    }
+    // Ask for the unit S - 1 ahead, and wait for unit i, whose blocks are x and y; false if it did not come in time.
+    __device__ __forceinline__ bool next(int i, int &x, int &y)
+    {
+        if ((i & 31) == 16 && (i | 31) + 1 < count)
+            later = look_up((i | 31) + 1 + (threadIdx.x & 31));
+        x = __shfl_sync(0xffffffffu, now.x, i & 31), y = __shfl_sync(0xffffffffu, now.y, i & 31);
+        fence_proxy_async_smem();
+        __syncwarp();  // every lane has read the stage that is asked for again
+        const int j = i + S - 1;
+        const bool chunk = (j ^ i) & 32;
+        ask(j, __shfl_sync(0xffffffffu, chunk ? later.x : now.x, j & 31), __shfl_sync(0xffffffffu, chunk ? later.y : now.y, j & 31));
+        if ((i & 31) == 31)
+            now = later;
+        return __all_sync(0xffffffffu, mbar_wait_bounded(bars + 8 * use, phase, a.wait_ns));
+    }
+    __device__ __forceinline__ void advance()
+    {
+        use = use + 1 == S ? 0 : use + 1;
+        phase = use == 0 ? phase ^ 1u : phase;
+    }
+    // After a wait that gave up: flag it, and wait (bounded) for the copies that may be in flight.
+    __device__ __forceinline__ void drain()
+    {
+        if ((threadIdx.x & 31) == 0) {
+            atomicOr(a.kv.err, (unsigned)ERRBIT_QMV_WAIT);
+            for (int i = 0; i < S; ++i) {
+                if (!mbar_wait_bounded(bars + 8 * use, phase, a.wait_ns)) {
+                    atomicOr(a.kv.err, (unsigned)ERRBIT_DRAIN_WAIT);
+                    break;
+                }
+                advance();
+            }
+        }
+        __syncwarp();
+    }
+};
+
+// A unit's keys, or values, as a tensor of 16-row blocks; a copy takes a unit or, where pages do not hold whole ones,
+// a block, swizzled as its rows are long.
+static inline qmd_status kv4_map(CUtensorMap *map, const void *base, const KvParams &kv, int head_dim, bool pairs)
+{
+    const TensorMapEncodeFn enc = tensor_map_encoder();
+    if (!enc)
+        return fail(QMD_ERR_LAUNCH, "cuTensorMapEncodeTiled entry point", cudaErrorNotSupported);
+    const cuuint64_t row = (cuuint64_t)head_dim / 2;
+    const cuuint64_t dim[3] = {row, KV_BLOCK, (cuuint64_t)kv.pages * kv.heads * kv.page_blocks}, str[2] = {row, row * KV_BLOCK};
+    const cuuint32_t box[3] = {(cuuint32_t)row, KV_BLOCK, pairs ? 2u : 1u}, one[3] = {1, 1, 1};
+    const CUtensorMapSwizzle swizzle = row == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                       : row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                   : CU_TENSOR_MAP_SWIZZLE_128B;
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dim, str, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? QMD_OK
+               : fail(QMD_ERR_LAUNCH, "tensor map of the 4-bit cache", cudaErrorInvalidValue);
 }
 
 }  // namespace qmd
