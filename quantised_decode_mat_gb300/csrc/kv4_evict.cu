@@ -4,13 +4,30 @@
 // largest weights stay (of equal ones the earlier); what stays moves to the front in its order.  A token moves
 // whole, codes, scales and weight, so nothing is rounded again.
 //
-// A CTA to a sequence and head.  The weight that just stays is found bit by bit, counting; then chunks of slots
-// in order: a running sum over what stays gives the places.  A token's place is never behind its slot, so a
-// chunk that is read before any of it is written disturbs none that comes after it.
+// Selection.  Weights become whole numbers in their order, kept in shared memory (those past CAP are read again).
+// The number that just stays is found by three histograms, of 11, 11 and 10 bits, each over the numbers
+// that agree with what was found so far; it ends early when a bin is taken whole.  A warp whose lanes hit one bin (weights of zero)
+// adds once.
+//
+// Moving.  Windows of slots in order: ballots give each warp its counts, one scan over the warps the places.  A
+// token's place is never behind its slot, and places and slots both rise, so a token may be written once all that
+// come before it have been read: a round of tokens is read, the CTA meets, the round is written; the next
+// round's reads may pass these writes.
+//
+// Split.  Four CTAs to a sequence and head, a cluster: each selects for itself, and moves its part of every row
+// (half of the keys' bytes or of the values'), which lies in nobody else's way.  Weights, which all four have
+// to have read, are moved by one of them, after a barrier of the cluster for each window.
+//
+// Bound: latency (some ten dependent steps), and for few sequences what their few SMs move.
+#include <mutex>
+#include <set>
+#include <type_traits>
+
 #include <cuda_runtime.h>
 
 #include "internal.h"
 #include "kv4.cuh"
+#include "kv_attn.cuh"
 #include "ptx.cuh"
 
 namespace qmd {
@@ -19,10 +36,15 @@ struct Evict4Args {
     Kv4Params kv;
     float *weight;
     int keep, sinks, recent;
+    int cap;  // weights that shared memory holds
+    FastDiv by_tokens;
     int32_t *len_out, *kept;
 };
 
-constexpr int EVICT_THREADS = 512;
+constexpr int EVICT_PARTS = 4;   // CTAs to a sequence and head
+constexpr int EVICT_BINS = 2048;
+constexpr int EVICT_STEPS = 8;   // times 32 slots of a warp in a window
+constexpr int EVICT_CAP = 32768;
 
 // Weights as whole numbers in their order: -0 as 0, NaN below everything.
 __device__ __forceinline__ unsigned weight_key(float w)
@@ -33,38 +55,34 @@ __device__ __forceinline__ unsigned weight_key(float w)
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Sum over the CTA, and this thread's exclusive sum.
-__device__ __forceinline__ int block_scan(int x, int *s_sum, int *total)
+__device__ __forceinline__ int warp_scan(int x)  // inclusive
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int sum = x;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o)
-            sum += y;
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if ((threadIdx.x & 31) >= o)
+            x += y;
     }
-    __syncthreads();
-    if (lane == 31)
-        s_sum[warp] = sum;
-    __syncthreads();
-    int base = 0, all = 0;
-    for (int w = 0; w < EVICT_THREADS / 32; ++w) {
-        if (w < warp)
-            base += s_sum[w];
-        all += s_sum[w];
-    }
-    *total = all;
-    return base + sum - x;
+    return x;
 }
 
-template <int D>
-__global__ void __launch_bounds__(EVICT_THREADS) kv4_evict_kernel(const Evict4Args a)
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+template <int D, int THREADS>
+__global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
+    kv4_evict_kernel(const Evict4Args a)
 {
+    constexpr int W = THREADS / 32, WINDOW = THREADS * EVICT_STEPS;
+    extern __shared__ unsigned s_key[];  // [cap], then [WINDOW] slots that stay
+    __shared__ int s_hist[EVICT_BINS], s_sum[W], s_equal[W], s_found[3];
+    const Kv4Params &p = a.kv;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int item = blockIdx.x / EVICT_PARTS, part = blockIdx.x % EVICT_PARTS;
+    const int s = item / p.heads, head = item % p.heads;
+    int *s_src = reinterpret_cast<int *>(s_key + a.cap);
     pdl_launch_dependents();
     pdl_wait();
-    __shared__ int s_sum[EVICT_THREADS / 32], s_src[EVICT_THREADS];
-    const Kv4Params &p = a.kv;
-    const int s = blockIdx.x / p.heads, head = blockIdx.x % p.heads, tid = threadIdx.x;
     const int tokens = p.page_blocks * KV_BLOCK;
     const int32_t *table = p.table + (int64_t)s * p.table_stride;
     int len = p.len[s];
@@ -72,107 +90,237 @@ __global__ void __launch_bounds__(EVICT_THREADS) kv4_evict_kernel(const Evict4Ar
     if (!ok)
         len = 0;
     bool bad = false;
-    for (int i = tid; i < (len + tokens - 1) / tokens; i += EVICT_THREADS)
+    for (int i = tid; i < (len + tokens - 1) / a.by_tokens; i += THREADS)
         bad |= table[i] < 0 || table[i] >= p.pages;
-    bad = __syncthreads_or(bad);
-    ok = ok && !bad;
-    if (!ok && tid == 0)
-        kv_index_error(p);
-    if (head == 0 && tid == 0)
-        a.len_out[s] = ok ? min(len, a.keep) : len;
-    int32_t *kept = a.kept ? a.kept + (int64_t)blockIdx.x * a.keep : nullptr;
-    if (!ok || len <= a.keep) {
+    ok = !__syncthreads_or(bad) && ok;
+    if (part == 0 && tid == 0) {
+        if (!ok)
+            kv_index_error(p);
+        if (head == 0)
+            a.len_out[s] = ok ? min(len, a.keep) : len;
+    }
+    int32_t *kept = a.kept && part == 0 ? a.kept + (int64_t)item * a.keep : nullptr;
+    if (!ok || len <= a.keep) {  // the same for the whole cluster
         if (kept)
-            for (int i = tid; i < a.keep; i += EVICT_THREADS)
+            for (int i = tid; i < a.keep; i += THREADS)
                 kept[i] = ok && i < len ? i : -1;
         return;
     }
-    auto token = [&](int j) { return kv4_token(p, table[j / tokens], head, j); };
-    const int need = a.keep - a.sinks - a.recent, m0 = a.sinks, m1 = len - a.recent;
-    // the largest key that at least `need` have or pass
-    unsigned key = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-        const unsigned with = key | 1u << bit;
-        int n = 0, total;
-        for (int j = m0 + tid; j < m1; j += EVICT_THREADS)
-            n += weight_key(a.weight[token(j)]) >= with;
-        block_scan(n, s_sum, &total);
-        if (total >= need)
-            key = with;
-    }
-    int above = 0;
-    {
-        int n = 0;
-        for (int j = m0 + tid; j < m1; j += EVICT_THREADS)
-            n += weight_key(a.weight[token(j)]) > key;
-        block_scan(n, s_sum, &above);
-    }
-    int equal_left = need - above, place = 0;
-    for (int j0 = 0; j0 < len; j0 += EVICT_THREADS) {
-        const int j = j0 + tid;
-        bool stay = j < len && (j < m0 || j >= m1), equal = false;
-        if (j >= m0 && j < m1) {
-            const unsigned k = weight_key(a.weight[token(j)]);
-            stay = k > key;
-            equal = k == key;
-        }
-        int total;
-        const int before = block_scan(equal, s_sum, &total);
-        if (equal && before < equal_left)
-            stay = true;
-        equal_left = max(0, equal_left - total);
-        const int at = block_scan(stay, s_sum, &total);
-        __syncthreads();
-        if (stay)
-            s_src[at] = j;
-        __syncthreads();
-        if (kept)
-            for (int i = tid; i < total; i += EVICT_THREADS)
-                kept[place + i] = s_src[i];
-        // words of a token: codes of K and V, their scales, the weight
-        constexpr int C = D / 8, S = D / 64, W = 2 * C + 2 * S + 1;
-        for (int i0 = 0; i0 < total * W; i0 += EVICT_THREADS) {
-            const int i = i0 + tid;
-            uint32_t *to = nullptr, x = 0;
-            if (i < total * W) {
-                const int w = i % W;
-                const int64_t src = token(s_src[i / W]), dst = token(place + i / W);
-                auto word = [&](int64_t t) {
-                    return w < C           ? reinterpret_cast<uint32_t *>(p.k) + t * C + w
-                           : w < 2 * C     ? reinterpret_cast<uint32_t *>(p.v) + t * C + w - C
-                           : w < 2 * C + S ? reinterpret_cast<uint32_t *>(p.ks4) + t * S + w - 2 * C
-                           : w < W - 1     ? reinterpret_cast<uint32_t *>(p.vs4) + t * S + w - 2 * C - S
-                                           : reinterpret_cast<uint32_t *>(a.weight) + t;
-                };
-                to = word(dst);
-                x = *word(src);
+    auto token = [&](int j) {
+        const int col = j / a.by_tokens;
+        return ((int64_t)table[col] * p.heads + head - col) * tokens + j;
+    };
+
+    // ---- which weight just stays -----------------------------------------------------------------
+    for (int j = tid; j < min(len, a.cap); j += THREADS)
+        s_key[j] = weight_key(a.weight[token(j)]);
+    __syncthreads();
+    auto key_of = [&](int j) { return j < a.cap ? s_key[j] : weight_key(a.weight[token(j)]); };
+    const int m0 = a.sinks, m1 = len - a.recent;
+    int need = a.keep - a.sinks - a.recent;  // of slots [m0, m1)
+    unsigned above = 0xffffffffu, equal = 0;  // keys from `above` on stay, and the first `need` that are `equal`
+    if (need > 0) {
+        unsigned prefix = 0;
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+            for (int i = tid; i < EVICT_BINS; i += THREADS)
+                s_hist[i] = 0;
+            __syncthreads();
+            for (int j0 = m0; j0 < m1; j0 += THREADS) {
+                const int j = j0 + tid;
+                const unsigned k = j < m1 ? key_of(j) : 0;
+                const bool in = j < m1 && (pass == 0 || k >> (shift + bits) == prefix);
+                const unsigned who = __ballot_sync(0xffffffffu, in);
+                if (!in)
+                    continue;
+                const int bin = (1 << bits) - 1 - (int)(k >> shift & ((1u << bits) - 1));  // larger keys first
+                int one;
+                __match_all_sync(who, bin, &one);
+                if (!one)
+                    atomicAdd(&s_hist[bin], 1);
+                else if (lane == __ffs(who) - 1)
+                    atomicAdd(&s_hist[bin], __popc(who));
             }
             __syncthreads();
-            if (to)
-                *to = x;
+            // the bin in which the need-th lies: a scan over threads of EVICT_BINS / THREADS bins each
+            constexpr int E = EVICT_BINS / THREADS;
+            int h[E], sum = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                sum += h[e] = s_hist[tid * E + e];
+            const int inc = warp_scan(sum);
+            if (lane == 31)
+                s_sum[warp] = inc;
+            __syncthreads();
+            const int others = warp_scan(lane < W ? s_sum[lane < W ? lane : 0] : 0);
+            int before = inc - sum + (warp ? __shfl_sync(0xffffffffu, others, warp - 1) : 0);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (before < need && need <= before + h[e]) {
+                    s_found[0] = (1 << bits) - 1 - (tid * E + e);
+                    s_found[1] = need - before;
+                    s_found[2] = h[e];
+                }
+                before += h[e];
+            }
+            __syncthreads();
+            prefix = prefix << bits | (unsigned)s_found[0];
+            need = s_found[1];
+            above = prefix << shift;
+            if (need == s_found[2]) {  // the bin stays whole
+                need = 0;
+                break;
+            }
+            if (pass == 2)
+                equal = above++;
+        }
+    }
+
+    // ---- what stays, window by window, and its move ------------------------------------------------
+    constexpr int PP = D / 64;                 // 16-byte pieces of a row in this part
+    const bool is_v = part & 1;
+    uint4 *codes = reinterpret_cast<uint4 *>(is_v ? p.v : p.k) + (part >> 1) * PP;
+    using Scales = std::conditional_t<D == 64, uint32_t, std::conditional_t<D == 128, uint2, uint4>>;
+    Scales *scales = reinterpret_cast<Scales *>(is_v ? p.vs4 : p.ks4);
+    const bool moves_scales = part < 2, moves_weights = part == 3;
+    int place = 0;
+    for (int w0 = 0; w0 < len; w0 += WINDOW) {
+        unsigned stay[EVICT_STEPS], same[EVICT_STEPS];
+        int n_stay = 0, n_same = 0;
+        const int j0 = w0 + warp * (32 * EVICT_STEPS) + lane;
+#pragma unroll
+        for (int i = 0; i < EVICT_STEPS; ++i) {
+            const int j = j0 + 32 * i;
+            bool in = j < len, eq = false;
+            if (j >= m0 && j < m1) {
+                const unsigned k = key_of(j);
+                in = k >= above;
+                eq = need > 0 && k == equal;
+            }
+            stay[i] = __ballot_sync(0xffffffffu, in);
+            same[i] = __ballot_sync(0xffffffffu, eq);
+            n_stay += __popc(stay[i]);
+            n_same += __popc(same[i]);
+        }
+        __syncthreads();  // the last window's list and sums are read
+        if (lane == 0)
+            s_sum[warp] = n_stay, s_equal[warp] = n_same;
+        __syncthreads();
+        const int their_same = lane < W ? s_equal[lane < W ? lane : 0] : 0;
+        const int same_before = warp_scan(their_same) - their_same;
+        const int take = max(0, min(their_same, need - same_before));
+        const int theirs = (lane < W ? s_sum[lane < W ? lane : 0] : 0) + take;
+        const int upto = warp_scan(theirs);
+        const int total = __shfl_sync(0xffffffffu, upto, 31);
+        int at = __shfl_sync(0xffffffffu, upto - theirs, warp), left = __shfl_sync(0xffffffffu, take, warp);
+        need -= __shfl_sync(0xffffffffu, warp_scan(take), 31);
+#pragma unroll
+        for (int i = 0; i < EVICT_STEPS; ++i) {
+            unsigned mine = stay[i], eq = same[i];
+            const int n = min(left, __popc(eq));
+            left -= n;
+            for (int drop = __popc(eq) - n; drop > 0; --drop)
+                eq &= ~(0x80000000u >> __clz(eq));  // the first n of them
+            mine |= eq;
+            if (mine >> lane & 1)
+                s_src[at + __popc(mine & ((1u << lane) - 1))] = j0 + 32 * i;
+            at += __popc(mine);
         }
         __syncthreads();
+        cluster_arrive();  // this window's weights are read
+        if (kept)
+            for (int i = tid; i < total; i += THREADS)
+                kept[place + i] = s_src[i];
+        for (int i0 = 0; i0 < total; i0 += THREADS) {
+            const int n = min(THREADS, total - i0);
+            if (s_src[i0 + n - 1] == place + i0 + n - 1)  // all of them are where they stay
+                continue;
+            uint4 x[PP];
+            int64_t to[PP];
+#pragma unroll
+            for (int e = 0; e < PP; ++e) {
+                const int i = (tid + e * THREADS) / PP, piece = (tid + e * THREADS) % PP;
+                to[e] = -1;
+                if (i < n) {
+                    to[e] = token(place + i0 + i) * (D / 32) + piece;
+                    x[e] = codes[token(s_src[i0 + i]) * (D / 32) + piece];
+                }
+            }
+            Scales d;
+            int64_t d_to = -1;
+            if (moves_scales && tid < n) {
+                d_to = token(place + i0 + tid);
+                d = scales[token(s_src[i0 + tid])];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < PP; ++e)
+                if (to[e] >= 0)
+                    codes[to[e]] = x[e];
+            if (d_to >= 0)
+                scales[d_to] = d;
+        }
+        cluster_wait();
+        if (moves_weights)
+            for (int i0 = 0; i0 < total; i0 += THREADS) {
+                const bool in = i0 + tid < total;
+                const float x = in ? a.weight[token(s_src[in ? i0 + tid : 0])] : 0.0f;
+                __syncthreads();
+                if (in)
+                    a.weight[token(place + i0 + tid)] = x;
+            }
         place += total;
     }
 }
 
-qmd_status launch_kv4_evict(const Kv4Params &kv, int head_dim, float *weight, int keep, int sinks, int recent,
-                            int32_t *len_out, int32_t *kept, const DeviceInfo &dev, cudaStream_t s)
+template <int D, int THREADS>
+static qmd_status launch_evict4(Evict4Args a, cudaStream_t s)
 {
-    const Evict4Args a = {kv, weight, keep, sinks, recent, len_out, kept};
+    // shared memory for as many weights as the page table's columns can hold, up to EVICT_CAP
+    const int64_t most = a.kv.table_stride * a.kv.page_blocks * KV_BLOCK;
+    a.cap = (int)(most < EVICT_CAP ? most : EVICT_CAP);
+    const size_t smem = ((size_t)a.cap + THREADS * EVICT_STEPS) * 4;
+    if (smem > 40 * 1024) {
+        static std::mutex mu;
+        static std::set<int> opted;
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess)
+            return QMD_ERR_DEVICE;
+        std::lock_guard<std::mutex> lock(mu);
+        if (!opted.count(dev)) {
+            const cudaError_t e = cudaFuncSetAttribute(kv4_evict_kernel<D, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       (EVICT_CAP + THREADS * EVICT_STEPS) * 4);
+            if (e != cudaSuccess)
+                return fail(QMD_ERR_LAUNCH, "kv4_evict smem attribute", e);
+            opted.insert(dev);
+        }
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(kv.seqs * kv.heads));
-    cfg.blockDim = dim3(EVICT_THREADS);
+    cfg.gridDim = dim3((unsigned)(a.kv.seqs * a.kv.heads * EVICT_PARTS));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (launch_flags() & LAUNCH_NO_PDL) ? 0 : 1;
-    const cudaError_t e = head_dim == 64    ? cudaLaunchKernelEx(&cfg, kv4_evict_kernel<64>, a)
-                          : head_dim == 128 ? cudaLaunchKernelEx(&cfg, kv4_evict_kernel<128>, a)
-                                            : cudaLaunchKernelEx(&cfg, kv4_evict_kernel<256>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_evict_kernel<D, THREADS>, a);
     return e == cudaSuccess ? QMD_OK : fail(QMD_ERR_LAUNCH, "kv4_evict launch", e);
+}
+
+qmd_status launch_kv4_evict(const Kv4Params &kv, int head_dim, float *weight, int keep, int sinks, int recent,
+                            int32_t *len_out, int32_t *kept, const DeviceInfo &dev, cudaStream_t s)
+{
+    const int tokens = kv.page_blocks * KV_BLOCK;
+    const Evict4Args a = {kv, weight, keep, sinks, recent, 0, fast_div((unsigned)tokens), len_out, kept};
+    // short tables: small CTAs, many to an SM
+    const bool small = kv.table_stride * tokens <= 4096;
+    switch (head_dim) {
+    case 64: return small ? launch_evict4<64, 256>(a, s) : launch_evict4<64, 1024>(a, s);
+    case 128: return small ? launch_evict4<128, 256>(a, s) : launch_evict4<128, 1024>(a, s);
+    default: return small ? launch_evict4<256, 256>(a, s) : launch_evict4<256, 1024>(a, s);
+    }
 }
 
 }  // namespace qmd
