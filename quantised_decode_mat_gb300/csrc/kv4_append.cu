@@ -158,7 +158,7 @@ template <int D>
 __global__ void __launch_bounds__(APP_WARPS * 32) kv4_read_kernel(const Read4Args a)
 {
     using H = HeadLanes<D>;
-    constexpr int E = H::E, N = H::RN;
+    constexpr int E = H::E, N = H::QN;
     __shared__ KvRow s_row[APP_CHUNK];
     __shared__ int s_order[APP_CHUNK], s_count;
     pdl_launch_dependents();
@@ -222,7 +222,7 @@ qmd_status launch_kv4_read(const Kv4Params &kv, int head_dim, float *k, int64_t 
 {
     const Read4Args a = {kv, k, v, k_stride, v_stride};
     const int64_t rows = kv.rows < APP_CHUNK ? kv.rows : APP_CHUNK;
-    const int64_t tasks = rows * 2 * ((kv.heads * head_dim + 511) / 512);
+    const int64_t tasks = rows * 2 * ((kv.heads * head_dim + 1023) / 1024);
     return head_dim == 64    ? launch_chunks(kv4_read_kernel<64>, a, tasks, sms, 32, 0, "kv4_read launch", s)
            : head_dim == 128 ? launch_chunks(kv4_read_kernel<128>, a, tasks, sms, 32, 0, "kv4_read launch", s)
                              : launch_chunks(kv4_read_kernel<256>, a, tasks, sms, 32, 0, "kv4_read launch", s);

@@ -38,23 +38,30 @@ struct Attn4Args : AttnArgs {
 template <int D, int R>
 struct Attn4Cfg {
     using T = Tile4<D>;
-    static constexpr int W = D == 256 ? (R == 4 ? 8 : 6) : R == 4 ? (D == 64 ? 16 : 12) : R == 8 ? 12 : D == 64 ? 12 : 8;
-    static constexpr int STAGES = D == 64 ? 4 : D == 256 || R == 16 ? 2 : 3;
-    static constexpr int RING = STAGES * 2 * T::CODES, SRING = STAGES * 2 * T::SCALES;
+    static constexpr int W = D == 256 ? (R == 4 ? 8 : 6) : R == 4 ? 16 : D == 64 ? (R == 8 ? 12 : 8) : R == 8 ? 12 : 8;
+    static constexpr int STAGES = D == 64 ? 4 : D == 256 || R != 8 ? 2 : 3;
+    static constexpr int RING = STAGES * Units4<D, STAGES, true>::STAGE;
     static constexpr int SLOT = R * D * 4;
     static constexpr bool QS = D == 256 || (D == 128 && R == 16);  // query fragments in shared memory
     static constexpr int QN = Query4<D, R>::N;
     static constexpr int QBYTES = QS ? QN * 128 : 0;
     static_assert(RING >= SLOT, "a warp's last part lies in its ring");
-    static_assert(RING % 1024 == 0, "rings begin where the swizzle does");
+    static_assert(RING % (4 * D) == 0, "rings begin where the swizzle does");
     static constexpr int BAR = 8 * STAGES;
-    static constexpr int FIXED = W * (RING + SRING + SLOT + QBYTES) + 2 * W * R * 8 + (W + 1) * 32 + W * (BAR + 8) + 8 + 16;
+    static constexpr int FIXED = W * (RING + SLOT + QBYTES + 512 + 32) + 2 * W * R * 8 + (W + 1) * 32 + W * (BAR + 8) + 8 + 16;
     static_assert(FIXED + 256 + (QMD_KV_MAX_SEQS + 1) * 4 <= 227 * 1024, "fits beside the sums of the most sequences");
 };
 
-constexpr float A4_TOP = 60000.0f;  // how large a weight times scale may get
-constexpr float A4_LOG = 14.0f;     // and (log2) may be where the reference moves
-constexpr float A4_WEIGHT = 44.0f;  // likewise a weight alone, whose limit is 2^2 above
+struct Item4 {  // what a warp needs of its item after its units
+    int row0, n;           // the sequence's first row and rows
+    int units, at, count;  // the item's units, the first of them in the warp's range, and how many
+    int rows;              // query rows
+    unsigned live;         // the sequences that have units, of up to 32
+    int pad;
+};
+
+// log2: how large a weight may get, where it may be when the reference moves, and likewise its product with a scale
+constexpr float A4_TOP = 14.9f, A4_WEIGHT = 12.0f, A4_LOG = 14.0f;
 
 // The least k with |d| < 2^k, for an f16 scale; 16 where it is not finite.
 __device__ __forceinline__ float scale4_log2(float d)
@@ -71,8 +78,10 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
     using Q = Cols4<R>;
     constexpr int W = C::W, S = C::STAGES, G = T::G, LR = Q::LR, NT = Q::NT;
     extern __shared__ __align__(1024) unsigned char smem[];
-    constexpr int SLOTS = W * C::RING, SRINGS = SLOTS + W * C::SLOT, QS0 = SRINGS + W * C::SRING;
-    float2 *s_ml = reinterpret_cast<float2 *>(smem + QS0 + W * C::QBYTES);  // [W][2][R] maximum, weight sum
+    constexpr int SLOTS = W * C::RING, QS0 = SLOTS + W * C::SLOT;
+    int2 *s_list = reinterpret_cast<int2 *>(smem + QS0 + W * C::QBYTES);    // [W][64]
+    Item4 *s_item = reinterpret_cast<Item4 *>(s_list + W * 64);             // [W]
+    float2 *s_ml = reinterpret_cast<float2 *>(s_item + W);                  // [W][2][R] maximum, weight sum
     Job *s_job = reinterpret_cast<Job *>(s_ml + 2 * W * R);                 // [1 + W]
     uint64_t *s_bar = reinterpret_cast<uint64_t *>(s_job + W + 1);          // [W][STAGES]
     int64_t *s_warp = reinterpret_cast<int64_t *>(s_bar + W * S);           // [W]
@@ -124,11 +133,14 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
     const int span = min(units - u0, per), pw = (span + W - 1) / W;
     if (tid == 0)
         s_range[0] = u0, s_range[1] = span, s_range[2] = pw, s_range[3] = per;  // (the joins read them again: registers are few in between)
+    const unsigned live = line_live(line);
+    if (lane == 0)
+        s_item[warp].live = live;
     int u = warp * pw;  // from here on counted from u0
     const int w1 = min(span, u + pw);
 
-    unsigned char *ring = smem + warp * C::RING, *sring = smem + SRINGS + warp * C::SRING;
-    Units4<D, S, true> kv = {a, a.units, maps, smem_addr(ring), smem_addr(sring), bar0};
+    Units4<D, S, true> kv = {a, a.units, maps, smem_addr(smem + warp * C::RING), bar0};
+    kv.list = s_list + warp * 64;
     uint32_t lane_at[T::LOADS];
 #pragma unroll
     for (int x = 0; x < T::LOADS; ++x)
@@ -157,9 +169,15 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
         const KvSeq sq = kv_seq(p, s);
         const Group gr = group_of<R>(a, sq, cg);
         const int lo2 = gr.lo >> 1, hi2 = (gr.hi + 1) >> 1;
-        const int nb = max(1, hi2 - lo2);
-        const int cnt = min(nb - b0, w1 - u);          // units of this item in the range
-        const int real = min(cnt, hi2 - lo2 - b0);     // those that hold slots
+        int real;  // units of this item in the range that hold slots
+        {
+            const int nb = max(1, hi2 - lo2), cnt = min(nb - b0, w1 - u);
+            real = min(cnt, hi2 - lo2 - b0);
+            __syncwarp();  // every lane has read the last item's
+            if (lane == 0)
+                s_item[warp] = {sq.row0, sq.n, nb, b0, cnt, gr.rows, s_item[warp].live};  // (registers are few in between)
+            __syncwarp();
+        }
 
         const int first_blk = 2 * (lo2 + b0);
         kv.begin(s, head, gr.lo, gr.hi, first_blk, real);
@@ -193,13 +211,12 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
                 o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
 
         for (int idx = 0; idx < real; ++idx) {
-            int bx, by;
-            if (!kv.next(idx, bx, by)) {
+            if (!kv.next(idx)) {
                 dead = true;
                 break;
             }
-            const uint32_t codes = kv.ring + kv.use * kv.CODES;
-            const unsigned char *scales = sring + kv.use * kv.SCALES;
+            const uint32_t codes = kv.stage();
+            const unsigned char *scales = smem + (codes + kv.SCALES - smem_addr(smem));
             float sc[2][LR][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -211,78 +228,74 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
 
             const int pos = (first_blk + 2 * idx) * KV_BLOCK;
             unsigned poison = 0;
-            if (pos < all_from || pos + KV4_UNIT > all_to || bx < 0 || by < 0) {
-                // some slot is not there, or not seen by some row
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int j = pos + 16 * h + 8 * e + g;
-                        bool any = false, all = true, bad = false;
-                        bool sees[LR];
-#pragma unroll
-                        for (int i = 0; i < LR; ++i) {
-                            const int end = row_end(sq, (cg * R + min(Q::row(i, t), gr.rows - 1)) / a.by_group);
-                            sees[i] = (h ? by : bx) >= 0 && j >= row_begin(a, end) && j < end;
-                            any |= sees[i];
-                            all &= sees[i];
-                            if (!sees[i])
-                                sc[h][i][e] = -INFINITY;
-                        }
-                        // a scale that is not finite must not reach rows that do not see its slot: where some of the
-                        // lane's do not, it is 0 and the others' values are made NaN below
-#pragma unroll
-                        for (int i = 0; i < G / 2; ++i) {
-                            const float2 d = halves(dv[h][e][i]);
-                            bad |= !(fabsf(d.x) <= 65504.0f && fabsf(d.y) <= 65504.0f);
-                        }
-                        if (!any || (bad && !all)) {
-#pragma unroll
-                            for (int i = 0; i < G / 2; ++i)
-                                dv[h][e][i] = 0;
-#pragma unroll
-                            for (int i = 0; i < LR; ++i)
-                                if (sees[i])
-                                    poison |= 1u << (4 * i + 2 * h + e);
-                        }
-                    }
-            }
-            // the slots' largest |scale|
-            float dm[2][2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    __half2 m = __habs2(*reinterpret_cast<const __half2 *>(&dv[h][e][0]));
-#pragma unroll
-                    for (int i = 1; i < G / 2; ++i)
-                        m = __hmax2(m, __habs2(*reinterpret_cast<const __half2 *>(&dv[h][e][i])));
-                    const float2 f = __half22float2(m);
-                    dm[h][e] = fmaxf(f.x, f.y);
-                }
-            float w[2][LR][2];
-            bool up = false;
-#pragma unroll
-            for (int i = 0; i < LR; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float x = sc[h][i][e] - ref[i];
-                        w[h][i][e] = ex2(x);
-                        up |= x > A4_WEIGHT + 2.0f || w[h][i][e] * dm[h][e] > A4_TOP;
-                    }
-            if (__any_sync(0xffffffffu, up)) {
-                float f[LR];
+            if (pos < all_from || pos + KV4_UNIT > all_to || kv.misses(idx)) {
+                const int2 at = kv.blocks(idx);
+                // some slot is not there, or not seen by some row: bit 2 h + e of these is the lane's slot (h, e)
+                unsigned any = 0, all = 15, bad = 0;
 #pragma unroll
                 for (int i = 0; i < LR; ++i) {
-                    float top = -INFINITY;
+                    const int end = row_end(sq, (cg * R + min(Q::row(i, t), gr.rows - 1)) / a.by_group) - (pos + g);
+                    const int begin = row_begin(a, end + pos + g) - (pos + g);
+                    unsigned sees = 0;
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
-                            top = fmaxf(top, sc[h][i][e] + fmaxf(dm[h][e] > 0.0f ? scale4_log2(dm[h][e]) - A4_LOG : -A4_WEIGHT,
-                                                                 -A4_WEIGHT));
+                            if ((h ? at.y : at.x) >= 0 && 16 * h + 8 * e >= begin && 16 * h + 8 * e < end)
+                                sees |= 1u << (2 * h + e);
+                            else
+                                sc[h][i][e] = -INFINITY;
+                    any |= sees;
+                    all &= sees;
+                    poison |= sees << (4 * i);
+                }
+                // a scale that is not finite must not reach rows that do not see its slot: where some of the lane's do
+                // not, it is 0 and the others' values are made NaN below
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const unsigned bit = 1u << (2 * h + e);
+#pragma unroll
+                        for (int i = 0; i < G / 2; ++i) {
+                            const uint32_t top = dv[h][e][i] & 0x7c007c00u;
+                            if ((top & 0x7c00u) == 0x7c00u || top >> 16 == 0x7c00u)
+                                bad |= bit;
+                        }
+                        if (!(any & bit) || (bad & ~all & bit))
+#pragma unroll
+                            for (int i = 0; i < G / 2; ++i)
+                                dv[h][e][i] = 0;
+                    }
+                poison &= (bad & ~all) * 0x1111u;
+            }
+            // Is a row's reference passed?  Scales under 2 need only the weights looked at.
+            unsigned all_bits = 0;
+#pragma unroll
+            for (int i = 0; i < 2 * G; ++i)
+                all_bits |= dv[i / G][i / (G / 2) & 1][i % (G / 2)];
+            bool up = all_bits & 0x40004000u;
+#pragma unroll
+            for (int i = 0; i < LR; ++i)
+                up |= fmaxf(fmaxf(sc[0][i][0], sc[0][i][1]), fmaxf(sc[1][i][0], sc[1][i][1])) - ref[i] > A4_TOP;
+            if (__any_sync(0xffffffffu, up)) {
+                float lg[2][2];  // the slots' largest |scale|: the least k with |d| < 2^k, at most 2^16
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        __half2 m = __habs2(as_half2(dv[h][e][0]));
+#pragma unroll
+                        for (int i = 1; i < G / 2; ++i)
+                            m = __hmax2(m, __habs2(as_half2(dv[h][e][i])));
+                        const float2 m2 = __half22float2(m);
+                        lg[h][e] = fmaxf(scale4_log2(fmaxf(m2.x, m2.y)) - A4_LOG, -A4_WEIGHT);
+                    }
+                float f[LR];
+#pragma unroll
+                for (int i = 0; i < LR; ++i) {
+                    float top = fmaxf(fmaxf(sc[0][i][0] + lg[0][0], sc[0][i][1] + lg[0][1]),
+                                      fmaxf(sc[1][i][0] + lg[1][0], sc[1][i][1] + lg[1][1]));
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1)
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -290,11 +303,6 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
                     f[i] = pow2(ref[i] - now);
                     ref[i] = now;
                     l[i] *= f[i];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            w[h][i][e] = ex2(sc[h][i][e] - now);
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -304,9 +312,16 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
                         for (int e = 0; e < 4; ++e)
                             o[n][i][e] *= f[R == 4 ? 0 : 2 * n + (e & 1)];
             }
+            float w[2][LR][2];
 #pragma unroll
-            for (int i = 0; i < LR; ++i)
+            for (int i = 0; i < LR; ++i) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        w[h][i][e] = ex2(sc[h][i][e] - ref[i]);
                 l[i] += (w[0][i][0] + w[0][i][1]) + (w[1][i][0] + w[1][i][1]);
+            }
             if (poison) {
 #pragma unroll
                 for (int i = 0; i < LR; ++i)
@@ -329,31 +344,30 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
                     unpack4_f16(x, v[0][i]);
                     unpack4_f16(y, v[1][i]);
                     const uint32_t first[4] = {x[0], x[1], y[0], y[1]}, second[4] = {x[2], x[3], y[2], y[3]};
-                    float d[2];
+                    uint32_t q[LR][2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float2 two = halves(dv[h][e][i / 2]);
-                        d[e] = i & 1 ? two.y : two.x;
+                        const float d = i & 1 ? two.y : two.x;
+#pragma unroll
+                        for (int j = 0; j < LR; ++j) {
+                            const float x = w[h][j][e] * d, hi = first_bits(x);
+                            q[j][e] = pack_f16(hi, x - hi);
+                        }
                     }
                     if constexpr (R == 4) {
-                        uint32_t b[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float q = w[h][0][e] * d[e], hi = first_bits(q);
-                            b[e] = transpose_8x8(pack_f16(hi, q - hi));
-                        }
-                        mma_16816(o[0][2 * i], first, b[0], b[1]);
-                        mma_16816(o[0][2 * i + 1], second, b[0], b[1]);
+                        const uint32_t b0 = transpose_8x8(q[0][0]), b1 = transpose_8x8(q[0][1]);
+                        mma_16816(o[0][2 * i], first, b0, b1);
+                        mma_16816(o[0][2 * i + 1], second, b0, b1);
                     } else {
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            uint32_t bh[2], bl[2];
+                            uint32_t bh[2], bl[2];  // the first parts of two rows, and the second
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const float q0 = w[h][(2 * n) % LR][e] * d[e], q1 = w[h][(2 * n + 1) % LR][e] * d[e];
-                                const float h0 = first_bits(q0), h1 = first_bits(q1);
-                                bh[e] = transpose_8x8(pack_f16(h0, h1));
-                                bl[e] = transpose_8x8(pack_f16(q0 - h0, q1 - h1));
+                                const uint32_t q0 = q[(2 * n) % LR][e], q1 = q[(2 * n + 1) % LR][e];
+                                bh[e] = transpose_8x8(__byte_perm(q0, q1, 0x5410));
+                                bl[e] = transpose_8x8(__byte_perm(q0, q1, 0x7632));
                             }
                             mma_16816(o[n][2 * i], first, bl[0], bl[1]);
                             mma_16816(o[n][2 * i + 1], second, bl[0], bl[1]);
@@ -371,9 +385,12 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
         }
 
         // ---- the item's part: finished, or laid down for the join --------------------------------
+        const Item4 it = s_item[warp];
+        const int row0 = it.row0, nb = it.units, cnt = it.count;
+        b0 = it.at;
         const bool done = b0 == 0 && cnt == nb;
         const int part = b0 > 0 ? 0 : 1;
-        float *dst = reinterpret_cast<float *>(part == 0 ? smem + SLOTS + warp * C::SLOT : ring);
+        float *dst = reinterpret_cast<float *>(part == 0 ? smem + SLOTS + warp * C::SLOT : smem + warp * C::RING);
         if (part == 1 && !done)
             __syncwarp();  // every lane has read the ring
 #pragma unroll
@@ -384,12 +401,12 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
             const int r = Q::row(i, t);
             if (!done && g == 0)
                 s_ml[(warp * 2 + part) * R + r] = make_float2(ref[i], l[i]);
-            if (done && r >= gr.rows)
+            if (done && r >= it.rows)
                 continue;
             if (done && a.lse && g == 0)
-                store_lse(a, sq.row0, head, cg * R + r, ref[i], l[i]);
+                store_lse(a, row0, head, cg * R + r, ref[i], l[i]);
             const float f = done ? (l[i] == 0.0f ? 0.0f : 1.0f / l[i]) : 1.0f;
-            float *to = (done ? a.out + row_offset(a, sq.row0, head, cg * R + r, a.out_stride, D) : dst + r * D) + 4 * g;
+            float *to = (done ? a.out + row_offset(a, row0, head, cg * R + r, a.out_stride, D) : dst + r * D) + 4 * g;
 #pragma unroll
             for (int j = 0; j < G; ++j) {
                 float y[4];
@@ -406,18 +423,18 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
             Job &j = s_job[part == 1 ? 1 + warp : 0];
             j.start = u - b0;
             j.end = u - b0 + nb;
-            j.row0 = sq.row0;
+            j.row0 = row0;
             j.first = cg * R;
             j.head = head;
-            j.rows = gr.rows;
+            j.rows = it.rows;
         }
         u += cnt;
         b0 = 0;
-        if (u < w1 && ++cg * R >= sq.n * a.group) {  // on to the next head, or the next sequence with rows
+        if (u < w1 && ++cg * R >= it.n * a.group) {  // on to the next head, or the next sequence with rows
             cg = 0;
             if (++head == p.heads) {
                 head = 0;
-                s = line_next(line, s, s_pre);
+                s = line_next(p, it.live, s, s_pre);
             }
         }
     }

@@ -77,7 +77,16 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[2][Tile4<D>::G], uint32
     }
 }
 
-// A word's codes, less 8, as f16 pairs: f[n] holds nibbles n and n + 4.
+// (a & b) | c in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
+// A word's codes, less 8, as f16 pairs: f[n] holds nibbles n and n + 4.  (Whole bytes by __byte_perm in place of the
+// upper nibbles, with what multiplies them adjusted, came to an instruction more a word.)
 __device__ __forceinline__ void unpack4_f16(uint32_t (&f)[4], uint32_t w)
 {
     // a nibble under the exponent of 1024 is 1024 + c, or 1024 + 16 c where it is the second
@@ -87,7 +96,7 @@ __device__ __forceinline__ void unpack4_f16(uint32_t (&f)[4], uint32_t w)
 #pragma unroll
     for (int n = 0; n < 4; n += 2) {
         const uint32_t v = n ? w >> 8 : w;
-        uint32_t x = (v & 0x000f000fu) | 0x64006400u, y = (v & 0x00f000f0u) | 0x64006400u;
+        const uint32_t x = and_or(v, 0x000f000fu, 0x64006400u), y = and_or(v, 0x00f000f0u, 0x64006400u);
         const __half2 a = __hadd2(*reinterpret_cast<const __half2 *>(&x), low);
         const __half2 b = __hfma2(*reinterpret_cast<const __half2 *>(&y), by16, high);
         f[n] = *reinterpret_cast<const uint32_t *>(&a);
@@ -113,6 +122,8 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); }
 
 // The query fragments of a warp's item: [tile][group][step of 16][part][2] registers.
 template <int D, int R>
@@ -270,14 +281,16 @@ template <int D, int S, bool VALUES>
 struct Units4 {
     using T = Tile4<D>;
     static constexpr int KV = VALUES ? 2 : 1;
-    static constexpr int CODES = KV * T::CODES, SCALES = KV * T::SCALES;  // bytes of a stage
+    // a stage: codes of keys and values, then their scales, up to where the swizzle begins anew
+    static constexpr int SCALES = KV * T::CODES, STAGE = (SCALES + KV * T::SCALES + 4 * D - 1) / (4 * D) * (4 * D);
     const AttnArgs &a;
     const Units4Args &u;
     const Maps4 &maps;
-    uint32_t ring, sring, bars;         // this warp's, in shared memory
-    uint32_t use = 0, phase = 0, put = 0;  // the stage to read next, its barrier's phase; the stage to ask for next
+    uint32_t ring, bars;          // this warp's, in shared memory
+    uint32_t use = 0, phase = 0;  // the stage to read next, its barrier's phase
     int seq = 0, head = 0, lo = 0, hi = 0, first = 0, count = 0;
-    int2 now, later;                    // the units' two blocks in the pool, or -1: of this chunk of 32, and of the next
+    int2 *list;         // of 64 units, in shared memory: their two blocks in the pool, or -1
+    unsigned gone = 0, gone_next = 0;  // of this chunk of 32 units and of the next: those that miss a block
 
     __device__ __forceinline__ int block_of(int blk) const
     {
@@ -308,56 +321,76 @@ struct Units4 {
         }
         return b;
     }
-    __device__ __forceinline__ void ask(int i, int x, int y)  // for the item's i-th unit, blocks x and y
+    __device__ __forceinline__ uint32_t stage() const { return ring + use * STAGE; }
+    // Look up 32 units from the i-th on, a lane each; those that miss a block.
+    __device__ __forceinline__ unsigned look_up_32(int i) const
     {
-        if (i < count && (threadIdx.x & 31) == 0) {
-            constexpr int HC = T::CODES / 2, HS = T::SCALES / 2;
-            const uint32_t dst = ring + put * CODES, sdst = sring + put * SCALES, bar = bars + 8 * put;
-            mbar_arrive_expect_tx(bar, (x >= 0 ? KV * (HC + HS) : 0) + (y >= 0 ? KV * (HC + HS) : 0));
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int b = h ? y : x;
-                if (b < 0 || (h && u.pairs))
-                    continue;
-                const uint32_t bytes = u.pairs ? 2 * HS : HS;
-                load_tile(dst + h * HC, &maps.k, 0, b, bar);
-                load_bytes(sdst + h * HS, u.ks4 + (int64_t)b * (HS / 2), bytes, bar);
+        const int lane = threadIdx.x & 31;
+        const int2 b = look_up(i + lane);
+        list[(i & 32) + lane] = b;
+        return __ballot_sync(0xffffffffu, b.x < 0 || b.y < 0);
+    }
+    __device__ __forceinline__ void ask(int i, uint32_t put) const  // lane 0: for the item's i-th unit, into a stage
+    {
+        constexpr int HC = T::CODES / 2, HS = T::SCALES / 2;
+        const int2 b = list[i & 63];
+        const uint32_t bar = bars + 8 * put, dst = ring + put * STAGE;
+        mbar_arrive_expect_tx(bar, (b.x >= 0 ? KV * (HC + HS) : 0) + (b.y >= 0 ? KV * (HC + HS) : 0));
+        if (u.pairs) {
+            if (b.x >= 0) {
+                load_tile(dst, &maps.k, 0, b.x, bar);
+                load_bytes(dst + SCALES, u.ks4 + (int64_t)b.x * (HS / 2), 2 * HS, bar);
                 if constexpr (VALUES) {
-                    load_tile(dst + T::CODES + h * HC, &maps.v, 0, b, bar);
-                    load_bytes(sdst + T::SCALES + h * HS, u.vs4 + (int64_t)b * (HS / 2), bytes, bar);
+                    load_tile(dst + T::CODES, &maps.v, 0, b.x, bar);
+                    load_bytes(dst + SCALES + T::SCALES, u.vs4 + (int64_t)b.x * (HS / 2), 2 * HS, bar);
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                const int one = h ? b.y : b.x;
+                if (one < 0)
+                    continue;
+                load_tile(dst + h * HC, &maps.k, 0, one, bar);
+                load_bytes(dst + SCALES + h * HS, u.ks4 + (int64_t)one * (HS / 2), HS, bar);
+                if constexpr (VALUES) {
+                    load_tile(dst + T::CODES + h * HC, &maps.v, 0, one, bar);
+                    load_bytes(dst + SCALES + T::SCALES + h * HS, u.vs4 + (int64_t)one * (HS / 2), HS, bar);
                 }
             }
         }
-        put = put + 1 == S ? 0 : put + 1;
     }
     // An item's units: `count` of them from 16-token block `first` (even) on, of which [lo, hi) are seen.
     __device__ __forceinline__ void begin(int seq_, int head_, int lo_, int hi_, int first_, int count_)
     {
         seq = seq_, head = head_, lo = lo_, hi = hi_, first = first_, count = count_;
-        now = look_up(threadIdx.x & 31);
-        later = make_int2(-1, -1);
-        put = use;
+        __syncwarp();  // every lane has read the last item's list
+        gone = look_up_32(0);
         fence_proxy_async_smem();
-        __syncwarp();  // every lane has read the last item's stages
-#pragma unroll
-        for (int i = 0; i < S - 1; ++i)
-            ask(i, __shfl_sync(0xffffffffu, now.x, i), __shfl_sync(0xffffffffu, now.y, i));
+        __syncwarp();  // the list is written, and the last item's stages are read
+        if ((threadIdx.x & 31) == 0) {
+#pragma unroll 1
+            for (int i = 0; i < min(S - 1, count); ++i)
+                ask(i, use + i < S ? use + i : use + i - S);
+        }
     }
-    // Ask for the unit S - 1 ahead, and wait for unit i, whose blocks are x and y; false if it did not come in time.
-    __device__ __forceinline__ bool next(int i, int &x, int &y)
+    // Ask for the unit S - 1 ahead, and wait for unit i; false if it did not come in time.
+    __device__ __forceinline__ bool next(int i)
     {
-        if ((i & 31) == 16 && (i | 31) + 1 < count)
-            later = look_up((i | 31) + 1 + (threadIdx.x & 31));
-        x = __shfl_sync(0xffffffffu, now.x, i & 31), y = __shfl_sync(0xffffffffu, now.y, i & 31);
+        if ((i & 15) == 0 && i > 0) {
+            if (!(i & 16))
+                gone = gone_next;
+            else if (i + 16 < count)  // half way through a chunk the next is looked up
+                gone_next = look_up_32(i + 16);
+        }
         fence_proxy_async_smem();
         __syncwarp();  // every lane has read the stage that is asked for again
-        const int j = i + S - 1;
-        const bool chunk = (j ^ i) & 32;
-        ask(j, __shfl_sync(0xffffffffu, chunk ? later.x : now.x, j & 31), __shfl_sync(0xffffffffu, chunk ? later.y : now.y, j & 31));
-        if ((i & 31) == 31)
-            now = later;
+        if ((threadIdx.x & 31) == 0 && i + S - 1 < count)
+            ask(i + S - 1, use == 0 ? S - 1 : use - 1);
         return __all_sync(0xffffffffu, mbar_wait_bounded(bars + 8 * use, phase, a.wait_ns));
     }
+    __device__ __forceinline__ bool misses(int i) const { return gone >> (i & 31) & 1; }  // a block of unit i
+    __device__ __forceinline__ int2 blocks(int i) const { return list[i & 63]; }
     __device__ __forceinline__ void advance()
     {
         use = use + 1 == S ? 0 : use + 1;

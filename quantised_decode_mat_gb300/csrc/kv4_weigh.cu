@@ -29,10 +29,10 @@ template <int D, int R>
 struct Weigh4Cfg {
     using T = Tile4<D>;
     static constexpr int W = D == 256 ? (R == 4 ? 12 : 8) : R == 4 || D == 64 ? 16 : R == 8 ? 12 : 8;
-    static constexpr int STAGES = 4;
-    static constexpr int RING = STAGES * T::CODES, SRING = STAGES * T::SCALES;
-    static constexpr int FIXED = W * (RING + SRING) + W * (8 * STAGES + 8);
-    static_assert(RING % 1024 == 0, "rings begin where the swizzle does");
+    static constexpr int STAGES = D == 256 ? 3 : 4;
+    static constexpr int RING = STAGES * Units4<D, STAGES, false>::STAGE;
+    static constexpr int FIXED = W * (RING + 512) + W * (8 * STAGES + 8);
+    static_assert(RING % (4 * D) == 0, "rings begin where the swizzle does");
     static_assert(FIXED + 256 + (QMD_KV_MAX_SEQS + 1) * 4 <= 227 * 1024, "fits beside the sums of the most sequences");
 };
 
@@ -45,7 +45,8 @@ __global__ void __launch_bounds__(Weigh4Cfg<D, R>::W * 32, 1)
     using Q = Cols4<R>;
     constexpr int W = C::W, S = C::STAGES, LR = Q::LR;
     extern __shared__ __align__(1024) unsigned char smem[];
-    uint64_t *s_bar = reinterpret_cast<uint64_t *>(smem + W * (C::RING + C::SRING));  // [W][STAGES]
+    int2 *s_list = reinterpret_cast<int2 *>(smem + W * C::RING);  // [W][64]
+    uint64_t *s_bar = reinterpret_cast<uint64_t *>(s_list + W * 64);  // [W][STAGES]
     int64_t *s_warp = reinterpret_cast<int64_t *>(s_bar + W * S);                     // [W]
     int *s_pre = reinterpret_cast<int *>(s_warp + W);                                 // [seqs + 1]
 
@@ -88,13 +89,14 @@ __global__ void __launch_bounds__(Weigh4Cfg<D, R>::W * 32, 1)
     int u = (int)u64;
     const int w1 = (int)min((int64_t)units, u64 + pw);
 
-    unsigned char *sring = smem + W * C::RING + warp * C::SRING;
-    Units4<D, S, false> kv = {a, a.units, maps, smem_addr(smem + warp * C::RING), smem_addr(sring), bar0};
+    Units4<D, S, false> kv = {a, a.units, maps, smem_addr(smem + warp * C::RING), bar0};
+    kv.list = s_list + warp * 64;
     uint32_t lane_at[T::LOADS];
 #pragma unroll
     for (int x = 0; x < T::LOADS; ++x)
         lane_at[x] = T::at(lane, x);
 
+    const unsigned live = line_live(line);
     int pre, count;
     int s = line_find(line, p, u, s_pre, &pre, &count);
     const int of_head = count / a.by_heads;
@@ -120,24 +122,24 @@ __global__ void __launch_bounds__(Weigh4Cfg<D, R>::W * 32, 1)
             const int all_from = row_begin(a, row_end(sq, (cg * R + rows - 1) / a.by_group));
 
             for (int idx = 0; idx < cnt; ++idx) {
-                int bx, by;
-                if (!kv.next(idx, bx, by)) {
+                if (!kv.next(idx)) {
                     kv.drain();
                     return;
                 }
                 const int pos = (first_blk + 2 * idx) * KV_BLOCK;
                 // this lane's slot: that of h = t >> 1, e = t & 1
-                const int mine = pos + 16 * (t >> 1) + 8 * (t & 1) + g, blk = t >> 1 ? by : bx;
+                const int mine = pos + 16 * (t >> 1) + 8 * (t & 1) + g, blk = t >> 1 ? kv.blocks(idx).y : kv.blocks(idx).x;
                 float *at = a.weight + (int64_t)max(blk, 0) * KV_BLOCK + 8 * (t & 1) + g;
                 const bool here = blk >= 0 && mine < sq.len && mine >= lo * KV_BLOCK;
                 const float old = here && (cg > 0 || mine < own) ? *at : 0.0f;
 
+                const uint32_t codes = kv.stage();
+                const unsigned char *scales = smem + (codes + kv.SCALES - smem_addr(smem));
                 float sum[2][2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float sc[LR][2];
-                    scores4<D, R>(sc, kv.ring + kv.use * kv.CODES + h * 16 * T::ROW,
-                                  sring + kv.use * kv.SCALES + h * 16 * T::G * 2, lane_at, query, qf.scale);
+                    scores4<D, R>(sc, codes + h * 16 * T::ROW, scales + h * 16 * T::G * 2, lane_at, query, qf.scale);
                     const bool whole = pos >= all_from && pos + KV4_UNIT <= all_to;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -173,7 +175,7 @@ __global__ void __launch_bounds__(Weigh4Cfg<D, R>::W * 32, 1)
         b0 = 0;
         if (u < w1 && ++head == p.heads) {
             head = 0;
-            s = line_next(line, s, s_pre);
+            s = line_next(p, live, s, s_pre);
         }
     }
 }

@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
     };
     const UnitLine line = unit_line<W>(p, units_of, s_warp, s_pre);
     const int units = line.units;
+    const unsigned live = line_live(line);
     if (line.too_many) {  // more blocks than a launch counts
         kv_index_error(p);
         return;
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(AttnCfg<D, R>::W * 32, 1)
             cg = 0;
             if (++head == p.heads) {
                 head = 0;
-                s = line_next(line, s, s_pre);
+                s = line_next(p, live, s, s_pre);
             }
         }
     }

@@ -225,11 +225,14 @@ __device__ __forceinline__ int line_find(const UnitLine &l, const KvParams &p, i
     return lo;
 }
 
+// Up to 32 sequences: those that have units.
+__device__ __forceinline__ unsigned line_live(const UnitLine &l) { return __ballot_sync(0xffffffffu, l.units_of > 0); }
+
 // The next sequence with units after s (there is one).
-__device__ __forceinline__ int line_next(const UnitLine &l, int s, const int *s_pre)
+__device__ __forceinline__ int line_next(const KvParams &p, unsigned live, int s, const int *s_pre)
 {
-    if (l.few)
-        return __ffs(__ballot_sync(0xffffffffu, l.units_of > 0) & ~((2u << s) - 1)) - 1;
+    if (p.seqs <= 32)
+        return __ffs(live & ~((2u << s) - 1)) - 1;
     do
         ++s;
     while (s_pre[s + 1] == s_pre[s]);
