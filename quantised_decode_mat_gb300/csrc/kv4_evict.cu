@@ -6,17 +6,16 @@
 //
 // Selection.  Weights become whole numbers in their order, kept in shared memory (those past CAP are read again).
 // The number that just stays is found by three histograms, of 11, 11 and 10 bits, each over the numbers
-// that agree with what was found so far; it ends early when a bin is taken whole.  A warp whose lanes hit one bin (weights of zero)
-// adds once.
+// that agree with what was found so far; it ends early when a bin is taken whole.
 //
-// Moving.  Windows of slots in order: ballots give each warp its counts, one scan over the warps the places.  A
-// token's place is never behind its slot, and places and slots both rise, so a token may be written once all that
-// come before it have been read: a round of tokens is read, the CTA meets, the round is written; the next
-// round's reads may pass these writes.
+// Moving.  A window of slots at a time (all of them, where the list of what stays fits): ballots give each warp its
+// counts, one scan over the warps the places, and a second round of ballots the list.  A token's place is never behind
+// its slot, and places and slots both rise, so a token may be written once all that come before it have been
+// read: a round of tokens is read, the CTA meets, the round is written; the next round's reads may pass these writes.
 //
 // Split.  Four CTAs to a sequence and head, a cluster: each selects for itself, and moves its part of every row
 // (half of the keys' bytes or of the values'), which lies in nobody else's way.  Weights, which all four have
-// to have read, are moved by one of them, after a barrier of the cluster for each window.
+// to have read, are moved by one of them, after a barrier of the cluster in each window.
 //
 // Bound: latency (some ten dependent steps), and for few sequences what their few SMs move.
 #include <mutex>
@@ -36,14 +35,14 @@ struct Evict4Args {
     Kv4Params kv;
     float *weight;
     int keep, sinks, recent;
-    int cap;  // weights that shared memory holds
+    int cap, list;  // weights, and slots that stay, that shared memory holds (multiples of 16)
     FastDiv by_tokens;
     int32_t *len_out, *kept;
 };
 
 constexpr int EVICT_PARTS = 4;   // CTAs to a sequence and head
 constexpr int EVICT_BINS = 2048;
-constexpr int EVICT_STEPS = 8;   // times 32 slots of a warp in a window
+constexpr int EVICT_LIST = 8192; // slots that stay, of a window
 constexpr int EVICT_CAP = 32768;
 
 // Weights as whole numbers in their order: -0 as 0, NaN below everything.
@@ -73,8 +72,8 @@ template <int D, int THREADS>
 __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
     kv4_evict_kernel(const Evict4Args a)
 {
-    constexpr int W = THREADS / 32, WINDOW = THREADS * EVICT_STEPS;
-    extern __shared__ unsigned s_key[];  // [cap], then [WINDOW] slots that stay
+    constexpr int W = THREADS / 32;
+    extern __shared__ __align__(16) unsigned s_key[];  // [cap], then [list] slots that stay
     __shared__ int s_hist[EVICT_BINS], s_sum[W], s_equal[W], s_found[3];
     const Kv4Params &p = a.kv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -112,8 +111,12 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
     };
 
     // ---- which weight just stays -----------------------------------------------------------------
-    for (int j = tid; j < min(len, a.cap); j += THREADS)
-        s_key[j] = weight_key(a.weight[token(j)]);
+    // four at a time (a page's tokens are a multiple of 16)
+#pragma unroll 4
+    for (int j = 4 * tid; j < min(len, a.cap); j += 4 * THREADS) {
+        const float4 w = *reinterpret_cast<const float4 *>(a.weight + token(j));
+        *reinterpret_cast<uint4 *>(s_key + j) = make_uint4(weight_key(w.x), weight_key(w.y), weight_key(w.z), weight_key(w.w));
+    }
     __syncthreads();
     auto key_of = [&](int j) { return j < a.cap ? s_key[j] : weight_key(a.weight[token(j)]); };
     const int m0 = a.sinks, m1 = len - a.recent;
@@ -126,20 +129,11 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
             for (int i = tid; i < EVICT_BINS; i += THREADS)
                 s_hist[i] = 0;
             __syncthreads();
-            for (int j0 = m0; j0 < m1; j0 += THREADS) {
-                const int j = j0 + tid;
-                const unsigned k = j < m1 ? key_of(j) : 0;
-                const bool in = j < m1 && (pass == 0 || k >> (shift + bits) == prefix);
-                const unsigned who = __ballot_sync(0xffffffffu, in);
-                if (!in)
-                    continue;
-                const int bin = (1 << bits) - 1 - (int)(k >> shift & ((1u << bits) - 1));  // larger keys first
-                int one;
-                __match_all_sync(who, bin, &one);
-                if (!one)
-                    atomicAdd(&s_hist[bin], 1);
-                else if (lane == __ffs(who) - 1)
-                    atomicAdd(&s_hist[bin], __popc(who));
+#pragma unroll 4
+            for (int j = m0 + tid; j < m1; j += THREADS) {
+                const unsigned k = key_of(j);
+                if (pass == 0 || k >> (shift + bits) == prefix)  // larger keys first
+                    atomicAdd(&s_hist[(1 << bits) - 1 - (int)(k >> shift & ((1u << bits) - 1))], 1);
             }
             __syncthreads();
             // the bin in which the need-th lies: a scan over threads of EVICT_BINS / THREADS bins each
@@ -183,24 +177,26 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
     using Scales = std::conditional_t<D == 64, uint32_t, std::conditional_t<D == 128, uint2, uint4>>;
     Scales *scales = reinterpret_cast<Scales *>(is_v ? p.vs4 : p.ks4);
     const bool moves_scales = part < 2, moves_weights = part == 3;
+    constexpr int M = (THREADS == 256 ? 4 : 2) / (D == 256 ? 2 : 1), ROUND = M * THREADS;  // rows read before they are written
+    const int window = a.keep <= a.list ? (len + 32 * W - 1) / (32 * W) * (32 * W) : a.list / (32 * W) * (32 * W);
+    const int steps = window / (32 * W);  // times 32 slots of a warp
     int place = 0;
-    for (int w0 = 0; w0 < len; w0 += WINDOW) {
-        unsigned stay[EVICT_STEPS], same[EVICT_STEPS];
+    for (int w0 = 0; w0 < len; w0 += window) {
+        const int j0 = w0 + warp * 32 * steps + lane;
+        auto stays = [&](int j, bool &same) {  // surely; or if there is room for one that is just equal
+            same = false;
+            if (j < m0 || j >= m1)
+                return j < len;
+            const unsigned k = key_of(j);
+            same = need > 0 && k == equal;
+            return k >= above;
+        };
         int n_stay = 0, n_same = 0;
-        const int j0 = w0 + warp * (32 * EVICT_STEPS) + lane;
-#pragma unroll
-        for (int i = 0; i < EVICT_STEPS; ++i) {
-            const int j = j0 + 32 * i;
-            bool in = j < len, eq = false;
-            if (j >= m0 && j < m1) {
-                const unsigned k = key_of(j);
-                in = k >= above;
-                eq = need > 0 && k == equal;
-            }
-            stay[i] = __ballot_sync(0xffffffffu, in);
-            same[i] = __ballot_sync(0xffffffffu, eq);
-            n_stay += __popc(stay[i]);
-            n_same += __popc(same[i]);
+#pragma unroll 4
+        for (int i = 0; i < steps; ++i) {
+            bool same;
+            n_stay += __popc(__ballot_sync(0xffffffffu, stays(j0 + 32 * i, same)));
+            n_same += __popc(__ballot_sync(0xffffffffu, same));
         }
         __syncthreads();  // the last window's list and sums are read
         if (lane == 0)
@@ -210,65 +206,64 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
         const int same_before = warp_scan(their_same) - their_same;
         const int take = max(0, min(their_same, need - same_before));
         const int theirs = (lane < W ? s_sum[lane < W ? lane : 0] : 0) + take;
-        const int upto = warp_scan(theirs);
+        const int upto = warp_scan(theirs), taken = warp_scan(take);
         const int total = __shfl_sync(0xffffffffu, upto, 31);
         int at = __shfl_sync(0xffffffffu, upto - theirs, warp), left = __shfl_sync(0xffffffffu, take, warp);
-        need -= __shfl_sync(0xffffffffu, warp_scan(take), 31);
-#pragma unroll
-        for (int i = 0; i < EVICT_STEPS; ++i) {
-            unsigned mine = stay[i], eq = same[i];
-            const int n = min(left, __popc(eq));
-            left -= n;
-            for (int drop = __popc(eq) - n; drop > 0; --drop)
-                eq &= ~(0x80000000u >> __clz(eq));  // the first n of them
-            mine |= eq;
+        for (int i = 0; i < steps; ++i) {
+            bool same;
+            unsigned mine = __ballot_sync(0xffffffffu, stays(j0 + 32 * i, same));
+            const unsigned eq = __ballot_sync(0xffffffffu, same);
+            const unsigned first = __ballot_sync(0xffffffffu, same && __popc(eq & ((1u << lane) - 1)) < left);
+            left -= __popc(first);
+            mine |= first;
             if (mine >> lane & 1)
                 s_src[at + __popc(mine & ((1u << lane) - 1))] = j0 + 32 * i;
             at += __popc(mine);
         }
+        need -= __shfl_sync(0xffffffffu, taken, 31);
         __syncthreads();
         cluster_arrive();  // this window's weights are read
         if (kept)
             for (int i = tid; i < total; i += THREADS)
                 kept[place + i] = s_src[i];
-        for (int i0 = 0; i0 < total; i0 += THREADS) {
-            const int n = min(THREADS, total - i0);
+        cluster_wait();
+        for (int i0 = 0; i0 < total; i0 += ROUND) {
+            const int n = min(ROUND, total - i0);
             if (s_src[i0 + n - 1] == place + i0 + n - 1)  // all of them are where they stay
                 continue;
-            uint4 x[PP];
-            int64_t to[PP];
+            uint4 x[M * PP];
+            Scales d[M];
+            float w[M];
 #pragma unroll
-            for (int e = 0; e < PP; ++e) {
+            for (int e = 0; e < M * PP; ++e) {
                 const int i = (tid + e * THREADS) / PP, piece = (tid + e * THREADS) % PP;
-                to[e] = -1;
-                if (i < n) {
-                    to[e] = token(place + i0 + i) * (D / 32) + piece;
+                if (i < n)
                     x[e] = codes[token(s_src[i0 + i]) * (D / 32) + piece];
-                }
             }
-            Scales d;
-            int64_t d_to = -1;
-            if (moves_scales && tid < n) {
-                d_to = token(place + i0 + tid);
-                d = scales[token(s_src[i0 + tid])];
+#pragma unroll
+            for (int e = 0; e < M; ++e) {
+                const int i = tid + e * THREADS;
+                if (i < n && moves_scales)
+                    d[e] = scales[token(s_src[i0 + i])];
+                if (i < n && moves_weights)
+                    w[e] = a.weight[token(s_src[i0 + i])];
             }
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < PP; ++e)
-                if (to[e] >= 0)
-                    codes[to[e]] = x[e];
-            if (d_to >= 0)
-                scales[d_to] = d;
-        }
-        cluster_wait();
-        if (moves_weights)
-            for (int i0 = 0; i0 < total; i0 += THREADS) {
-                const bool in = i0 + tid < total;
-                const float x = in ? a.weight[token(s_src[in ? i0 + tid : 0])] : 0.0f;
-                __syncthreads();
-                if (in)
-                    a.weight[token(place + i0 + tid)] = x;
+            for (int e = 0; e < M * PP; ++e) {
+                const int i = (tid + e * THREADS) / PP, piece = (tid + e * THREADS) % PP;
+                if (i < n)
+                    codes[token(place + i0 + i) * (D / 32) + piece] = x[e];
             }
+#pragma unroll
+            for (int e = 0; e < M; ++e) {
+                const int i = tid + e * THREADS;
+                if (i < n && moves_scales)
+                    scales[token(place + i0 + i)] = d[e];
+                if (i < n && moves_weights)
+                    a.weight[token(place + i0 + i)] = w[e];
+            }
+        }
         place += total;
     }
 }
@@ -279,8 +274,9 @@ static qmd_status launch_evict4(Evict4Args a, cudaStream_t s)
     // shared memory for as many weights as the page table's columns can hold, up to EVICT_CAP
     const int64_t most = a.kv.table_stride * a.kv.page_blocks * KV_BLOCK;
     a.cap = (int)(most < EVICT_CAP ? most : EVICT_CAP);
-    const size_t smem = ((size_t)a.cap + THREADS * EVICT_STEPS) * 4;
-    if (smem > 40 * 1024) {
+    a.list = (int)(most < EVICT_LIST ? (most + THREADS - 1) / THREADS * THREADS : EVICT_LIST);
+    const size_t smem = ((size_t)a.cap + a.list) * 4;
+    if (smem > 32 * 1024) {  // (48 KB with what the kernel declares itself need no asking)
         static std::mutex mu;
         static std::set<int> opted;
         int dev = 0;
@@ -289,7 +285,7 @@ static qmd_status launch_evict4(Evict4Args a, cudaStream_t s)
         std::lock_guard<std::mutex> lock(mu);
         if (!opted.count(dev)) {
             const cudaError_t e = cudaFuncSetAttribute(kv4_evict_kernel<D, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       (EVICT_CAP + THREADS * EVICT_STEPS) * 4);
+                                                       (EVICT_CAP + EVICT_LIST) * 4);
             if (e != cudaSuccess)
                 return fail(QMD_ERR_LAUNCH, "kv4_evict smem attribute", e);
             opted.insert(dev);
@@ -313,7 +309,7 @@ qmd_status launch_kv4_evict(const Kv4Params &kv, int head_dim, float *weight, in
                             int32_t *len_out, int32_t *kept, const DeviceInfo &dev, cudaStream_t s)
 {
     const int tokens = kv.page_blocks * KV_BLOCK;
-    const Evict4Args a = {kv, weight, keep, sinks, recent, 0, fast_div((unsigned)tokens), len_out, kept};
+    const Evict4Args a = {kv, weight, keep, sinks, recent, 0, 0, fast_div((unsigned)tokens), len_out, kept};
     // short tables: small CTAs, many to an SM
     const bool small = kv.table_stride * tokens <= 4096;
     switch (head_dim) {

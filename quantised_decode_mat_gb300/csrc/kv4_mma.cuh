@@ -292,7 +292,8 @@ struct Units4 {
     int2 *list;         // of 64 units, in shared memory: their two blocks in the pool, or -1
     unsigned gone = 0, gone_next = 0;  // of this chunk of 32 units and of the next: those that miss a block
 
-    __device__ __forceinline__ int block_of(int blk) const
+    // Where 16-token block blk of a sequence's head lies in the pool, or -1 if it is not in [lo, hi) or its page is bad.
+    __device__ __forceinline__ int look_up_in(int seq, int head, int lo, int hi, int blk) const
     {
         if (blk < lo || blk >= hi)
             return -1;
@@ -303,6 +304,7 @@ struct Units4 {
         }
         return (page * a.kv.heads + head - col) * a.kv.page_blocks + blk;
     }
+    __device__ __forceinline__ int block_of(int blk) const { return look_up_in(seq, head, lo, hi, blk); }
     __device__ __forceinline__ int2 look_up(int i) const
     {
         int2 b = make_int2(-1, -1);

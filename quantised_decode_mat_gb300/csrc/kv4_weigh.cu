@@ -4,11 +4,16 @@
 // heads of the key/value head of e^(s_j - lse), s_j = scale q . K_j and lse attention's.  With the log-sum-exp
 // known there is nothing to keep from one slot to the next and no value to read: half of the cache, and 8 bytes a slot.
 //
-// A unit is 32 slots of a sequence and key/value head, with all its rows.  The line of all units is cut into
-// equal ranges for one CTA per SM and its warps; a range takes its rows in groups of R = 4, 8 or 16, one after the
-// other (their keys come from L2 again), so a slot's weight is only ever touched by one warp, in one order: no atomics,
-// the same bits every time.  The scores are kv4_mma.cuh's; a lane adds its rows' weights of four slots, and
-// three exchanges leave every lane with the sum of one slot.
+// A unit is 32 slots of a sequence and key/value head, with all its rows, R = 4, 8 or 16 of them at a time.  The line of all
+// units is cut into equal ranges for the warps of one CTA per SM.  The scores are kv4_mma.cuh's; a lane adds its rows'
+// weights of four slots, and three exchanges leave every lane with the sum of one slot.
+//
+// More rows than R (TEAM: a prompt's last ones): a range belongs to a team of 2, 4 or 8 warps of a CTA, each of which
+// takes every team-th group of rows through all of it; their sums meet in shared memory, a few units at a time, and
+// are added in the groups' order.  (One warp taking the groups one after the other has its pipeline of copies and its
+// queries anew for each: 8 groups over 16010 slots 62 us.)
+//
+// Either way a slot's weight is only ever touched by one warp at a time, in one order: no atomics, the same bits every time.
 #include <climits>
 #include <mutex>
 
@@ -23,29 +28,39 @@ namespace qmd {
 struct Weigh4Args : AttnArgs {
     Units4Args units;
     float *weight;
+    int team;  // warps to a range
 };
 
-template <int D, int R>
+template <int D, int R, bool TEAM>
 struct Weigh4Cfg {
     using T = Tile4<D>;
     static constexpr int W = D == 256 ? (R == 4 ? 12 : 8) : R == 4 || D == 64 ? 16 : R == 8 ? 12 : 8;
     static constexpr int STAGES = D == 256 ? 3 : 4;
     static constexpr int RING = STAGES * Units4<D, STAGES, false>::STAGE;
-    static constexpr int FIXED = W * (RING + 512) + W * (8 * STAGES + 8);
+    static constexpr int CHUNK = 4;  // units whose sums a team's warps lay down before they are added
+    static constexpr int PART = TEAM ? CHUNK * 128 : 0;
+    static constexpr int FIXED = W * (RING + 512 + PART) + W * (8 * STAGES + 8);
     static_assert(RING % (4 * D) == 0, "rings begin where the swizzle does");
     static_assert(FIXED + 256 + (QMD_KV_MAX_SEQS + 1) * 4 <= 227 * 1024, "fits beside the sums of the most sequences");
 };
 
-template <int D, int R>
-__global__ void __launch_bounds__(Weigh4Cfg<D, R>::W * 32, 1)
+// A barrier of one of a CTA's teams of warps.
+__device__ __forceinline__ void team_barrier(int id, int warps)
+{
+    asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(warps * 32) : "memory");
+}
+
+template <int D, int R, bool TEAM>
+__global__ void __launch_bounds__(Weigh4Cfg<D, R, TEAM>::W * 32, 1)
     kv4_weigh_kernel(const Weigh4Args a, const __grid_constant__ Maps4 maps)
 {
-    using C = Weigh4Cfg<D, R>;
+    using C = Weigh4Cfg<D, R, TEAM>;
     using T = Tile4<D>;
     using Q = Cols4<R>;
     constexpr int W = C::W, S = C::STAGES, LR = Q::LR;
     extern __shared__ __align__(1024) unsigned char smem[];
-    int2 *s_list = reinterpret_cast<int2 *>(smem + W * C::RING);  // [W][64]
+    float *s_part = reinterpret_cast<float *>(smem + W * C::RING);                   // [W][CHUNK][32]
+    int2 *s_list = reinterpret_cast<int2 *>(smem + W * (C::RING + C::PART));          // [W][64]
     uint64_t *s_bar = reinterpret_cast<uint64_t *>(s_list + W * 64);  // [W][STAGES]
     int64_t *s_warp = reinterpret_cast<int64_t *>(s_bar + W * S);                     // [W]
     int *s_pre = reinterpret_cast<int *>(s_warp + W);                                 // [seqs + 1]
@@ -80,14 +95,16 @@ __global__ void __launch_bounds__(Weigh4Cfg<D, R>::W * 32, 1)
         kv_index_error(p);
         return;
     }
-    // the warps' ranges, of all CTAs: short calls spread over the SMs
-    const int units = line.units, warps = gridDim.x * W;
-    const int pw = (units + warps - 1) / warps;
-    int64_t u64 = (int64_t)(warp * (int)gridDim.x + (int)blockIdx.x) * pw;
+    // the warps' (or teams') ranges, of all CTAs: short calls spread over the SMs
+    const int team = TEAM ? a.team : 1, mate = TEAM ? warp & (team - 1) : 0;
+    const int units = line.units, ranges = gridDim.x * (W / team);
+    const int pw = (units + ranges - 1) / ranges;
+    const int64_t u64 = (int64_t)(warp / team * (int)gridDim.x + (int)blockIdx.x) * pw;
     if (u64 >= units)
         return;
     int u = (int)u64;
     const int w1 = (int)min((int64_t)units, u64 + pw);
+    bool dead = false;  // a copy did not land in time: what follows is left out
 
     Units4<D, S, false> kv = {a, a.units, maps, smem_addr(smem + warp * C::RING), bar0};
     kv.list = s_list + warp * 64;
@@ -107,69 +124,109 @@ __global__ void __launch_bounds__(Weigh4Cfg<D, R>::W * 32, 1)
         const int cnt = min(nb - b0, w1 - u);
         const int first_blk = 2 * ((lo >> 1) + b0);
         const int own = max(0, sq.len - sq.n);  // the first of the rows' own slots
-        for (int cg = 0; cg * R < sq.n * a.group; ++cg) {
-            kv.begin(s, head, lo, hi, first_blk, cnt);
+        // a slot's place among the weights, and whether it has one
+        auto place = [&](int blk, int j, int64_t &at) {
+            at = (int64_t)max(blk, 0) * KV_BLOCK + j % KV_BLOCK;
+            return blk >= 0 && j < sq.len && j >= lo * KV_BLOCK;
+        };
+        for (int cg0 = 0; cg0 * R < sq.n * a.group; cg0 += team) {
+            const int cg = cg0 + mate;
+            const bool mine = cg * R < sq.n * a.group;  // (without TEAM always)
             const int rows = min(R, sq.n * a.group - cg * R);
             Query4<D, R> qf;
-            qf.load(a.q, [&](int r) { return row_offset(a, sq.row0, head, cg * R + r, a.q_stride, D); }, rows, a.scale_log2e);
-            auto query = [&](int i) { return make_uint4(qf.f[4 * i], qf.f[4 * i + 1], qf.f[4 * i + 2], qf.f[4 * i + 3]); };
             float lse[LR];
+            if (mine && !dead) {
+                kv.begin(s, head, lo, hi, first_blk, cnt);
+                qf.load(a.q, [&](int r) { return row_offset(a, sq.row0, head, cg * R + r, a.q_stride, D); }, rows, a.scale_log2e);
 #pragma unroll
-            for (int i = 0; i < LR; ++i)
-                lse[i] = a.lse[row_offset(a, sq.row0, head, cg * R + min(Q::row(i, t), rows - 1), a.group * p.heads, 1)] *
-                         1.4426950408889634f;
+                for (int i = 0; i < LR; ++i)
+                    lse[i] = a.lse[row_offset(a, sq.row0, head, cg * R + min(Q::row(i, t), rows - 1), a.group * p.heads, 1)] *
+                             1.4426950408889634f;
+            }
+            auto query = [&](int i) { return make_uint4(qf.f[4 * i], qf.f[4 * i + 1], qf.f[4 * i + 2], qf.f[4 * i + 3]); };
             const int all_to = row_end(sq, cg * R / a.by_group);
             const int all_from = row_begin(a, row_end(sq, (cg * R + rows - 1) / a.by_group));
+            // the lane's slot of a unit is that of h = t >> 1, e = t & 1
+            const int my_slot = 16 * (t >> 1) + 8 * (t & 1) + g;
 
-            for (int idx = 0; idx < cnt; ++idx) {
-                if (!kv.next(idx)) {
-                    kv.drain();
-                    return;
-                }
-                const int pos = (first_blk + 2 * idx) * KV_BLOCK;
-                // this lane's slot: that of h = t >> 1, e = t & 1
-                const int mine = pos + 16 * (t >> 1) + 8 * (t & 1) + g, blk = t >> 1 ? kv.blocks(idx).y : kv.blocks(idx).x;
-                float *at = a.weight + (int64_t)max(blk, 0) * KV_BLOCK + 8 * (t & 1) + g;
-                const bool here = blk >= 0 && mine < sq.len && mine >= lo * KV_BLOCK;
-                const float old = here && (cg > 0 || mine < own) ? *at : 0.0f;
-
-                const uint32_t codes = kv.stage();
-                const unsigned char *scales = smem + (codes + kv.SCALES - smem_addr(smem));
-                float sum[2][2];
+            for (int c0 = 0; c0 < cnt; c0 += TEAM ? C::CHUNK : cnt) {
+                const int c1 = TEAM ? min(cnt, c0 + C::CHUNK) : cnt;
+                for (int idx = c0; idx < c1 && mine && !dead; ++idx) {
+                    if (!kv.next(idx)) {
+                        kv.drain();
+                        dead = true;
+                        break;
+                    }
+                    const int pos = (first_blk + 2 * idx) * KV_BLOCK;
+                    int64_t at;
+                    bool here = false;
+                    float old = 0.0f;
+                    if constexpr (!TEAM) {
+                        const int2 b = kv.blocks(idx);
+                        here = place(t >> 1 ? b.y : b.x, pos + my_slot, at);
+                        if (here && (cg > 0 || pos + my_slot < own))
+                            old = a.weight[at];
+                    }
+                    const uint32_t codes = kv.stage();
+                    const unsigned char *scales = smem + (codes + kv.SCALES - smem_addr(smem));
+                    float sum[2][2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float sc[LR][2];
-                    scores4<D, R>(sc, codes + h * 16 * T::ROW, scales + h * 16 * T::G * 2, lane_at, query, qf.scale);
-                    const bool whole = pos >= all_from && pos + KV4_UNIT <= all_to;
+                    for (int h = 0; h < 2; ++h) {
+                        float sc[LR][2];
+                        scores4<D, R>(sc, codes + h * 16 * T::ROW, scales + h * 16 * T::G * 2, lane_at, query, qf.scale);
+                        const bool whole = pos >= all_from && pos + KV4_UNIT <= all_to;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        sum[h][e] = 0.0f;
+                        for (int e = 0; e < 2; ++e) {
+                            sum[h][e] = 0.0f;
 #pragma unroll
-                        for (int i = 0; i < LR; ++i) {
-                            bool sees = Q::row(i, t) < rows;
-                            if (!whole) {
-                                const int j = pos + 16 * h + 8 * e + g;
-                                const int end = row_end(sq, (cg * R + min(Q::row(i, t), rows - 1)) / a.by_group);
-                                sees &= j >= row_begin(a, end) && j < end;
+                            for (int i = 0; i < LR; ++i) {
+                                bool sees = Q::row(i, t) < rows;
+                                if (!whole) {
+                                    const int j = pos + 16 * h + 8 * e + g;
+                                    const int end = row_end(sq, (cg * R + min(Q::row(i, t), rows - 1)) / a.by_group);
+                                    sees &= j >= row_begin(a, end) && j < end;
+                                }
+                                const float w = ex2(sc[i][e] - lse[i]);
+                                sum[h][e] += sees ? w : 0.0f;
                             }
-                            const float w = ex2(sc[i][e] - lse[i]);
-                            sum[h][e] += sees ? w : 0.0f;
                         }
                     }
-                }
-                kv.advance();
-                // over the four lanes of a slot, each ending with one of their four slots
-                float keep[2], give[2];
+                    kv.advance();
+                    // over the four lanes of a slot, each ending with one of their four slots
+                    float keep[2], give[2];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    keep[e] = t & 2 ? sum[1][e] : sum[0][e];
-                    give[e] = t & 2 ? sum[0][e] : sum[1][e];
-                    keep[e] += __shfl_xor_sync(0xffffffffu, give[e], 2);
+                    for (int e = 0; e < 2; ++e) {
+                        keep[e] = t & 2 ? sum[1][e] : sum[0][e];
+                        give[e] = t & 2 ? sum[0][e] : sum[1][e];
+                        keep[e] += __shfl_xor_sync(0xffffffffu, give[e], 2);
+                    }
+                    const float one = (t & 1 ? keep[1] : keep[0]) + __shfl_xor_sync(0xffffffffu, t & 1 ? keep[0] : keep[1], 1);
+                    if constexpr (TEAM)
+                        s_part[(warp * C::CHUNK + idx - c0) * 32 + my_slot] = one;
+                    else if (here)
+                        a.weight[at] = old + one;
                 }
-                const float one = (t & 1 ? keep[1] : keep[0]) + __shfl_xor_sync(0xffffffffu, t & 1 ? keep[0] : keep[1], 1);
-                if (here)
-                    *at = old + one;
+                if constexpr (TEAM) {
+                    // a warp of the team adds each unit's parts, in their order.  (One whose copies failed adds nothing.)
+                    if (dead)
+                        for (int i = 0; i < C::CHUNK; ++i)
+                            s_part[(warp * C::CHUNK + i) * 32 + lane] = 0.0f;
+                    team_barrier(warp / team, team);
+                    for (int idx = c0 + mate; idx < c1; idx += team) {
+                        const int j = (first_blk + 2 * idx) * KV_BLOCK + lane;
+                        int64_t at;
+                        if (place(kv.look_up_in(s, head, lo, hi, j / KV_BLOCK), j, at)) {
+                            float sum = cg0 > 0 || j < own ? a.weight[at] : 0.0f;
+                            for (int m = 0; m < team && (cg0 + m) * R < sq.n * a.group; ++m)
+                                sum += s_part[((warp - mate + m) * C::CHUNK + idx - c0) * 32 + lane];
+                            a.weight[at] = sum;
+                        }
+                    }
+                    team_barrier(warp / team, team);
+                }
             }
+            if (!TEAM && dead)
+                return;
         }
         u += cnt;
         b0 = 0;
@@ -180,10 +237,10 @@ __global__ void __launch_bounds__(Weigh4Cfg<D, R>::W * 32, 1)
     }
 }
 
-template <int D, int R>
+template <int D, int R, bool TEAM>
 static qmd_status launch_weigh4(const Weigh4Args &a, const DeviceInfo &dev, cudaStream_t s)
 {
-    using C = Weigh4Cfg<D, R>;
+    using C = Weigh4Cfg<D, R, TEAM>;
     const size_t smem = C::FIXED + ((size_t)a.kv.seqs + 1) * sizeof(int);
     if (smem + 256 > (size_t)dev.smem_optin)
         return QMD_ERR_SHAPE;
@@ -192,7 +249,7 @@ static qmd_status launch_weigh4(const Weigh4Args &a, const DeviceInfo &dev, cuda
         static bool opted[64] = {false};
         std::lock_guard<std::mutex> lock(mu);
         if (!opted[dev.device]) {
-            const cudaError_t e = cudaFuncSetAttribute(kv4_weigh_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            const cudaError_t e = cudaFuncSetAttribute(kv4_weigh_kernel<D, R, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                        dev.smem_optin - 256);
             if (e != cudaSuccess)
                 return fail(QMD_ERR_LAUNCH, "kv4_weigh smem attribute", e);
@@ -213,7 +270,7 @@ static qmd_status launch_weigh4(const Weigh4Args &a, const DeviceInfo &dev, cuda
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (launch_flags() & LAUNCH_NO_PDL) ? 0 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_weigh_kernel<D, R>, a, maps);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_weigh_kernel<D, R, TEAM>, a, maps);
     return e == cudaSuccess ? QMD_OK : fail(QMD_ERR_LAUNCH, "kv4_weigh launch", e);
 }
 
@@ -226,16 +283,25 @@ qmd_status launch_kv4_weigh(const Kv4Params &kv, int head_dim, const float *q, i
     a.lse = const_cast<float *>(lse);
     a.units = {kv.ks4, nullptr, kv.page_blocks % 2 == 0};
     a.weight = weight;
-    const int64_t rows = (int64_t)a.group * kv.max_q;
+    // the least of 4, 8, 16 (8 at 256 dimensions) that holds a sequence's rows of one key/value head; for more, a team
+    // of as many warps as there are groups of them, to a power of two, up to 8 (a CTA of the widest instance)
+    const int64_t rows = (int64_t)a.group * kv.max_q, most = head_dim == 256 ? 8 : 16;
+    a.team = 1;
+    while (a.team < 8 && a.team * most < rows)
+        a.team *= 2;
     if (head_dim == 64)
-        return rows <= 4   ? launch_weigh4<64, 4>(a, dev, s)
-               : rows <= 8 ? launch_weigh4<64, 8>(a, dev, s)
-                           : launch_weigh4<64, 16>(a, dev, s);
+        return rows <= 4    ? launch_weigh4<64, 4, false>(a, dev, s)
+               : rows <= 8  ? launch_weigh4<64, 8, false>(a, dev, s)
+               : rows <= 16 ? launch_weigh4<64, 16, false>(a, dev, s)
+                            : launch_weigh4<64, 16, true>(a, dev, s);
     if (head_dim == 128)
-        return rows <= 4   ? launch_weigh4<128, 4>(a, dev, s)
-               : rows <= 8 ? launch_weigh4<128, 8>(a, dev, s)
-                           : launch_weigh4<128, 16>(a, dev, s);
-    return rows <= 4 ? launch_weigh4<256, 4>(a, dev, s) : launch_weigh4<256, 8>(a, dev, s);
+        return rows <= 4    ? launch_weigh4<128, 4, false>(a, dev, s)
+               : rows <= 8  ? launch_weigh4<128, 8, false>(a, dev, s)
+               : rows <= 16 ? launch_weigh4<128, 16, false>(a, dev, s)
+                            : launch_weigh4<128, 16, true>(a, dev, s);
+    return rows <= 4   ? launch_weigh4<256, 4, false>(a, dev, s)
+           : rows <= 8 ? launch_weigh4<256, 8, false>(a, dev, s)
+                       : launch_weigh4<256, 8, true>(a, dev, s);
 }
 
 }  // namespace qmd
