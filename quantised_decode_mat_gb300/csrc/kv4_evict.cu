@@ -4,18 +4,19 @@
 // largest weights stay (of equal ones the earlier); what stays moves to the front in its order.  A token moves
 // whole, codes, scales and weight, so nothing is rounded again.
 //
-// Selection.  Weights become whole numbers in their order, kept in shared memory (those past CAP are read again).
-// The number that just stays is found by three histograms, of 11, 11 and 10 bits, each over the numbers
-// that agree with what was found so far; it ends early when a bin is taken whole.
+// Selection.  Weights become whole numbers in their order, kept in shared memory, four neighbouring slots to a thread and
+// row of them (of more slots than a block of it holds, the blocks are read again for each pass).  The number that
+// just stays is found by three histograms in shared memory, of 11, 11 and 10 bits, each over the numbers that agree
+// with what was found so far; it ends early when a bin is taken whole.
 //
-// Moving.  A window of slots at a time (all of them, where the list of what stays fits): ballots give each warp its
-// counts, one scan over the warps the places, and a second round of ballots the list.  A token's place is never behind
-// its slot, and places and slots both rise, so a token may be written once all that come before it have been
-// read: a round of tokens is read, the CTA meets, the round is written; the next round's reads may pass these writes.
+// Moving, a block of slots at a time: ballots give each warp its counts, one scan over rows and warps the places, and
+// the ballots again the list of what stays.  A token's place is never behind its slot, and places and slots both
+// rise, so a token may be written once all that come before it have been read: a round of tokens is read, the CTA
+// meets, the round is written; the next round's reads may pass these writes.
 //
 // Split.  Four CTAs to a sequence and head, a cluster: each selects for itself, and moves its part of every row
 // (half of the keys' bytes or of the values'), which lies in nobody else's way.  Weights, which all four have
-// to have read, are moved by one of them, after a barrier of the cluster in each window.
+// to have read, are moved by one of them, after a barrier of the cluster in each block.
 //
 // Bound: latency (some ten dependent steps), and for few sequences what their few SMs move.
 #include <mutex>
@@ -35,21 +36,21 @@ struct Evict4Args {
     Kv4Params kv;
     float *weight;
     int keep, sinks, recent;
-    int cap, list;  // weights, and slots that stay, that shared memory holds (multiples of 16)
+    int block;  // slots worked on together, at most 4 * ROWS * THREADS
     FastDiv by_tokens;
     int32_t *len_out, *kept;
 };
 
 constexpr int EVICT_PARTS = 4;   // CTAs to a sequence and head
 constexpr int EVICT_BINS = 2048;
-constexpr int EVICT_LIST = 8192; // slots that stay, of a window
-constexpr int EVICT_CAP = 32768;
 
-// Weights as whole numbers in their order: -0 as 0, NaN below everything.
+// Weights as whole numbers in their order: -0 as 0, NaN below everything.  (0 is no weight's key.)
+constexpr unsigned EVICT_STAYS = 0xffffffffu, EVICT_NONE = 0xfffffffeu;  // nor are these
+
 __device__ __forceinline__ unsigned weight_key(float w)
 {
     if (w != w)
-        return 0;
+        return 1;
     const unsigned b = __float_as_uint(w + 0.0f);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
@@ -68,18 +69,21 @@ __device__ __forceinline__ int warp_scan(int x)  // inclusive
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
-template <int D, int THREADS>
+// ROWS: times four keys to a thread
+template <int D, int THREADS, int ROWS>
 __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
     kv4_evict_kernel(const Evict4Args a)
 {
-    constexpr int W = THREADS / 32;
-    extern __shared__ __align__(16) unsigned s_key[];  // [cap], then [list] slots that stay
-    __shared__ int s_hist[EVICT_BINS], s_sum[W], s_equal[W], s_found[3];
+    constexpr int W = THREADS / 32, PLACES = ROWS * W;
+    extern __shared__ __align__(16) unsigned char smem[];
+    uint4 *s_key = reinterpret_cast<uint4 *>(smem);                     // of a block's slots, [block / 4]
+    uint16_t *s_src = reinterpret_cast<uint16_t *>(s_key + a.block / 4);  // those that stay, counted from the block's first
+    __shared__ int s_hist[EVICT_BINS], s_sum[W], s_found[3];
+    __shared__ int s_count[PLACES], s_place[PLACES], s_take[PLACES], s_total[2];
     const Kv4Params &p = a.kv;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, block = a.block;
     const int item = blockIdx.x / EVICT_PARTS, part = blockIdx.x % EVICT_PARTS;
     const int s = item / p.heads, head = item % p.heads;
-    int *s_src = reinterpret_cast<int *>(s_key + a.cap);
     pdl_launch_dependents();
     pdl_wait();
     const int tokens = p.page_blocks * KV_BLOCK;
@@ -111,17 +115,33 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
     };
 
     // ---- which weight just stays -----------------------------------------------------------------
-    // four at a time (a page's tokens are a multiple of 16)
-#pragma unroll 4
-    for (int j = 4 * tid; j < min(len, a.cap); j += 4 * THREADS) {
-        const float4 w = *reinterpret_cast<const float4 *>(a.weight + token(j));
-        *reinterpret_cast<uint4 *>(s_key + j) = make_uint4(weight_key(w.x), weight_key(w.y), weight_key(w.z), weight_key(w.w));
-    }
-    __syncthreads();
-    auto key_of = [&](int j) { return j < a.cap ? s_key[j] : weight_key(a.weight[token(j)]); };
     const int m0 = a.sinks, m1 = len - a.recent;
+    // slots that stay anyway have a key above all weights', those behind the last one below them
+    auto key_at = [&](int j, float w) { return j >= len ? 0u : j < m0 || j >= m1 ? EVICT_STAYS : weight_key(w); };
+    int b0 = -1;  // the block whose keys are in shared memory
+    auto load = [&](int b) {
+        if (b0 == b)
+            return;
+        b0 = b;
+        __syncthreads();  // the last one's are read
+#pragma unroll 4
+        for (int j = 4 * tid; j < block; j += 4 * THREADS) {
+            float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (b + j < len)  // (a page's tokens are a multiple of 16)
+                w = *reinterpret_cast<const float4 *>(a.weight + token(b + j));
+            s_key[j / 4] = make_uint4(key_at(b + j, w.x), key_at(b + j + 1, w.y), key_at(b + j + 2, w.z), key_at(b + j + 3, w.w));
+        }
+        __syncthreads();
+    };
+    auto rows = [&] { return (min(block, len - b0) + 4 * THREADS - 1) / (4 * THREADS); };
+    // a row's keys of this thread (behind the block's last slot there are none)
+    auto keys = [&](int r) {
+        const int i = r * THREADS + tid;
+        return 4 * i < block ? s_key[i] : make_uint4(0, 0, 0, 0);
+    };
     int need = a.keep - a.sinks - a.recent;  // of slots [m0, m1)
-    unsigned above = 0xffffffffu, equal = 0;  // keys from `above` on stay, and the first `need` that are `equal`
+    // keys from `above` on stay, and the first `need` that are `equal`
+    unsigned above = EVICT_STAYS, equal = EVICT_NONE;
     if (need > 0) {
         unsigned prefix = 0;
         for (int pass = 0; pass < 3; ++pass) {
@@ -129,11 +149,18 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
             for (int i = tid; i < EVICT_BINS; i += THREADS)
                 s_hist[i] = 0;
             __syncthreads();
-#pragma unroll 4
-            for (int j = m0 + tid; j < m1; j += THREADS) {
-                const unsigned k = key_of(j);
-                if (pass == 0 || k >> (shift + bits) == prefix)  // larger keys first
-                    atomicAdd(&s_hist[(1 << bits) - 1 - (int)(k >> shift & ((1u << bits) - 1))], 1);
+            for (int b = 0; b < len; b += block) {
+                load(b);
+                auto count = [&](unsigned k) {  // larger keys first; 0 is no weight
+                    if (k != 0 && (pass == 0 ? k != EVICT_STAYS : k >> (shift + bits) == prefix))
+                        atomicAdd(&s_hist[(1 << bits) - 1 - (int)(k >> shift & ((1u << bits) - 1))], 1);
+                };
+                const int n = rows();
+#pragma unroll 1
+                for (int r = 0; r < n; ++r) {
+                    const uint4 k = keys(r);
+                    count(k.x), count(k.y), count(k.z), count(k.w);
+                }
             }
             __syncthreads();
             // the bin in which the need-th lies: a scan over threads of EVICT_BINS / THREADS bins each
@@ -170,112 +197,145 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
         }
     }
 
-    // ---- what stays, window by window, and its move ------------------------------------------------
+    // ---- what stays, block by block, and its move ------------------------------------------------
     constexpr int PP = D / 64;                 // 16-byte pieces of a row in this part
     const bool is_v = part & 1;
     uint4 *codes = reinterpret_cast<uint4 *>(is_v ? p.v : p.k) + (part >> 1) * PP;
     using Scales = std::conditional_t<D == 64, uint32_t, std::conditional_t<D == 128, uint2, uint4>>;
     Scales *scales = reinterpret_cast<Scales *>(is_v ? p.vs4 : p.ks4);
     const bool moves_scales = part < 2, moves_weights = part == 3;
-    constexpr int M = (THREADS == 256 ? 4 : 2) / (D == 256 ? 2 : 1), ROUND = M * THREADS;  // rows read before they are written
-    const int window = a.keep <= a.list ? (len + 32 * W - 1) / (32 * W) * (32 * W) : a.list / (32 * W) * (32 * W);
-    const int steps = window / (32 * W);  // times 32 slots of a warp
+    constexpr int M = D < 256 ? 2 : 1, ROUND = M * THREADS;  // rows read before they are written
+    const unsigned below = (1u << lane) - 1;
     int place = 0;
-    for (int w0 = 0; w0 < len; w0 += window) {
-        const int j0 = w0 + warp * 32 * steps + lane;
-        auto stays = [&](int j, bool &same) {  // surely; or if there is room for one that is just equal
-            same = false;
-            if (j < m0 || j >= m1)
-                return j < len;
-            const unsigned k = key_of(j);
-            same = need > 0 && k == equal;
-            return k >= above;
-        };
-        int n_stay = 0, n_same = 0;
-#pragma unroll 4
-        for (int i = 0; i < steps; ++i) {
-            bool same;
-            n_stay += __popc(__ballot_sync(0xffffffffu, stays(j0 + 32 * i, same)));
-            n_same += __popc(__ballot_sync(0xffffffffu, same));
+    for (int b = 0; b < len; b += block) {
+        load(b);
+        __syncthreads();  // the last block's list is read
+        const int n_rows = rows();
+#pragma unroll 1
+        for (int r = 0; r < ROWS; ++r) {
+            const uint4 k = r < n_rows ? keys(r) : make_uint4(0, 0, 0, 0);
+            // those that stay in the low half, those that are just equal in the high
+            int n = (k.x >= above) + (k.y >= above) + (k.z >= above) + (k.w >= above);
+            n += ((k.x == equal) + (k.y == equal) + (k.z == equal) + (k.w == equal)) << 16;
+            n = __reduce_add_sync(0xffffffffu, n);
+            if (lane == 0)
+                s_count[r * W + warp] = n;
         }
-        __syncthreads();  // the last window's list and sums are read
-        if (lane == 0)
-            s_sum[warp] = n_stay, s_equal[warp] = n_same;
         __syncthreads();
-        const int their_same = lane < W ? s_equal[lane < W ? lane : 0] : 0;
-        const int same_before = warp_scan(their_same) - their_same;
-        const int take = max(0, min(their_same, need - same_before));
-        const int theirs = (lane < W ? s_sum[lane < W ? lane : 0] : 0) + take;
-        const int upto = warp_scan(theirs), taken = warp_scan(take);
-        const int total = __shfl_sync(0xffffffffu, upto, 31);
-        int at = __shfl_sync(0xffffffffu, upto - theirs, warp), left = __shfl_sync(0xffffffffu, take, warp);
-        for (int i = 0; i < steps; ++i) {
-            bool same;
-            unsigned mine = __ballot_sync(0xffffffffu, stays(j0 + 32 * i, same));
-            const unsigned eq = __ballot_sync(0xffffffffu, same);
-            const unsigned first = __ballot_sync(0xffffffffu, same && __popc(eq & ((1u << lane) - 1)) < left);
-            left -= __popc(first);
-            mine |= first;
-            if (mine >> lane & 1)
-                s_src[at + __popc(mine & ((1u << lane) - 1))] = j0 + 32 * i;
-            at += __popc(mine);
+        if (warp == 0) {  // in the slots' order: row after row, warp after warp
+            constexpr int E = PLACES / 32;
+            int n[E], same = 0, stay = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                same += (n[e] = s_count[lane * E + e]) >> 16;
+            int same_before = warp_scan(same) - same, take[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                take[e] = max(0, min(n[e] >> 16, need - same_before));
+                same_before += n[e] >> 16;
+                stay += (n[e] & 0xffff) + take[e];
+            }
+            const int upto = warp_scan(stay);
+            int at = upto - stay, taken = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                s_place[lane * E + e] = at;
+                s_take[lane * E + e] = take[e];
+                at += (n[e] & 0xffff) + take[e];
+                taken += take[e];
+            }
+            taken = __reduce_add_sync(0xffffffffu, taken);
+            if (lane == 31)
+                s_total[0] = upto, s_total[1] = taken;
         }
-        need -= __shfl_sync(0xffffffffu, taken, 31);
         __syncthreads();
-        cluster_arrive();  // this window's weights are read
+        const int total = s_total[0];
+#pragma unroll 1
+        for (int r = 0; r < n_rows; ++r) {
+            const uint4 k4 = keys(r);
+            const unsigned k[4] = {k4.x, k4.y, k4.z, k4.w};
+            const int left = s_take[r * W + warp];
+            bool stays[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                stays[c] = k[c] >= above;
+            if (left > 0) {  // the first of those that are just equal
+                int rank = 0;
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    rank += __popc(__ballot_sync(0xffffffffu, k[c] == equal) & below);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (k[c] == equal)
+                        stays[c] |= rank++ < left;
+            }
+            int at = s_place[r * W + warp];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                at += __popc(__ballot_sync(0xffffffffu, stays[c]) & below);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (stays[c])
+                    s_src[at++] = (uint16_t)(4 * (r * THREADS + tid) + c);
+        }
+        need -= s_total[1];
+        __syncthreads();
+        cluster_arrive();  // this block's weights are read
         if (kept)
             for (int i = tid; i < total; i += THREADS)
-                kept[place + i] = s_src[i];
+                kept[place + i] = b + s_src[i];
         cluster_wait();
         for (int i0 = 0; i0 < total; i0 += ROUND) {
             const int n = min(ROUND, total - i0);
-            if (s_src[i0 + n - 1] == place + i0 + n - 1)  // all of them are where they stay
+            if (b + s_src[i0 + n - 1] == place + i0 + n - 1)  // all of them are where they stay
                 continue;
-            uint4 x[M * PP];
+            // a thread a row: its sector of codes, and its scales or its weight
+            uint4 x[M][PP];
             Scales d[M];
             float w[M];
 #pragma unroll
-            for (int e = 0; e < M * PP; ++e) {
-                const int i = (tid + e * THREADS) / PP, piece = (tid + e * THREADS) % PP;
-                if (i < n)
-                    x[e] = codes[token(s_src[i0 + i]) * (D / 32) + piece];
-            }
+            for (int m = 0; m < M; ++m) {
+                const int i = tid + m * THREADS;
+                if (i < n) {
+                    const int64_t from = token(b + s_src[i0 + i]);
 #pragma unroll
-            for (int e = 0; e < M; ++e) {
-                const int i = tid + e * THREADS;
-                if (i < n && moves_scales)
-                    d[e] = scales[token(s_src[i0 + i])];
-                if (i < n && moves_weights)
-                    w[e] = a.weight[token(s_src[i0 + i])];
+                    for (int e = 0; e < PP; ++e)
+                        x[m][e] = codes[from * (D / 32) + e];
+                    if (moves_scales)
+                        d[m] = scales[from];
+                    if (moves_weights)
+                        w[m] = a.weight[from];
+                }
             }
             __syncthreads();
 #pragma unroll
-            for (int e = 0; e < M * PP; ++e) {
-                const int i = (tid + e * THREADS) / PP, piece = (tid + e * THREADS) % PP;
-                if (i < n)
-                    codes[token(place + i0 + i) * (D / 32) + piece] = x[e];
-            }
+            for (int m = 0; m < M; ++m) {
+                const int i = tid + m * THREADS;
+                if (i < n) {
+                    const int64_t to = token(place + i0 + i);
 #pragma unroll
-            for (int e = 0; e < M; ++e) {
-                const int i = tid + e * THREADS;
-                if (i < n && moves_scales)
-                    scales[token(place + i0 + i)] = d[e];
-                if (i < n && moves_weights)
-                    a.weight[token(place + i0 + i)] = w[e];
+                    for (int e = 0; e < PP; ++e)
+                        codes[to * (D / 32) + e] = x[m][e];
+                    if (moves_scales)
+                        scales[to] = d[m];
+                    if (moves_weights)
+                        a.weight[to] = w[m];
+                }
             }
         }
         place += total;
     }
 }
 
-template <int D, int THREADS>
+template <int D, int THREADS, int ROWS>
 static qmd_status launch_evict4(Evict4Args a, cudaStream_t s)
 {
-    // shared memory for as many weights as the page table's columns can hold, up to EVICT_CAP
-    const int64_t most = a.kv.table_stride * a.kv.page_blocks * KV_BLOCK;
-    a.cap = (int)(most < EVICT_CAP ? most : EVICT_CAP);
-    a.list = (int)(most < EVICT_LIST ? (most + THREADS - 1) / THREADS * THREADS : EVICT_LIST);
-    const size_t smem = ((size_t)a.cap + a.list) * 4;
+    // a block: as many slots as the page table has room for, up to what the threads take; a list of those that stay
+    constexpr int MOST = THREADS * 4 * ROWS;
+    static_assert(MOST <= 65536, "listed in 16 bits");
+    const int64_t room = a.kv.table_stride * a.kv.page_blocks * KV_BLOCK;
+    a.block = (int)(room < MOST ? room : MOST);
+    const size_t smem = (size_t)a.block * 4 + ((a.keep < a.block ? a.keep : a.block) * 2 + 15) / 16 * 16;
     if (smem > 32 * 1024) {  // (48 KB with what the kernel declares itself need no asking)
         static std::mutex mu;
         static std::set<int> opted;
@@ -284,8 +344,8 @@ static qmd_status launch_evict4(Evict4Args a, cudaStream_t s)
             return QMD_ERR_DEVICE;
         std::lock_guard<std::mutex> lock(mu);
         if (!opted.count(dev)) {
-            const cudaError_t e = cudaFuncSetAttribute(kv4_evict_kernel<D, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       (EVICT_CAP + EVICT_LIST) * 4);
+            const cudaError_t e = cudaFuncSetAttribute(kv4_evict_kernel<D, THREADS, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       MOST * 6);
             if (e != cudaSuccess)
                 return fail(QMD_ERR_LAUNCH, "kv4_evict smem attribute", e);
             opted.insert(dev);
@@ -301,7 +361,7 @@ static qmd_status launch_evict4(Evict4Args a, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (launch_flags() & LAUNCH_NO_PDL) ? 0 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_evict_kernel<D, THREADS>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_evict_kernel<D, THREADS, ROWS>, a);
     return e == cudaSuccess ? QMD_OK : fail(QMD_ERR_LAUNCH, "kv4_evict launch", e);
 }
 
@@ -309,13 +369,13 @@ qmd_status launch_kv4_evict(const Kv4Params &kv, int head_dim, float *weight, in
                             int32_t *len_out, int32_t *kept, const DeviceInfo &dev, cudaStream_t s)
 {
     const int tokens = kv.page_blocks * KV_BLOCK;
-    const Evict4Args a = {kv, weight, keep, sinks, recent, 0, 0, fast_div((unsigned)tokens), len_out, kept};
+    const Evict4Args a = {kv, weight, keep, sinks, recent, 0, fast_div((unsigned)tokens), len_out, kept};
     // short tables: small CTAs, many to an SM
     const bool small = kv.table_stride * tokens <= 4096;
     switch (head_dim) {
-    case 64: return small ? launch_evict4<64, 256>(a, s) : launch_evict4<64, 1024>(a, s);
-    case 128: return small ? launch_evict4<128, 256>(a, s) : launch_evict4<128, 1024>(a, s);
-    default: return small ? launch_evict4<256, 256>(a, s) : launch_evict4<256, 1024>(a, s);
+    case 64: return small ? launch_evict4<64, 256, 4>(a, s) : launch_evict4<64, 1024, 8>(a, s);
+    case 128: return small ? launch_evict4<128, 256, 4>(a, s) : launch_evict4<128, 1024, 8>(a, s);
+    default: return small ? launch_evict4<256, 256, 4>(a, s) : launch_evict4<256, 1024, 8>(a, s);
     }
 }
 
