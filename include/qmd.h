@@ -533,7 +533,7 @@ qmd_status qmd_kv4_attention(const qmd_kv4_cache *cache, const qmd_kv_batch *bat
  *   lse     f32 [rows][q_heads], 4-byte aligned
  *   weight  f32 [pages][kv_heads][page_tokens], 16-byte aligned (read and written)
  * Values are not read (cache->v and v_scale may be NULL).  A weight is off by at most 2^-20 of itself while
- * |scale| * sum_d |q| |K| and |lse| are up to 32, and grows with them.  Rows that see no position (their lse is
+ * |scale| * sum_d |q| |K| and |lse| are up to 32, and grows with them; what is under 2^-126 counts as 0.  Rows that see no position (their lse is
  * -infinity) add nothing.  A slot must belong to one sequence, at one place of its table (no shared pages).
  * Other arguments, limits and errors as qmd_kv4_attention (there is no workspace).
  */

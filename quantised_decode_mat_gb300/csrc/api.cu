@@ -1070,6 +1070,6 @@ int64_t qmd_debug_trace_launches(int64_t *first, int32_t *ctas, int64_t max)
 }
 #endif
 
-int qmd_version(void) { return 200; }
+int qmd_version(void) { return 300; }
 
 }  // extern "C"

@@ -9,9 +9,10 @@ form of the pages' deferred streams ("One kernel, any device", §1; "The schedul
 when, beside what", §3), which issue a whole decode step as one graph.
 
 An AttentionBlock is the attention half of a layer as one chain: the fused q|k|v projection, the
-requests' adapters beside it, the rotation and the append to the 8-bit key/value cache, attention
+requests' adapters beside it, the rotation and the append to the key/value cache (8 or 4 bits), attention
 over the cache, the o projection and its adapters ("Language models on the device: the cajeta-llm
-kernels", §2.5 attention over the key/value cache, §2.6 rope).
+kernels", §2.5 attention over the key/value cache, §2.6 rope).  Over a 4-bit cache it can add up the
+attention that cached tokens get, and evict those that got least.
 
 All activations of the step live in one device buffer and all outputs in another, so an
 end-to-end step moves its inputs in with one host-to-device copy and its outputs out with one
@@ -24,8 +25,9 @@ from dataclasses import dataclass, field
 
 import numpy as np
 
-from . import (Q4_K, Q6_K_SPLIT, QMD_QK, ROPE_HALVES, KVBatch, KVCache, Q8K, QmdError, bind_q6k, kv_append,
-               kv_attention, kv_workspace, lora_add, q6k_prefix_stride, q8k_pack, qmatvec, qmatvec_x, rope_table)
+from . import (Q4_K, Q6_K_SPLIT, QMD_QK, ROPE_HALVES, KV4Cache, KVBatch, KVCache, Q8K, QmdError, bind_q6k, kv4_append,
+               kv4_attention, kv4_evict, kv4_weigh, kv_append, kv_attention, kv_workspace, lora_add, q6k_prefix_stride,
+               q8k_pack, qmatvec, qmatvec_x, rope_table)
 from . import synth
 
 @dataclass
@@ -323,12 +325,15 @@ class Adapters:
 class AttentionBlock:
     """The attention half of a decoder layer for up to 8 rows: x [rows, hidden] (normalised) to
     o(attention(rope(q), cache)) [rows, hidden].  W_qkv holds the rows of q, then k, then v; every
-    buffer belongs to the block, so a captured run can be replayed."""
+    buffer belongs to the block, so a captured run can be replayed.
+
+    Over a KV4Cache, `weights` (cache.new_weights()) makes every run add up the attention that each cached
+    token gets, and evict() drops the tokens that got least."""
     heads: int
     W_qkv: "object"             # Q4_K blocks, uint8 [(heads + 2 kv_heads) * head_dim, ..]
     W_o: "object"               # Q4_K blocks, uint8 [hidden, ..]
     rope: "object"              # f32 [positions, rot], or None
-    cache: KVCache
+    cache: "KVCache | KV4Cache"
     rows: int                   # rows of a call, at most 8
     hidden: int
     pairs: int = ROPE_HALVES
@@ -339,6 +344,8 @@ class AttentionBlock:
     attended: "object" = None   # f32 [rows, heads * head_dim]
     y: "object" = None          # f32 [rows, hidden]
     ws: "object" = None         # attention's workspace (one stream)
+    weights: "object" = None    # f32 [pages, kv_heads, page_tokens], or None: nothing is added up
+    lse: "object" = None        # f32 [rows, heads], with weights
 
     def __post_init__(self):
         import torch
@@ -360,14 +367,21 @@ class AttentionBlock:
         self.attended = torch.empty((self.rows, self.q_width), **f32)
         self.y = torch.empty((self.rows, self.hidden), **f32)
         self.ws = kv_workspace(dev)
+        self.four_bits = isinstance(self.cache, KV4Cache)
+        if self.weights is not None:
+            if not self.four_bits:
+                raise QmdError(2, "weights: of a KV4Cache's tokens only")
+            self.lse = torch.empty((self.rows, self.heads), **f32)
         k = self.q_width + self.kv_width
         self.q, self.k, self.v = self.qkv[:, :self.q_width], self.qkv[:, self.q_width:k], self.qkv[:, k:]
 
-    def run(self, x, batch: KVBatch, adapter=None, stream=None):
+    def run(self, x, batch: KVBatch, adapter=None, stream=None, positions=None):
         """One call's rows through the block: x f32 [rows, hidden]; batch says which sequences they
         belong to (kv_len counts them in); adapter int32 [rows] picks each row's adapter (below 0:
-        none) where the block has adapters.  Returns y.  A call whose arguments are refused has
+        none) where the block has adapters; positions int32 [batch.rows] are the rows' positions, where
+        something was evicted from a 4-bit cache (their slots otherwise).  Returns y.  A call whose arguments are refused has
         launched nothing."""
+        import torch
         if x.dtype is not self.qkv.dtype:
             raise QmdError(2, f"x: float32 is wanted, got {x.dtype}")
         adapted = self.qkv_adapters is not None or self.o_adapters is not None
@@ -383,25 +397,46 @@ class AttentionBlock:
             raise QmdError(1, "adapter: the block has adapters, each row's choice is wanted")
         if adapted and adapter.shape != (self.rows,):
             raise QmdError(6, f"adapter: shape ({self.rows},) is wanted, got {tuple(adapter.shape)}")
+        if positions is not None and not self.four_bits:
+            raise QmdError(10, "positions: of a KV4Cache's rows only")
+        if positions is not None and (positions.shape != (batch.rows,) or positions.dtype is not torch.int32):
+            raise QmdError(6, f"positions: int32 ({batch.rows},) is wanted, got {positions.dtype} {tuple(positions.shape)}")
         qmatvec_x(Q4_K, self.W_qkv, None, x, self.qkv, stream=stream)
         if self.qkv_adapters is not None:
             a = self.qkv_adapters
             lora_add(x, self.qkv, a.A, a.B, adapter, a.scale, out=self.qkv, stream=stream)
-        kv_append(self.cache, batch, self.k, self.v, self.rope, self.q, self.q, self.pairs, stream=stream)
-        kv_attention(self.cache, batch, self.q, self.cache.head_dim ** -0.5, self.ws, self.window, self.attended, stream=stream)
+        scale = self.cache.head_dim ** -0.5
+        if self.four_bits:
+            lse = None if self.weights is None else self.lse[:batch.rows]
+            kv4_append(self.cache, batch, self.k, self.v, self.rope, self.q, self.q, self.pairs, positions, stream)
+            kv4_attention(self.cache, batch, self.q, scale, self.ws, self.window, self.attended, lse, stream)
+            if lse is not None:
+                kv4_weigh(self.cache, batch, self.q, scale, lse, self.weights, self.window, stream)
+        else:
+            kv_append(self.cache, batch, self.k, self.v, self.rope, self.q, self.q, self.pairs, stream=stream)
+            kv_attention(self.cache, batch, self.q, scale, self.ws, self.window, self.attended, stream=stream)
         qmatvec_x(Q4_K, self.W_o, None, self.attended, self.y, stream=stream)
         if self.o_adapters is not None:
             a = self.o_adapters
             lora_add(self.attended, self.y, a.A, a.B, adapter, a.scale, out=self.y, stream=stream)
         return self.y
 
+    def evict(self, batch: KVBatch, keep: int, sinks: int = 0, recent: int = 0, len_out=None, stream=None):
+        """Bring every sequence of the batch back to `keep` tokens: for each key/value head the first `sinks`, the
+        last `recent` and those of the others that got most attention stay.  Returns their lengths, int32 [seqs]
+        (len_out), with which the next batch goes on; positions go on as if nothing was evicted."""
+        if self.weights is None:
+            raise QmdError(1, "weights: the block adds none up")
+        return kv4_evict(self.cache, batch, self.weights, keep, sinks, recent, len_out, stream=stream)
+
 
 def make_attention_block(rows: int, seqs: int, max_tokens: int, heads: int = 32, kv_heads: int = 8, head_dim: int = 128,
                          hidden: int = 4096, page_tokens: int = 64, rope_base: float = 500000.0, layer: int = 0,
-                         device="cuda"):
+                         device="cuda", kv_bits: int = 8, weigh: bool = False, positions: int | None = None):
     """A block of the 7B-shaped step (q|k|v 6144 x 4096 and o 4096 x 4096 by default) with the
     step's seeded weights, and the page table (int32 [seqs, columns]) of an empty cache that holds
-    max_tokens of each sequence."""
+    max_tokens of each sequence.  kv_bits 8 or 4; weigh: a 4-bit cache's block adds up its tokens' attention,
+    for evict(); positions: of the rope table (max_tokens by default)."""
     import torch
     dev = torch.device(device)
     seed = synth.step_seed(layer)
@@ -409,7 +444,10 @@ def make_attention_block(rows: int, seqs: int, max_tokens: int, heads: int = 32,
     Ws = [torch.from_numpy(synth.weights("q4k", seed, n, K, layer, t).reshape(n, -1)).to(dev)
           for n, K, t in ((qkv_rows, hidden, 0), (hidden, width, 1))]
     columns = -(-max_tokens // page_tokens)
-    cache = KVCache.empty(seqs * columns, kv_heads, page_tokens, head_dim, dev)
+    if kv_bits not in (4, 8):
+        raise QmdError(10, f"kv_bits: 4 or 8, got {kv_bits}")
+    cache = (KV4Cache if kv_bits == 4 else KVCache).empty(seqs * columns, kv_heads, page_tokens, head_dim, dev)
     table = torch.arange(seqs * columns, dtype=torch.int32, device=dev).view(seqs, columns)
-    block = AttentionBlock(heads, Ws[0], Ws[1], rope_table(max_tokens, head_dim, rope_base, device=dev), cache, rows, hidden)
+    rope = rope_table(max_tokens if positions is None else positions, head_dim, rope_base, device=dev)
+    block = AttentionBlock(heads, Ws[0], Ws[1], rope, cache, rows, hidden, weights=cache.new_weights() if weigh else None)
     return block, table

@@ -128,7 +128,8 @@ def attention(cache, table, lens, q_start, q, scale, window=0):
 def weigh(cache, table, lens, q_start, q, scale, lse, weight, window=0):
     """(weight, bound) after the rows' weights are added, 64 bits, from the given lse (f32).
     Bound: the scores' error and the argument's rounding (|s| + |lse| at 4 u), exp2 4 u, and one rounding for
-    each of the rows x heads terms and of the sum with the old weight."""
+    each of the rows x heads terms and of the sum with the old weight; a term under 2^-126, the least normal f32,
+    may be 0."""
     rows, heads, dim = q.shape
     G = heads // cache.heads
     new, bound = weight.astype(np.float64), np.zeros(weight.shape)
@@ -154,7 +155,7 @@ def weigh(cache, table, lens, q_start, q, scale, lse, weight, window=0):
                 e = score_bound(dim, mass, np.abs(sc)) + 4 * U * (abs(np.float64(lse[r, h])) + np.abs(arg))
                 at = (pg[begin:end], h // G, tok[begin:end])
                 new[at] += p
-                bound[at] += p * (np.expm1(e) + 4 * U)
+                bound[at] += p * (np.expm1(e) + 4 * U) + 2.0 ** -126
     return new, bound + (rows * G + 2) * U * np.abs(np.nan_to_num(new))
 
 
