@@ -60,8 +60,9 @@ struct Item4 {  // what a warp needs of its item after its units
     int pad;
 };
 
-// log2: how large a weight may get, where it may be when the reference moves, and likewise its product with a scale
-constexpr float A4_TOP = 14.9f, A4_WEIGHT = 12.0f, A4_LOG = 14.0f;
+constexpr float A4_TOP = 60000.0f;  // how large a weight times scale may get
+constexpr float A4_LOG = 14.0f;     // and (log2) may be where the reference moves
+constexpr float A4_WEIGHT = 44.0f;  // likewise a weight alone, whose limit is 2^2 above
 
 // The least k with |d| < 2^k, for an f16 scale; 16 where it is not finite.
 __device__ __forceinline__ float scale4_log2(float d)
@@ -269,15 +270,19 @@ __global__ void __launch_bounds__(Attn4Cfg<D, R>::W * 32, 1)
                     }
                 poison &= (bad & ~all) * 0x1111u;
             }
-            // Is a row's reference passed?  Scales under 2 need only the weights looked at.
-            unsigned all_bits = 0;
+            // Is a row's reference passed?  (By a bound on every weight times scale of this lane's four slots.)
+            __half2 most = __habs2(as_half2(dv[0][0][0]));
 #pragma unroll
-            for (int i = 0; i < 2 * G; ++i)
-                all_bits |= dv[i / G][i / (G / 2) & 1][i % (G / 2)];
-            bool up = all_bits & 0x40004000u;
+            for (int i = 1; i < 2 * G; ++i)
+                most = __hmax2(most, __habs2(as_half2(dv[i / G][i / (G / 2) & 1][i % (G / 2)])));
+            const float2 most2 = __half22float2(most);
+            const float most1 = fmaxf(most2.x, most2.y);
+            bool up = false;
 #pragma unroll
-            for (int i = 0; i < LR; ++i)
-                up |= fmaxf(fmaxf(sc[0][i][0], sc[0][i][1]), fmaxf(sc[1][i][0], sc[1][i][1])) - ref[i] > A4_TOP;
+            for (int i = 0; i < LR; ++i) {
+                const float x = fmaxf(fmaxf(sc[0][i][0], sc[0][i][1]), fmaxf(sc[1][i][0], sc[1][i][1])) - ref[i];
+                up |= x > A4_WEIGHT + 2.0f || ex2(x) * most1 > A4_TOP;
+            }
             if (__any_sync(0xffffffffu, up)) {
                 float lg[2][2];  // the slots' largest |scale|: the least k with |d| < 2^k, at most 2^16
 #pragma unroll

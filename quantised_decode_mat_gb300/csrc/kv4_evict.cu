@@ -249,7 +249,7 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
                 s_total[0] = upto, s_total[1] = taken;
         }
         __syncthreads();
-        const int total = s_total[0];
+        const int total = min(s_total[0], a.keep - place);
 #pragma unroll 1
         for (int r = 0; r < n_rows; ++r) {
             const uint4 k4 = keys(r);
@@ -335,7 +335,9 @@ static qmd_status launch_evict4(Evict4Args a, cudaStream_t s)
     static_assert(MOST <= 65536, "listed in 16 bits");
     const int64_t room = a.kv.table_stride * a.kv.page_blocks * KV_BLOCK;
     a.block = (int)(room < MOST ? room : MOST);
-    const size_t smem = (size_t)a.block * 4 + ((a.keep < a.block ? a.keep : a.block) * 2 + 15) / 16 * 16;
+    // (blocks that are read more than once could be written by someone in between: then any number may stay)
+    const int list = a.keep < a.block && room <= MOST ? a.keep : a.block;
+    const size_t smem = (size_t)a.block * 4 + (list * 2 + 15) / 16 * 16;
     if (smem > 32 * 1024) {  // (48 KB with what the kernel declares itself need no asking)
         static std::mutex mu;
         static std::set<int> opted;

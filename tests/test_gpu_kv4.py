@@ -226,6 +226,17 @@ def test_value_scales_far_apart(ws, heads, dim, n):
     s.check(x, ws, weigh=False)
 
 
+@pytest.mark.parametrize("size", [2.0 ** -22, 2.0 ** -14, 2.0 ** -6, 2.0 ** 12])
+@pytest.mark.parametrize("heads,dim", [(4, 128), (8, 64), (16, 128)])
+def test_values_of_all_sizes(ws, size, heads, dim):
+    """The error is relative to the values, from scales that are subnormal in f16 to the largest."""
+    s = Scene([2000, 45], [1, 2], heads, 1, dim, 32, seed=heads)
+    with np.errstate(invalid="ignore"):
+        s.c.vs = (s.c.vs.astype(np.float32) * np.float32(size)).astype(np.float16)
+    s.place()
+    s.check(s.queries(), ws, weigh=False)
+
+
 @pytest.mark.parametrize("heads", [4, 8, 16])
 def test_groups_far_apart_and_scales_of_zero(ws, heads):
     """Groups of a head 2^10 apart, one whose scales are all zero, and keys of zero."""
@@ -426,6 +437,12 @@ def test_evict_ties(keep):
     evict_case([300, 120, 301], keep, 3, 5, 2, 64, 32, seed=keep, weights=tied)
     evict_case([300, 2000], keep, 0, 0, 2, 64, 32, seed=keep, weights=lambda s: np.zeros_like(s.w))
     evict_case([300, 2000], keep, 0, 0, 2, 64, 32, seed=keep, weights=lambda s: np.full_like(s.w, np.nan))
+
+
+def test_evict_more_than_a_block():
+    """More slots than are worked on together, few and many of them kept, ties among them."""
+    for keep, weights in ((70, None), (40000, None), (40000, tied)):
+        evict_case([50000, 70000], keep, 4, 30, 1, 64, 128, seed=keep, weights=weights)
 
 
 def test_evict_rising_and_falling():
