@@ -4,21 +4,23 @@
 // largest weights stay (of equal ones the earlier); what stays moves to the front in its order.  A token moves
 // whole, codes, scales and weight, so nothing is rounded again.
 //
+// Split.  Four CTAs to a sequence and head, a cluster.  Each moves its part of every row that stays (half of the keys'
+// bytes or of the values'), which lies in nobody else's way, and (SPLIT) selects among its quarter of the slots; where
+// tables are short each selects among all for itself, which takes less than the cluster's meetings (12 x 8 heads of
+// 1088 slots: 16.2 us against 28.4 with quarters; 8 heads of 24000: 24.9 against 18.8).
+//
 // Selection.  Weights become whole numbers in their order, kept in shared memory, four neighbouring slots to a thread and
 // row of them (of more slots than a block of it holds, the blocks are read again for each pass).  The number that
-// just stays is found by three histograms in shared memory, of 11, 11 and 10 bits, each over the numbers that agree
-// with what was found so far; it ends early when a bin is taken whole.
+// just stays is found by three histograms, of 11, 11 and 10 bits, each over the numbers that agree with what was
+// found so far, summed over the cluster (SPLIT) by reading the others' shared memory; it ends early when a bin is taken whole.
 //
-// Moving, a block of slots at a time: ballots give each warp its counts, one scan over rows and warps the places, and
-// the ballots again the list of what stays.  A token's place is never behind its slot, and places and slots both
-// rise, so a token may be written once all that come before it have been read: a round of tokens is read, the CTA
-// meets, the round is written; the next round's reads may pass these writes.
+// Moving, a block of slots at a time: counts of each row and warp, one scan, and ballots give every slot that stays its
+// place in the list, which with SPLIT each CTA writes into all four.  A token's place is never behind its slot, and places and
+// slots both rise, so a token may be written once all that come before it have been read: a round of tokens is read,
+// the CTA meets, the round is written; the next round's reads may pass these writes.  Weights are moved by one
+// CTA, after the barrier behind which all have read theirs.
 //
-// Split.  Four CTAs to a sequence and head, a cluster: each selects for itself, and moves its part of every row
-// (half of the keys' bytes or of the values'), which lies in nobody else's way.  Weights, which all four have
-// to have read, are moved by one of them, after a barrier of the cluster in each block.
-//
-// Bound: latency (some ten dependent steps), and for few sequences what their few SMs move.
+// Bound: latency (some twenty dependent steps), and for few sequences what their few SMs move.
 #include <mutex>
 #include <set>
 #include <type_traits>
@@ -36,7 +38,7 @@ struct Evict4Args {
     Kv4Params kv;
     float *weight;
     int keep, sinks, recent;
-    int block;  // slots worked on together, at most 4 * ROWS * THREADS
+    int block;  // slots worked on together, at most 4 * ROWS * THREADS a share
     FastDiv by_tokens;
     int32_t *len_out, *kept;
 };
@@ -66,20 +68,44 @@ __device__ __forceinline__ int warp_scan(int x)  // inclusive
     return x;
 }
 
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+// All threads of the cluster meet; what they wrote to shared memory before is seen after.
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
 
-// ROWS: times four keys to a thread
-template <int D, int THREADS, int ROWS>
+// Where this CTA's shared memory at p lies in that of the cluster's `rank`-th.
+__device__ __forceinline__ uint32_t in_cta(const void *p, int rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ int4 load_remote4(uint32_t at)
+{
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void store_remote16(uint32_t at, uint16_t v)
+{
+    asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(at), "h"(v) : "memory");
+}
+
+// ROWS: times four keys to a thread.  SPLIT: each CTA of a cluster has a quarter of the slots.
+template <int D, int THREADS, int ROWS, bool SPLIT>
 __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, THREADS == 256 ? 3 : 1)
     kv4_evict_kernel(const Evict4Args a)
 {
-    constexpr int W = THREADS / 32, PLACES = ROWS * W;
+    constexpr int W = THREADS / 32, SHARES = SPLIT ? EVICT_PARTS : 1, PLACES = (ROWS * W + 31) / 32 * 32;
     extern __shared__ __align__(16) unsigned char smem[];
-    uint4 *s_key = reinterpret_cast<uint4 *>(smem);                     // of a block's slots, [block / 4]
-    uint16_t *s_src = reinterpret_cast<uint16_t *>(s_key + a.block / 4);  // those that stay, counted from the block's first
-    __shared__ int s_hist[EVICT_BINS], s_sum[W], s_found[3];
-    __shared__ int s_count[PLACES], s_place[PLACES], s_take[PLACES], s_total[2];
+    uint4 *s_key = reinterpret_cast<uint4 *>(smem);                      // of this CTA's share of a block
+    uint16_t *s_src = reinterpret_cast<uint16_t *>(s_key + a.block / (4 * SHARES));  // slots that stay, counted from the block's first
+    __shared__ __align__(16) int s_hists[2][EVICT_BINS], s_all[4];
+    __shared__ int s_sum[W], s_found[3];
+    __shared__ int s_count[PLACES], s_place[PLACES], s_take[PLACES];
     const Kv4Params &p = a.kv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, block = a.block;
     const int item = blockIdx.x / EVICT_PARTS, part = blockIdx.x % EVICT_PARTS;
@@ -118,26 +144,34 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
     const int m0 = a.sinks, m1 = len - a.recent;
     // slots that stay anyway have a key above all weights', those behind the last one below them
     auto key_at = [&](int j, float w) { return j >= len ? 0u : j < m0 || j >= m1 ? EVICT_STAYS : weight_key(w); };
-    int b0 = -1;  // the block whose keys are in shared memory
+    // the share of block b that this CTA has: slots c0 .. c0 + n - 1, n a multiple of 128
+    int b0 = -1, c0 = 0, n = 0;
     auto load = [&](int b) {
         if (b0 == b)
             return;
         b0 = b;
-        __syncthreads();  // the last one's are read
+        n = (min(block, len - b) + SHARES * 128 - 1) / (SHARES * 128) * 128;
+        c0 = SPLIT ? b + part * n : b;
+        __syncthreads();  // the last one's keys are read
 #pragma unroll 4
-        for (int j = 4 * tid; j < block; j += 4 * THREADS) {
+        for (int j = 4 * tid; j < n; j += 4 * THREADS) {
             float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (b + j < len)  // (a page's tokens are a multiple of 16)
-                w = *reinterpret_cast<const float4 *>(a.weight + token(b + j));
-            s_key[j / 4] = make_uint4(key_at(b + j, w.x), key_at(b + j + 1, w.y), key_at(b + j + 2, w.z), key_at(b + j + 3, w.w));
+            if (c0 + j < min(len, b + block))  // (a page's tokens are a multiple of 16)
+                w = *reinterpret_cast<const float4 *>(a.weight + token(c0 + j));
+            s_key[j / 4] = make_uint4(key_at(c0 + j, w.x), key_at(c0 + j + 1, w.y), key_at(c0 + j + 2, w.z), key_at(c0 + j + 3, w.w));
         }
         __syncthreads();
     };
-    auto rows = [&] { return (min(block, len - b0) + 4 * THREADS - 1) / (4 * THREADS); };
-    // a row's keys of this thread (behind the block's last slot there are none)
+    // a row's keys of this thread (behind the share's last slot there are none)
     auto keys = [&](int r) {
         const int i = r * THREADS + tid;
-        return 4 * i < block ? s_key[i] : make_uint4(0, 0, 0, 0);
+        return 4 * i < n ? s_key[i] : make_uint4(0, 0, 0, 0);
+    };
+    auto meet = [] {  // those who have shares
+        if constexpr (SPLIT)
+            cluster_barrier();
+        else
+            __syncthreads();
     };
     int need = a.keep - a.sinks - a.recent;  // of slots [m0, m1)
     // keys from `above` on stay, and the first `need` that are `equal`
@@ -146,6 +180,8 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
         unsigned prefix = 0;
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+            // (two by turns: the others may still read the last pass's)
+            int *s_hist = s_hists[pass & 1];
             for (int i = tid; i < EVICT_BINS; i += THREADS)
                 s_hist[i] = 0;
             __syncthreads();
@@ -155,20 +191,27 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
                     if (k != 0 && (pass == 0 ? k != EVICT_STAYS : k >> (shift + bits) == prefix))
                         atomicAdd(&s_hist[(1 << bits) - 1 - (int)(k >> shift & ((1u << bits) - 1))], 1);
                 };
-                const int n = rows();
 #pragma unroll 1
-                for (int r = 0; r < n; ++r) {
+                for (int r = 0; 4 * r * THREADS < n; ++r) {
                     const uint4 k = keys(r);
                     count(k.x), count(k.y), count(k.z), count(k.w);
                 }
             }
-            __syncthreads();
-            // the bin in which the need-th lies: a scan over threads of EVICT_BINS / THREADS bins each
+            meet();
+            // the bin in which the need-th lies: a scan over threads of EVICT_BINS / THREADS bins each, of all shares
             constexpr int E = EVICT_BINS / THREADS;
             int h[E], sum = 0;
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                sum += h[e] = s_hist[tid * E + e];
+            for (int e = 0; e < E; e += 4) {
+                h[e] = h[e + 1] = h[e + 2] = h[e + 3] = 0;
+#pragma unroll
+                for (int c = 0; c < SHARES; ++c) {
+                    const int *at = s_hist + tid * E + e;
+                    const int4 v = SPLIT ? load_remote4(in_cta(at, c)) : *reinterpret_cast<const int4 *>(at);
+                    h[e] += v.x, h[e + 1] += v.y, h[e + 2] += v.z, h[e + 3] += v.w;
+                }
+                sum += (h[e] + h[e + 1]) + (h[e + 2] + h[e + 3]);
+            }
             const int inc = warp_scan(sum);
             if (lane == 31)
                 s_sum[warp] = inc;
@@ -209,49 +252,65 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
     int place = 0;
     for (int b = 0; b < len; b += block) {
         load(b);
-        __syncthreads();  // the last block's list is read
-        const int n_rows = rows();
+        __syncthreads();
 #pragma unroll 1
         for (int r = 0; r < ROWS; ++r) {
-            const uint4 k = r < n_rows ? keys(r) : make_uint4(0, 0, 0, 0);
+            const uint4 k = keys(r);
             // those that stay in the low half, those that are just equal in the high
-            int n = (k.x >= above) + (k.y >= above) + (k.z >= above) + (k.w >= above);
-            n += ((k.x == equal) + (k.y == equal) + (k.z == equal) + (k.w == equal)) << 16;
-            n = __reduce_add_sync(0xffffffffu, n);
+            int m = (k.x >= above) + (k.y >= above) + (k.z >= above) + (k.w >= above);
+            m += ((k.x == equal) + (k.y == equal) + (k.z == equal) + (k.w == equal)) << 16;
+            m = __reduce_add_sync(0xffffffffu, m);
             if (lane == 0)
-                s_count[r * W + warp] = n;
+                s_count[r * W + warp] = m;
         }
+        if (tid >= ROWS * W && tid < PLACES)
+            s_count[tid] = 0;
         __syncthreads();
-        if (warp == 0) {  // in the slots' order: row after row, warp after warp
-            constexpr int E = PLACES / 32;
-            int n[E], same = 0, stay = 0;
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                same += (n[e] = s_count[lane * E + e]) >> 16;
-            int same_before = warp_scan(same) - same, take[E];
+        constexpr int E = PLACES / 32;
+        int m[E], same = 0, stay = 0;
+        if (warp == 0) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                take[e] = max(0, min(n[e] >> 16, need - same_before));
-                same_before += n[e] >> 16;
-                stay += (n[e] & 0xffff) + take[e];
+                m[e] = s_count[lane * E + e];
+                same += m[e] >> 16;
+                stay += m[e] & 0xffff;
             }
-            const int upto = warp_scan(stay);
-            int at = upto - stay, taken = 0;
+            const int all_same = __reduce_add_sync(0xffffffffu, same), all_stay = __reduce_add_sync(0xffffffffu, stay);
+            if (lane == 0)
+                s_all[0] = all_stay, s_all[1] = all_same;
+        }
+        meet();  // (behind which, too, the others have read the last block's list)
+        // this CTA's first place, and how many of its equals stay: the shares lie one after the other
+        int first = 0, room = 0, total = 0, taken = 0;
+#pragma unroll
+        for (int c = 0; c < SHARES; ++c) {
+            const int4 v = SPLIT ? load_remote4(in_cta(s_all, c)) : *reinterpret_cast<const int4 *>(s_all);
+            const int take = max(0, min(v.y, need - taken));
+            if (!SPLIT || c == part)
+                first = total, room = take;
+            total += v.x + take;
+            taken += take;
+        }
+        total = min(total, a.keep - place);
+        if (warp == 0) {  // in the slots' order: row after row, warp after warp
+            int same_before = warp_scan(same) - same, take[E], sum = stay;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                take[e] = max(0, min(m[e] >> 16, room - same_before));
+                same_before += m[e] >> 16;
+                sum += take[e];
+            }
+            int at = first + warp_scan(sum) - sum;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 s_place[lane * E + e] = at;
                 s_take[lane * E + e] = take[e];
-                at += (n[e] & 0xffff) + take[e];
-                taken += take[e];
+                at += (m[e] & 0xffff) + take[e];
             }
-            taken = __reduce_add_sync(0xffffffffu, taken);
-            if (lane == 31)
-                s_total[0] = upto, s_total[1] = taken;
         }
         __syncthreads();
-        const int total = min(s_total[0], a.keep - place);
 #pragma unroll 1
-        for (int r = 0; r < n_rows; ++r) {
+        for (int r = 0; 4 * r * THREADS < n; ++r) {
             const uint4 k4 = keys(r);
             const unsigned k[4] = {k4.x, k4.y, k4.z, k4.w};
             const int left = s_take[r * W + warp];
@@ -275,16 +334,23 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
                 at += __popc(__ballot_sync(0xffffffffu, stays[c]) & below);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                if (stays[c])
-                    s_src[at++] = (uint16_t)(4 * (r * THREADS + tid) + c);
+                if (stays[c]) {
+                    const uint16_t j = (uint16_t)(c0 - b + 4 * (r * THREADS + tid) + c);
+                    if constexpr (SPLIT) {
+#pragma unroll
+                        for (int to = 0; to < EVICT_PARTS; ++to)
+                            store_remote16(in_cta(s_src + at, to), j);
+                    } else {
+                        s_src[at] = j;
+                    }
+                    ++at;
+                }
         }
-        need -= s_total[1];
-        __syncthreads();
-        cluster_arrive();  // this block's weights are read
+        need -= taken;
+        cluster_barrier();  // the list is whole, and this block's weights are read
         if (kept)
             for (int i = tid; i < total; i += THREADS)
                 kept[place + i] = b + s_src[i];
-        cluster_wait();
         for (int i0 = 0; i0 < total; i0 += ROUND) {
             const int n = min(ROUND, total - i0);
             if (b + s_src[i0 + n - 1] == place + i0 + n - 1)  // all of them are where they stay
@@ -327,17 +393,17 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
     }
 }
 
-template <int D, int THREADS, int ROWS>
+template <int D, int THREADS, int ROWS, bool SPLIT>
 static qmd_status launch_evict4(Evict4Args a, cudaStream_t s)
 {
     // a block: as many slots as the page table has room for, up to what the threads take; a list of those that stay
-    constexpr int MOST = THREADS * 4 * ROWS;
+    constexpr int SHARES = SPLIT ? EVICT_PARTS : 1, MOST = SHARES * THREADS * 4 * ROWS;
     static_assert(MOST <= 65536, "listed in 16 bits");
     const int64_t room = a.kv.table_stride * a.kv.page_blocks * KV_BLOCK;
-    a.block = (int)(room < MOST ? room : MOST);
+    a.block = room < MOST ? (int)((room + 511) / 512 * 512) : MOST;  // (shares of whole 128s)
     // (blocks that are read more than once could be written by someone in between: then any number may stay)
     const int list = a.keep < a.block && room <= MOST ? a.keep : a.block;
-    const size_t smem = (size_t)a.block * 4 + (list * 2 + 15) / 16 * 16;
+    const size_t smem = (size_t)a.block * 4 / SHARES + (list * 2 + 15) / 16 * 16;
     if (smem > 32 * 1024) {  // (48 KB with what the kernel declares itself need no asking)
         static std::mutex mu;
         static std::set<int> opted;
@@ -346,8 +412,8 @@ static qmd_status launch_evict4(Evict4Args a, cudaStream_t s)
             return QMD_ERR_DEVICE;
         std::lock_guard<std::mutex> lock(mu);
         if (!opted.count(dev)) {
-            const cudaError_t e = cudaFuncSetAttribute(kv4_evict_kernel<D, THREADS, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       MOST * 6);
+            const cudaError_t e = cudaFuncSetAttribute(kv4_evict_kernel<D, THREADS, ROWS, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       MOST * 4 / SHARES + MOST * 2);
             if (e != cudaSuccess)
                 return fail(QMD_ERR_LAUNCH, "kv4_evict smem attribute", e);
             opted.insert(dev);
@@ -363,7 +429,7 @@ static qmd_status launch_evict4(Evict4Args a, cudaStream_t s)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = (launch_flags() & LAUNCH_NO_PDL) ? 0 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_evict_kernel<D, THREADS, ROWS>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv4_evict_kernel<D, THREADS, ROWS, SPLIT>, a);
     return e == cudaSuccess ? QMD_OK : fail(QMD_ERR_LAUNCH, "kv4_evict launch", e);
 }
 
@@ -375,9 +441,9 @@ qmd_status launch_kv4_evict(const Kv4Params &kv, int head_dim, float *weight, in
     // short tables: small CTAs, many to an SM
     const bool small = kv.table_stride * tokens <= 4096;
     switch (head_dim) {
-    case 64: return small ? launch_evict4<64, 256, 4>(a, s) : launch_evict4<64, 1024, 8>(a, s);
-    case 128: return small ? launch_evict4<128, 256, 4>(a, s) : launch_evict4<128, 1024, 8>(a, s);
-    default: return small ? launch_evict4<256, 256, 4>(a, s) : launch_evict4<256, 1024, 8>(a, s);
+    case 64: return small ? launch_evict4<64, 256, 4, false>(a, s) : launch_evict4<64, 512, 8, true>(a, s);
+    case 128: return small ? launch_evict4<128, 256, 4, false>(a, s) : launch_evict4<128, 512, 8, true>(a, s);
+    default: return small ? launch_evict4<256, 256, 4, false>(a, s) : launch_evict4<256, 512, 8, true>(a, s);
     }
 }
 
