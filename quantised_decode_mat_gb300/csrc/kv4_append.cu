@@ -8,6 +8,9 @@
 // queries, keys or values, whose loads are in flight together and whose angles are read once.  A lane owns 4 or
 // 8 neighbouring values of a head, a group is 8 or 4 lanes.  Rows do not depend on each other (a scale belongs to
 // one token), so nothing waits for a block and nothing is written twice.
+//
+// Bound: memory for prompts (11739 rows of 32 + 2 x 8 heads of 128: 97 us for 500 MB, 5.1 TB/s, seven eighths of it
+// queries in and out; their read back 24 us, 4.5 TB/s), launch latency for single tokens (8 rows 5.7 us, read back 3.1).
 #include <cuda_runtime.h>
 
 #include "internal.h"

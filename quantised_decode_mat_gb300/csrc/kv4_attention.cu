@@ -19,7 +19,14 @@
 //
 // Loads: per unit a warp asks for the keys' and the values' codes by tiled tensor copies (swizzled, so that
 // ldmatrix meets no bank conflicts) and for their scales by plain bulk copies, into a ring of STAGES units.
-// A page of an even number of 16-token blocks holds whole units: one copy of 32 rows instead of two of 16.
+// A page of an even number of 16-token blocks holds whole units: one copy of 32 rows instead of two of 16.  Rings of two
+// units and as many warps as registers allow: at 128 dimensions and 4 rows 16 warps 72.4 us, 12 with two or three
+// units 76.0 (40 sequences of 1500-14011 tokens); 8 rows 12 warps 68.4, 8 warps 76.9 (24 x 8100, 8 heads to one).
+//
+// Measured: those 40 sequences (32 heads over 8 of 128, 343 MB) 74 us, 4.6 TB/s, 0.68 of the copy rate: 9 us of lookups
+// and joins, then 5.4 TB/s.  Instructions bound it: 653 a unit, of them 288 that make codes f16 (without these 64 us;
+// without either product 62, which is the copies).  One sequence of 32768 20.7 us, of 19 5.2 us; 16 rows to a head (12 x
+// 8100, 4 rows each) 66.8 us.
 #include <climits>
 #include <mutex>
 

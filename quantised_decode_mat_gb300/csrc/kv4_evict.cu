@@ -20,7 +20,8 @@
 // the CTA meets, the round is written; the next round's reads may pass these writes.  Weights are moved by one
 // CTA, after the barrier behind which all have read theirs.
 //
-// Bound: latency (some twenty dependent steps), and for few sequences what their few SMs move.
+// Bound: latency (some twenty dependent steps), and for few sequences what their few SMs move.  8 heads of 24000 slots to
+// 2048: 18.8 us; 12 x 8 heads of 1088 to 1024: 14.8 us, half of it the moves (28 MB).
 #include <mutex>
 #include <set>
 #include <type_traits>

@@ -13,6 +13,10 @@
 // are added in the groups' order.  (One warp taking the groups one after the other has its pipeline of copies and its
 // queries anew for each: 8 groups over 16010 slots 62 us.)
 //
+// Measured: 24 sequences of 2080 slots, 32 heads over 8 of 128, 15.2 us (32 MB: 2.1 TB/s; 5 units a warp behind the same
+// 5 us of launch and lookups that a single unit takes); a prompt's last 32 rows over 16010 slots 50.7 us (4.2 GFLOP, as
+// two f16 parts each 8.4 on mma.sync).
+//
 // Either way a slot's weight is only ever touched by one warp at a time, in one order: no atomics, the same bits every time.
 #include <climits>
 #include <mutex>
