@@ -502,14 +502,17 @@ qmd_status launch_kv4_attention(const Kv4Params &kv, int head_dim, const float *
     static_cast<AttnArgs &>(a) = attn_args(kv, q, q_stride, q_heads, scale, window, out, out_stride, ws, dev);
     a.lse = lse;
     a.units = {kv.ks4, kv.vs4, kv.page_blocks % 2 == 0};
-    // rows per item: the least of 4, 8, 16 that holds a sequence's rows of one key/value head
+    // rows per item: 4 or 8 where that holds a sequence's rows of one key/value head; of more, 16 where they make whole
+    // pairs of groups of 8 (16 rows, 12 x 8100: 66.5 us, 69.8 in eights; 32 rows, 8 x 3000: 41.4 and 42.5), else 8 (20 rows, 8 x
+    // 3000: 34.1 us, 39.6 in sixteens, of which the last would be more than half empty)
     const int64_t rows = (int64_t)a.group * kv.max_q;
+    const bool eights = (rows + 7) / 8 & 1;
     if (head_dim == 64)
-        return rows <= 4 ? launch_att4<64, 4>(a, dev, s) : rows <= 8 ? launch_att4<64, 8>(a, dev, s) : launch_att4<64, 16>(a, dev, s);
+        return rows <= 4 ? launch_att4<64, 4>(a, dev, s) : eights ? launch_att4<64, 8>(a, dev, s) : launch_att4<64, 16>(a, dev, s);
     if (head_dim == 128)
-        return rows <= 4   ? launch_att4<128, 4>(a, dev, s)
-               : rows <= 8 ? launch_att4<128, 8>(a, dev, s)
-                           : launch_att4<128, 16>(a, dev, s);
+        return rows <= 4 ? launch_att4<128, 4>(a, dev, s)
+               : eights  ? launch_att4<128, 8>(a, dev, s)
+                         : launch_att4<128, 16>(a, dev, s);
     return rows <= 4 ? launch_att4<256, 4>(a, dev, s) : launch_att4<256, 8>(a, dev, s);
 }
 

@@ -13,8 +13,8 @@
 // are added in the groups' order.  (One warp taking the groups one after the other has its pipeline of copies and its
 // queries anew for each: 8 groups over 16010 slots 62 us.)
 //
-// Measured: 24 sequences of 2080 slots, 32 heads over 8 of 128, 15.2 us (32 MB: 2.1 TB/s; 5 units a warp behind the same
-// 5 us of launch and lookups that a single unit takes); a prompt's last 32 rows over 16010 slots 50.7 us (4.2 GFLOP, as
+// Measured: 24 sequences of 2080 slots, 32 heads over 8 of 128, 14.0 us (32 MB: 2.3 TB/s; 5 units a warp behind the same
+// 5 us of launch and lookups that a single unit takes); a prompt's last 32 rows over 16010 slots 48.5 us (4.2 GFLOP, as
 // two f16 parts each 8.4 on mma.sync).
 //
 // Either way a slot's weight is only ever touched by one warp at a time, in one order: no atomics, the same bits every time.
@@ -39,9 +39,10 @@ template <int D, int R, bool TEAM>
 struct Weigh4Cfg {
     using T = Tile4<D>;
     static constexpr int W = D == 256 ? (R == 4 ? 12 : 8) : R == 4 || D == 64 ? 16 : R == 8 ? 12 : 8;
-    static constexpr int STAGES = D == 256 ? 3 : 4;
+    // (24 x 2080 slots, a row each: 14.0, 14.5, 15.0 us with 2, 3, 4; asking for a unit is some 60 instructions of one lane)
+    static constexpr int STAGES = !TEAM ? 2 : D == 256 ? 3 : 4;
     static constexpr int RING = STAGES * Units4<D, STAGES, false>::STAGE;
-    static constexpr int CHUNK = 4;  // units whose sums a team's warps lay down before they are added
+    static constexpr int CHUNK = 8;  // units whose sums a team's warps lay down before they are added (4: 50.8, 8: 48.5 us)
     static constexpr int PART = TEAM ? CHUNK * 128 : 0;
     static constexpr int FIXED = W * (RING + 512 + PART) + W * (8 * STAGES + 8);
     static_assert(RING % (4 * D) == 0, "rings begin where the swizzle does");
