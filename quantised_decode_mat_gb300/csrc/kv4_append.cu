@@ -9,8 +9,9 @@
 // 8 neighbouring values of a head, a group is 8 or 4 lanes.  Rows do not depend on each other (a scale belongs to
 // one token), so nothing waits for a block and nothing is written twice.
 //
-// Bound: memory for prompts (11739 rows of 32 + 2 x 8 heads of 128: 97 us for 500 MB, 5.1 TB/s, seven eighths of it
-// queries in and out; their read back 24 us, 4.5 TB/s), launch latency for single tokens (8 rows 4.4 us, read back 3.1).
+// Bound: memory for prompts (11739 rows of 32 + 2 x 8 heads of 128: 97 to 105 us for 500 MB, 4.8 to 5.1 TB/s, seven
+// eighths of it queries in and out; their read back 24 us, 4.5 TB/s), launch latency for single tokens (8 rows 4.0 us, read
+// back 2.8).
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -80,8 +81,8 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv4_append_kernel(const Append
     const int other = hl * H::LPH + partner<E>(a.rope, l);
     const int kv_groups = (p.heads + N * H::HPW - 1) / (N * H::HPW);
     const int q_groups = (a.q_heads + N * H::HPW - 1) / (N * H::HPW);
-    const int of_row = 2 * kv_groups + q_groups;
-    for (int task = blockIdx.y * APP_WARPS + warp; task < APP_CHUNK * of_row; task += gridDim.y * APP_WARPS) {
+    const int of_row = 2 * kv_groups + q_groups, tasks = (int)min((int64_t)APP_CHUNK, p.rows - t0) * of_row;
+    for (int task = blockIdx.y * APP_WARPS + warp; task < tasks; task += gridDim.y * APP_WARPS) {
         const int i = task / of_row, part = task % of_row;
         const int kind = part < kv_groups ? 0 : part < 2 * kv_groups ? 1 : 2;  // keys, values, queries
         const int h = (part - kind * kv_groups) * (N * H::HPW) + hl, heads = kind == 2 ? a.q_heads : p.heads;
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(APP_WARPS * 32) kv4_read_kernel(const Read4Arg
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int hl = lane / H::LPH, l = lane % H::LPH;
     const int groups = (p.heads + N * H::HPW - 1) / (N * H::HPW);
-    const int tasks = APP_CHUNK * groups * 2;
+    const int tasks = (int)min((int64_t)APP_CHUNK, p.rows - t0) * groups * 2;
     for (int task = blockIdx.y * APP_WARPS + warp; task < tasks; task += gridDim.y * APP_WARPS) {
         const int i = task / (2 * groups), h = task / 2 % groups * (N * H::HPW) + hl;
         const bool is_v = task & 1;
