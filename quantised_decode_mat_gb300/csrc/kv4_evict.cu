@@ -23,7 +23,6 @@
 // Bound: latency (some twenty dependent steps), and for few sequences what their few SMs move.  8 heads of 24000 slots to
 // 2048: 18.8 us; 12 x 8 heads of 1088 to 1024: 14.8 us, half of it the moves (28 MB).
 #include <mutex>
-#include <set>
 #include <type_traits>
 
 #include <cuda_runtime.h>
@@ -395,7 +394,7 @@ __global__ void __cluster_dims__(EVICT_PARTS, 1, 1) __launch_bounds__(THREADS, T
 }
 
 template <int D, int THREADS, int ROWS, bool SPLIT>
-static qmd_status launch_evict4(Evict4Args a, cudaStream_t s)
+static qmd_status launch_evict4(Evict4Args a, const DeviceInfo &dev, cudaStream_t s)
 {
     // a block: as many slots as the page table has room for, up to what the threads take; a list of those that stay
     constexpr int SHARES = SPLIT ? EVICT_PARTS : 1, MOST = SHARES * THREADS * 4 * ROWS;
@@ -405,19 +404,17 @@ static qmd_status launch_evict4(Evict4Args a, cudaStream_t s)
     // (blocks that are read more than once could be written by someone in between: then any number may stay)
     const int list = a.keep < a.block && room <= MOST ? a.keep : a.block;
     const size_t smem = (size_t)a.block * 4 / SHARES + (list * 2 + 15) / 16 * 16;
-    if (smem > 32 * 1024) {  // (48 KB with what the kernel declares itself need no asking)
+    {   // with what the kernel declares itself (18016 bytes, SPLIT) a launch may pass 48 KB from 31 KB on: asked for
+        // once per device, whatever the first call's size
         static std::mutex mu;
-        static std::set<int> opted;
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess)
-            return QMD_ERR_DEVICE;
+        static bool opted[64] = {false};
         std::lock_guard<std::mutex> lock(mu);
-        if (!opted.count(dev)) {
+        if (!opted[dev.device]) {
             const cudaError_t e = cudaFuncSetAttribute(kv4_evict_kernel<D, THREADS, ROWS, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                        MOST * 4 / SHARES + MOST * 2);
             if (e != cudaSuccess)
                 return fail(QMD_ERR_LAUNCH, "kv4_evict smem attribute", e);
-            opted.insert(dev);
+            opted[dev.device] = true;
         }
     }
     cudaLaunchConfig_t cfg = {};
@@ -442,9 +439,9 @@ qmd_status launch_kv4_evict(const Kv4Params &kv, int head_dim, float *weight, in
     // short tables: small CTAs, many to an SM
     const bool small = kv.table_stride * tokens <= 4096;
     switch (head_dim) {
-    case 64: return small ? launch_evict4<64, 256, 4, false>(a, s) : launch_evict4<64, 512, 8, true>(a, s);
-    case 128: return small ? launch_evict4<128, 256, 4, false>(a, s) : launch_evict4<128, 512, 8, true>(a, s);
-    default: return small ? launch_evict4<256, 256, 4, false>(a, s) : launch_evict4<256, 512, 8, true>(a, s);
+    case 64: return small ? launch_evict4<64, 256, 4, false>(a, dev, s) : launch_evict4<64, 512, 8, true>(a, dev, s);
+    case 128: return small ? launch_evict4<128, 256, 4, false>(a, dev, s) : launch_evict4<128, 512, 8, true>(a, dev, s);
+    default: return small ? launch_evict4<256, 256, 4, false>(a, dev, s) : launch_evict4<256, 512, 8, true>(a, dev, s);
     }
 }
 
