@@ -550,8 +550,9 @@ qmd_status qmd_kv4_weigh(const qmd_kv4_cache *cache, const qmd_kv_batch *batch, 
  *             to one sequence, at one place of its table (no shared pages).
  *   weight    f32 [pages][kv_heads][page_tokens], 16-byte aligned (read, moved)
  *   len_out   int32 [seqs], 4-byte aligned: min(kv_len, keep), the next call's kv_len (before its rows are
- *             counted in).  Must not overlap kv_len.
+ *             counted in).
  *   kept      int32 [seqs][kv_heads][keep], 4-byte aligned, or NULL: the slots that the tokens came from, then -1
+ *   weight, len_out and kept must not overlap each other, the page table or kv_len.
  *   keep 1 .. 2^24, sinks and recent >= 0, together at most keep
  * A length out of range gives len_out 0, a page out of range leaves the whole sequence as it was (len_out its
  * length); kept is -1 for both, and both are index errors.

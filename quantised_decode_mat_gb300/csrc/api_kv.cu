@@ -360,8 +360,14 @@ qmd_status qmd_kv4_evict(const qmd_kv4_cache *cache, const qmd_kv_batch *batch, 
         return QMD_ERR_MISALIGNED;
     if (keep < 1 || keep > (1 << 24) || sinks < 0 || recent < 0 || sinks > keep || recent > keep - sinks)
         return QMD_ERR_VALUE;
-    const size_t lb = (size_t)b.seqs * 4, kb = lb * cache->kv_heads * keep;
-    if (overlaps(len_out, lb, b.kv_len, lb) || overlaps(kept, kb, b.kv_len, lb) || overlaps(kept, kb, len_out, lb))
+    // what is written must not be what the selection and the moves read: the table's pages are checked once, and
+    // looked up again for every token that moves
+    const size_t lb = (size_t)b.seqs * 4, kb = lb * cache->kv_heads * keep, tb = lb * b.table_stride;
+    const size_t wb = (size_t)cache->pages * cache->kv_heads * cache->page_tokens * 4;
+    if (overlaps(len_out, lb, b.kv_len, lb) || overlaps(kept, kb, b.kv_len, lb) || overlaps(kept, kb, len_out, lb) ||
+        overlaps(len_out, lb, b.page_table, tb) || overlaps(kept, kb, b.page_table, tb) ||
+        overlaps(len_out, lb, weight, wb) || overlaps(kept, kb, weight, wb) || overlaps(weight, wb, b.page_table, tb) ||
+        overlaps(weight, wb, b.kv_len, lb))
         return QMD_ERR_VALUE;
     DeviceInfo dev;
     if ((st = find_device(&dev, &kv)) != QMD_OK)
