@@ -25,9 +25,9 @@ from dataclasses import dataclass, field
 
 import numpy as np
 
-from . import (Q4_K, Q6_K_SPLIT, QMD_QK, ROPE_HALVES, KV4Cache, KVBatch, KVCache, Q8K, QmdError, bind_q6k, kv4_append,
-               kv4_attention, kv4_evict, kv4_weigh, kv_append, kv_attention, kv_workspace, lora_add, q6k_prefix_stride,
-               q8k_pack, qmatvec, qmatvec_x, rope_table)
+from . import (Q4_K, Q6_K_SPLIT, QMD_QK, ROPE_HALVES, KV4Cache, KVBatch, KVCache, Q8K, QmdError, _array, bind_q6k,
+               kv4_append, kv4_attention, kv4_evict, kv4_weigh, kv_append, kv_attention, kv_workspace, lora_add,
+               q6k_prefix_stride, q8k_pack, qmatvec, qmatvec_x, rope_table)
 from . import synth
 
 @dataclass
@@ -371,6 +371,12 @@ class AttentionBlock:
         if self.weights is not None:
             if not self.four_bits:
                 raise QmdError(2, "weights: of a KV4Cache's tokens only")
+            at = _array(self.weights, torch.float32, (self.cache.pages, self.cache.kv_heads, self.cache.page_tokens),
+                        self.cache.index, "weights")
+            if self.weights.device != dev:
+                raise QmdError(9, f"weights is on {self.weights.device}, not on the cache's device")
+            if at % 16:
+                raise QmdError(5, "weights: 16-byte aligned memory is wanted")
             self.lse = torch.empty((self.rows, self.heads), **f32)
         k = self.q_width + self.kv_width
         self.q, self.k, self.v = self.qkv[:, :self.q_width], self.qkv[:, self.q_width:k], self.qkv[:, k:]
@@ -399,8 +405,12 @@ class AttentionBlock:
             raise QmdError(6, f"adapter: shape ({self.rows},) is wanted, got {tuple(adapter.shape)}")
         if positions is not None and not self.four_bits:
             raise QmdError(10, "positions: of a KV4Cache's rows only")
-        if positions is not None and (positions.shape != (batch.rows,) or positions.dtype is not torch.int32):
-            raise QmdError(6, f"positions: int32 ({batch.rows},) is wanted, got {positions.dtype} {tuple(positions.shape)}")
+        if positions is not None:
+            if positions.shape != (batch.rows,) or positions.dtype is not torch.int32 or not positions.is_contiguous():
+                raise QmdError(6, f"positions: contiguous int32 ({batch.rows},) is wanted, got {positions.dtype} "
+                                  f"{tuple(positions.shape)}, strides {tuple(positions.stride())}")
+            if positions.device != self.cache.device:
+                raise QmdError(9, f"positions is on {positions.device}, not on the cache's device")
         qmatvec_x(Q4_K, self.W_qkv, None, x, self.qkv, stream=stream)
         if self.qkv_adapters is not None:
             a = self.qkv_adapters
