@@ -23,6 +23,7 @@ Q4_K = 12
 Q5_K = 13
 Q6_K_SPLIT = 14
 QMD_KV_BLOCK = 16
+QMD_KV_MAX_SEQS = 2048
 QMD_KV4_GROUP = 32
 ROPE_HALVES, ROPE_ADJACENT = 0, 1
 F16, BF16 = 1, 2

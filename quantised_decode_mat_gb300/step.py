@@ -25,9 +25,9 @@ from dataclasses import dataclass, field
 
 import numpy as np
 
-from . import (Q4_K, Q6_K_SPLIT, QMD_QK, ROPE_HALVES, KV4Cache, KVBatch, KVCache, Q8K, QmdError, _array, bind_q6k,
-               kv4_append, kv4_attention, kv4_evict, kv4_weigh, kv_append, kv_attention, kv_workspace, lora_add,
-               q6k_prefix_stride, q8k_pack, qmatvec, qmatvec_x, rope_table)
+from . import (Q4_K, Q6_K_SPLIT, QMD_KV_BLOCK, QMD_KV_MAX_SEQS, QMD_QK, ROPE_HALVES, KV4Cache, KVBatch, KVCache, Q8K, QmdError,
+               _array, _stream_on, bind_q6k, kv4_append, kv4_attention, kv4_evict, kv4_weigh, kv_append, kv_attention,
+               kv_workspace, lora_add, q6k_prefix_stride, q8k_pack, qmatvec, qmatvec_x, rope_table)
 from . import synth
 
 @dataclass
@@ -321,6 +321,15 @@ class Adapters:
     scale: "object"
 
 
+def _fits(t, dtype, shape, device, what: str, align: int = 4) -> None:
+    """Refuses a tensor that a call would refuse: not contiguous, of this type, shape, device and alignment."""
+    at = _array(t, dtype, shape, t.get_device(), what)
+    if t.device != device:
+        raise QmdError(9, f"{what} is on {t.device}, not on the cache's device")
+    if at % align:
+        raise QmdError(5, f"{what}: {align}-byte aligned memory is wanted")
+
+
 @dataclass
 class AttentionBlock:
     """The attention half of a decoder layer for up to 8 rows: x [rows, hidden] (normalised) to
@@ -362,6 +371,31 @@ class AttentionBlock:
                 raise QmdError(6, f"{what}: {rows} rows of {K // QMD_QK} Q4_K blocks are wanted, got {tuple(W.shape)}")
             if W.device != dev:
                 raise QmdError(9, f"{what} is on {W.device}, not on the cache's device")
+        # and what the later calls would refuse when the earlier ones have run
+        kv, tokens = self.cache.kv_heads, self.cache.k.shape[2]
+        if D not in (64, 128, 256) or tokens % QMD_KV_BLOCK or not QMD_KV_BLOCK <= tokens <= 65536:
+            raise QmdError(6, f"the cache: heads of 64, 128 or 256 and pages of whole blocks of {QMD_KV_BLOCK} tokens are wanted")
+        if self.heads % kv or self.heads // kv > 64:
+            raise QmdError(6, f"heads: a multiple of {kv}, at most 64 to a key/value head, is wanted, got {self.heads}")
+        if self.rope is not None:
+            n, rot = self.rope.shape if self.rope.dim() == 2 else (0, 0)
+            if n < 1 or rot % 32 or not 32 <= rot <= D:
+                raise QmdError(6, f"rope: [positions, rot] with rot 32 .. {D} is wanted, got {tuple(self.rope.shape)}")
+            _fits(self.rope, torch.float32, (n, rot), dev, "rope", 16)
+        if self.pairs not in (0, 1) or self.window >> 63:
+            raise QmdError(10, f"pairs {self.pairs}, window {self.window}")
+        for a, rows, K, what in ((self.qkv_adapters, self.q_width + 2 * self.kv_width, self.hidden, "qkv_adapters"),
+                                 (self.o_adapters, self.hidden, self.q_width, "o_adapters")):
+            if a is None:
+                continue
+            if a.A.dtype not in (torch.float16, torch.bfloat16):
+                raise QmdError(2, f"{what}: A float16 or bfloat16 is wanted, got {a.A.dtype}")
+            n, rank = a.A.shape[:2] if a.A.dim() == 3 else (0, 0)
+            if n < 1 or rank % 8 or not 8 <= rank <= 128:
+                raise QmdError(6, f"{what}: A [adapters, rank, {K}] with rank 8 .. 128 is wanted, got {tuple(a.A.shape)}")
+            _fits(a.A, a.A.dtype, (n, rank, K), dev, what + ".A", 16)
+            _fits(a.B, a.A.dtype, (n, rows, rank), dev, what + ".B", 16)
+            _fits(a.scale, torch.float32, (n,), dev, what + ".scale")
         f32 = dict(dtype=torch.float32, device=dev)
         self.qkv = torch.empty((self.rows, self.q_width + 2 * self.kv_width), **f32)
         self.attended = torch.empty((self.rows, self.q_width), **f32)
@@ -371,12 +405,7 @@ class AttentionBlock:
         if self.weights is not None:
             if not self.four_bits:
                 raise QmdError(2, "weights: of a KV4Cache's tokens only")
-            at = _array(self.weights, torch.float32, (self.cache.pages, self.cache.kv_heads, self.cache.page_tokens),
-                        self.cache.index, "weights")
-            if self.weights.device != dev:
-                raise QmdError(9, f"weights is on {self.weights.device}, not on the cache's device")
-            if at % 16:
-                raise QmdError(5, "weights: 16-byte aligned memory is wanted")
+            _fits(self.weights, torch.float32, (self.cache.pages, self.cache.kv_heads, self.cache.page_tokens), dev, "weights", 16)
             self.lse = torch.empty((self.rows, self.heads), **f32)
         k = self.q_width + self.kv_width
         self.q, self.k, self.v = self.qkv[:, :self.q_width], self.qkv[:, self.q_width:k], self.qkv[:, k:]
@@ -385,8 +414,8 @@ class AttentionBlock:
         """One call's rows through the block: x f32 [rows, hidden]; batch says which sequences they
         belong to (kv_len counts them in); adapter int32 [rows] picks each row's adapter (below 0:
         none) where the block has adapters; positions int32 [batch.rows] are the rows' positions, where
-        something was evicted from a 4-bit cache (their slots otherwise).  Returns y.  A call whose arguments are refused has
-        launched nothing."""
+        something was evicted from a 4-bit cache (their slots otherwise).  Returns y.  A call whose arguments are
+        refused has launched nothing."""
         import torch
         if x.dtype is not self.qkv.dtype:
             raise QmdError(2, f"x: float32 is wanted, got {x.dtype}")
@@ -401,8 +430,14 @@ class AttentionBlock:
             raise QmdError(9, f"the batch is on {batch.page_table.device}, the cache on {self.cache.device}")
         if adapted and adapter is None:
             raise QmdError(1, "adapter: the block has adapters, each row's choice is wanted")
-        if adapted and adapter.shape != (self.rows,):
-            raise QmdError(6, f"adapter: shape ({self.rows},) is wanted, got {tuple(adapter.shape)}")
+        if adapted:
+            _fits(adapter, torch.int32, (self.rows,), x.device, "adapter")
+        seqs, columns = batch.page_table.shape
+        if (not 1 <= seqs <= QMD_KV_MAX_SEQS or columns < 1 or batch.rows < 1 or not 1 <= batch.max_q <= 1 << 20
+                or batch.q_start is None and seqs * batch.max_q > batch.rows):
+            raise QmdError(6, f"batch: {seqs} sequences, {columns} columns, {batch.rows} rows, {batch.max_q} of a sequence at most")
+        if self.cache.index >= 0:
+            _stream_on(stream, self.cache.index, "the cache")
         if positions is not None and not self.four_bits:
             raise QmdError(10, "positions: of a KV4Cache's rows only")
         if positions is not None:
