@@ -483,14 +483,16 @@ def make_attention_block(rows: int, seqs: int, max_tokens: int, heads: int = 32,
     max_tokens of each sequence.  kv_bits 8 or 4; weigh: a 4-bit cache's block adds up its tokens' attention,
     for evict(); positions: of the rope table (max_tokens by default)."""
     import torch
+    if kv_bits not in (4, 8):
+        raise QmdError(10, f"kv_bits: 4 or 8, got {kv_bits}")
+    if weigh and kv_bits != 4:
+        raise QmdError(10, "weigh: of a 4-bit cache's tokens only (kv_bits=4)")
     dev = torch.device(device)
     seed = synth.step_seed(layer)
     qkv_rows, width = (heads + 2 * kv_heads) * head_dim, heads * head_dim
     Ws = [torch.from_numpy(synth.weights("q4k", seed, n, K, layer, t).reshape(n, -1)).to(dev)
           for n, K, t in ((qkv_rows, hidden, 0), (hidden, width, 1))]
     columns = -(-max_tokens // page_tokens)
-    if kv_bits not in (4, 8):
-        raise QmdError(10, f"kv_bits: 4 or 8, got {kv_bits}")
     cache = (KV4Cache if kv_bits == 4 else KVCache).empty(seqs * columns, kv_heads, page_tokens, head_dim, dev)
     table = torch.arange(seqs * columns, dtype=torch.int32, device=dev).view(seqs, columns)
     rope = rope_table(max_tokens if positions is None else positions, head_dim, rope_base, device=dev)

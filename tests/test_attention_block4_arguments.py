@@ -125,3 +125,12 @@ def test_another_device_than_the_current_one(calls, monkeypatch):  # noqa: F811
     with pytest.raises(q.QmdError, match="DEVICE"):
         b.run(torch.zeros((ROWS, HIDDEN)), rows)
     assert calls == []
+
+
+@pytest.mark.parametrize("kw", [dict(weigh=True), dict(weigh=True, kv_bits=8), dict(kv_bits=3), dict(kv_bits=16, weigh=True)])
+def test_a_block_of_a_kind_that_is_not_there(calls, monkeypatch, kw):  # noqa: F811
+    """... is refused before its weights are made."""
+    monkeypatch.setattr(S.synth, "weights", lambda *a: pytest.fail("weights were made"))
+    with pytest.raises(q.QmdError, match="VALUE"):
+        S.make_attention_block(1, 1, 16, 4, 2, 64, 256, device="cpu", **kw)
+    assert calls == []
