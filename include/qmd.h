@@ -532,9 +532,11 @@ qmd_status qmd_kv4_attention(const qmd_kv4_cache *cache, const qmd_kv_batch *bat
  * same device give the same bits.
  *   lse     f32 [rows][q_heads], 4-byte aligned
  *   weight  f32 [pages][kv_heads][page_tokens], 16-byte aligned (read and written)
- * Values are not read (cache->v and v_scale may be NULL).  A weight is off by at most 2^-20 of itself while
- * |scale| * sum_d |q| |K| and |lse| are up to 32, and grows with them; what is under 2^-126 counts as 0.  Rows that see no position (their lse is
- * -infinity) add nothing.  A slot must belong to one sequence, at one place of its table (no shared pages).
+ * Values are not read (cache->v and v_scale may be NULL).  With M the largest |scale| * sum_d (|q| + 2^-15 max |q|) |K|
+ * of its slot and T rows times heads, a weight is off by at most 2^-24 ((head_dim / 2 + 52) M + 8 |lse| + 8 + T) of
+ * itself (every rounding the same way, sums that cut off at 2^-23 a step), and by 2^-18 root mean square while M and
+ * |lse| are up to 32; a term under 2^-126 counts as 0.  Rows that see no position (their lse is -infinity) add
+ * nothing.  A slot must belong to one sequence, at one place of its table (no shared pages).
  * Other arguments, limits and errors as qmd_kv4_attention (there is no workspace).
  */
 qmd_status qmd_kv4_weigh(const qmd_kv4_cache *cache, const qmd_kv_batch *batch, const float *q, int64_t q_stride,

@@ -18,6 +18,9 @@
 // two f16 parts each 8.4 on mma.sync).
 //
 // Either way a slot's weight is only ever touched by one warp at a time, in one order: no atomics, the same bits every time.
+// The exponent's two terms are rounded at their own size in log2 units (half a step of f32 is 2^-19 from 32 on) before they are
+// subtracted: with sums |scale| |q| |K| of 26 and log-sum-exps up to 32 a weight is off by up to 3.4 * 2^-20 of itself, 1.2 to 2.0 *
+// 2^-20 root mean square (64 to 256 dimensions).
 #include <climits>
 #include <mutex>
 
