@@ -511,7 +511,8 @@ qmd_status qmd_kv4_read(const qmd_kv4_cache *cache, const qmd_kv_batch *batch, f
  * Window and causal order count slots.
  *   lse  f32 [rows][q_heads], 4-byte aligned, or NULL; must not overlap out or q
  * Accuracy as qmd_kv_attention's, with one more limit: what a group of 32 values adds to an output is kept down
- * to 2^-36 of the largest weight times scale among all the groups that the row has met.
+ * to 2^-36 of the largest weight times scale among all the groups that the row has met, or to 2^-67 of its largest weight
+ * where that is more (tokens without value that have nearly all the weight).
  * NaN or infinite queries affect their own row and head only, a scale that is not finite only rows that see
  * its slot.  Other arguments (workspace among them, of qmd_kv_workspace_bytes()), limits and errors as
  * qmd_kv_attention.

@@ -15,7 +15,9 @@
 // Reference.  Weights are taken over 2^ref, an integer for each query row, such that weight times |scale| stays
 // under 2^16 (what f16 holds) and weights under 2^46; it moves up only when one of these is passed, to leave
 // the largest product in (2^12, 2^14] (then every sum is rescaled, exactly).  What two f16 parts lose is then
-// at most 2^-22 of a product, or 2^-37 of the largest that the row has met.  (A scale without weight does not count.)
+// at most 2^-22 of a product, or, where the parts are subnormal and each is rounded to a multiple of 2^-24, 2^-36 of the
+// largest that the row has met.  (A scale without weight does not count.)  Where slots of scale zero have the weight, the
+// reference leaves theirs at 2^43 at least, and 2^-67 of it is lost at most.
 //
 // Loads: per unit a warp asks for the keys' and the values' codes by tiled tensor copies (swizzled, so that
 // ldmatrix meets no bank conflicts) and for their scales by plain bulk copies, into a ring of STAGES units.
