@@ -8,6 +8,9 @@
 // bytes or of the values'), which lies in nobody else's way, and (SPLIT) selects among its quarter of the slots; where
 // tables are short each selects among all for itself, which takes less than the cluster's meetings (12 x 8 heads of
 // 1088 slots: 16.2 us against 28.4 with quarters; 8 heads of 24000: 24.9 against 18.8).
+// The host decides, by the page table's width: it does not know the lengths.  So short sequences behind a wide table take the
+// quarters, and shared memory for its width (those 12 x 8 heads: 15.1 us up to 4096 slots of table, 36.3 from there on, 37.8
+// behind 131072, where the list has room for a whole block).
 //
 // Selection.  Weights become whole numbers in their order, kept in shared memory, four neighbouring slots to a thread and
 // row of them (of more slots than a block of it holds, the blocks are read again for each pass).  The number that
@@ -21,7 +24,7 @@
 // CTA, after the barrier behind which all have read theirs.
 //
 // Bound: latency (some twenty dependent steps), and for few sequences what their few SMs move.  8 heads of 24000 slots to
-// 2048: 18.8 us; 12 x 8 heads of 1088 to 1024: 14.8 us, half of it the moves (28 MB).
+// 2048: 18.8 us; 12 x 8 heads of 1088 to 1024: 14.9 us, half of it the moves (28 MB).
 #include <mutex>
 #include <type_traits>
 
