@@ -17,8 +17,8 @@ pytestmark = [
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 # (slots of the table, keep): 31136 bytes, 31152 (48 KB are passed), 32768, and 32784
-SIZES = {64: [(30720, 208), (30720, 209), (16384, 8192), (16384, 8193)],
-         128: [(24576, 4096), (30720, 208)],
+SIZES = {64: [(30208, 464), (30208, 465), (16384, 8192), (16384, 8193)],
+         128: [(24576, 4096), (30208, 464)],
          256: [(28672, 2048), (24576, 3281)]}
 
 
